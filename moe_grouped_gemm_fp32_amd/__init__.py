@@ -13,6 +13,10 @@ GEMM"):
   fp8_gemm_nt                       D = A . B^T
   fp8_grouped_gemm_nt_contiguous    experts concatenated along M, m_indices per row
   fp8_grouped_gemm_nt_masked        [G, M_max, K] input, masked_m[g] live rows
+
+The operators around the GEMMs of a transformer layer (include/fp8layer.h) are in layer.py:
+  rmsnorm_quantize_1x128, rmsnorm_backward          norm into a GEMM's 8-bit A operand
+  rope_append_paged_kv, paged_attention             a paged 8-bit cache and its attention
 """
 from __future__ import annotations
 
@@ -628,3 +632,10 @@ def scale_ld(rows: int) -> int:
 
 def num_tiles(M: int, N: int, block_m: int, block_n: int) -> int:
     return int(lib().fp8_gemm_num_tiles(M, N, block_m, block_n))
+
+
+from . import layer as _layer  # noqa: E402  (the layer operators build on the helpers above)
+from .layer import (PagedKVCache, attention_workspace_size, make_attention_workspace, make_paged_kv_cache,  # noqa: E402
+                    paged_attention, rmsnorm_backward, rmsnorm_quantize_1x128, rope_append_paged_kv)
+
+__all__ += _layer.__all__

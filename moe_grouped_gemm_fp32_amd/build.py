@@ -5,6 +5,7 @@ picks one per call. Packed-FP32 VALU instructions are disabled for all device co
 """
 from __future__ import annotations
 
+import glob
 import os
 import shutil
 import subprocess
@@ -12,8 +13,7 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "fp8gemm.hip")
-HEADERS = [os.path.join(PKG, "csrc", "fp8gemm_kernel.hpp"), os.path.join(ROOT, "include", "fp8gemm.h")]
+SRCS = [os.path.join(PKG, "csrc", "fp8gemm.hip"), os.path.join(PKG, "csrc_layer", "fp8layer.hip")]
 LIB = os.path.join(PKG, "libfp8gemm.so")
 ARCH = "gfx950"
 
@@ -25,30 +25,49 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: the HIP library cannot be built")
 
 
-def command(out: str, extra=()) -> list:
-    return [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-shared", "-fPIC",
-            "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-            # MFMA results in VGPRs: the FP32 promotion FMAs read them directly
-            "-mllvm", "-amdgpu-mfma-vgpr-form",
-            "-I", os.path.join(ROOT, "include"), *extra, SRC, "-o", out]
+FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+         # MFMA results in VGPRs: the FP32 promotion FMAs read them directly
+         "-mllvm", "-amdgpu-mfma-vgpr-form",
+         "-I", os.path.join(ROOT, "include")]
 
 
-def _compile(cmd, out: str, verbose: bool) -> str:
+def sources() -> list:
+    """Every file that the library is built from."""
+    return [f for d in ("csrc", "csrc_layer") for f in sorted(glob.glob(os.path.join(PKG, d, "*")))] + \
+        sorted(glob.glob(os.path.join(ROOT, "include", "*.h"))) + [os.path.abspath(__file__)]
+
+
+def _compile(out: str, extra: list, verbose: bool) -> str:
+    """One object per source, compiled side by side, linked into `out`."""
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [tmp if c == out else c for c in cmd]
-    if verbose:
-        print("[build]", " ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed building " + os.path.basename(out))
-    os.replace(tmp, out)
+    objs = ["%s.%d.o" % (tmp, i) for i in range(len(SRCS))]
+    steps = [[hipcc(), *FLAGS, *extra, "-c", src, "-o", obj] for src, obj in zip(SRCS, objs)]
+    link = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *extra, *objs, "-o", tmp]
+    try:
+        if verbose:
+            print("\n".join("[build] " + " ".join(c) for c in [*steps, link]), flush=True)
+        running = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in steps]
+        said = [p.communicate()[0] for p in running]
+        done = [p.returncode for p in running]
+        if not any(done):
+            res = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+            said.append(res.stdout)
+            done.append(res.returncode)
+        if any(done):
+            sys.stderr.write("".join(said))
+            raise RuntimeError("hipcc failed building " + os.path.basename(out))
+        os.replace(tmp, out)
+    finally:
+        for f in (*objs, tmp):
+            if os.path.exists(f):
+                os.remove(f)
     return out
 
 
 def build(verbose: bool = True) -> str:
     """Compile libfp8gemm.so next to this file (always rebuilds). Returns its path."""
-    return _compile(command(LIB), LIB, verbose)
+    return _compile(LIB, [], verbose)
 
 
 # Host-sanitizer build: the same library with its host code (argument checks, planner,
@@ -77,12 +96,10 @@ def sanitizer_runtime() -> str:
 def build_host_sanitized(verbose: bool = True, force: bool = False) -> str:
     """Compile libfp8gemm_hostsan.so next to this file unless it is newer than every
     source. Returns its path."""
-    srcs = [SRC, *HEADERS, os.path.join(PKG, "csrc", "fp8kgroup_kernel.hpp"),
-            os.path.join(PKG, "csrc", "fp8quant_kernel.hpp"), os.path.abspath(__file__)]
     if not force and os.path.exists(LIB_HOSTSAN) and \
-            os.path.getmtime(LIB_HOSTSAN) > max(os.path.getmtime(s) for s in srcs):
+            os.path.getmtime(LIB_HOSTSAN) > max(os.path.getmtime(s) for s in sources()):
         return LIB_HOSTSAN
-    return _compile(command(LIB_HOSTSAN, extra=HOSTSAN_FLAGS), LIB_HOSTSAN, verbose)
+    return _compile(LIB_HOSTSAN, HOSTSAN_FLAGS, verbose)
 
 
 if __name__ == "__main__":

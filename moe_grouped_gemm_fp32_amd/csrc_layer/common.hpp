@@ -1,0 +1,106 @@
+// Small device helpers shared by the layer operators' kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp8layer {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+constexpr float kE4m3Max = 448.0f;
+
+// Eight consecutive elements (BF16 bits or FP32), 16-byte aligned, as FP32.
+template <typename T>
+__device__ __forceinline__ void load8(const T* src, float (&x)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(src);
+    const float4 b = *reinterpret_cast<const float4*>(src + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+}
+
+// Two FP32 values rounded to nearest even BF16, packed.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2bf));
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* dst, const float (&x)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(dst) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  } else {
+    reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+// x rounded to T and back: what a T in memory will hold.
+template <typename T>
+__device__ __forceinline__ float rounded(float x) {
+  if constexpr (sizeof(T) == 2)
+    return (float)(__bf16)x;
+  else
+    return x;
+}
+
+// Eight FP32 values to e4m3 codes, round to nearest even.
+__device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8]) {
+  int a = 0, b = 0;
+  a = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], a, false);
+  a = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], a, true);
+  b = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], b, false);
+  b = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], b, true);
+  return make_uint2((uint32_t)a, (uint32_t)b);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+// Inclusive prefix sum over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o, 64);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// The part of a sequence that a call concerns, from its device arrays, clamped to what
+// the call's host arguments allow (nothing read from these arrays becomes an address
+// unchecked).
+struct Sequence {
+  int row0;  // its first row among the call's tokens
+  int rows;  // its number of rows
+  int len;   // its length in the cache
+};
+__device__ __forceinline__ Sequence sequence(const int32_t* cu_q, const int32_t* seq_lens, int b, int T, int max_len) {
+  const int q0 = min(max(cu_q[b], 0), T);
+  const int q1 = min(max(cu_q[b + 1], q0), T);
+  return {q0, q1 - q0, min(max(seq_lens[b], 0), max_len)};
+}
+
+}  // namespace fp8layer

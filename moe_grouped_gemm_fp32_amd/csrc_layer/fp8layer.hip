@@ -1,0 +1,343 @@
+// Host side of the layer operators of libfp8gemm (include/fp8layer.h): argument checks,
+// the choice among compiled instances, and the launches.
+#include "fp8layer.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "attention_kernel.hpp"
+#include "kvcache_kernel.hpp"
+#include "rmsnorm_kernel.hpp"
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// FP8GEMM_OK and the current device's compute units if it is a gfx950. The units are capped
+// by fp8_gemm_set_num_cus, like those of the GEMMs' grids.
+int device(int* cus) {
+  struct Info {
+    int status = 1, cus = 0;
+  };
+  static Info infos[kMaxDevices];
+  static std::mutex mutex;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return FP8GEMM_ERR_DEVICE;
+  std::lock_guard<std::mutex> lock(mutex);
+  Info& d = infos[dev];
+  if (d.status == 1) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return FP8GEMM_ERR_DEVICE;
+    d.cus = prop.multiProcessorCount;
+    d.status = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? FP8GEMM_OK : FP8GEMM_ERR_DEVICE;
+  }
+  const int cap = fp8_gemm_get_num_cus();
+  *cus = cap > 0 ? std::min(cap, d.cus) : d.cus;
+  return d.status;
+}
+
+int launched() { return hipGetLastError() == hipSuccess ? FP8GEMM_OK : FP8GEMM_ERR_LAUNCH; }
+
+// ---------------------------------------------------------------------------- RMS norm
+
+constexpr int kMaxNormCols = 65536;
+
+// Waves that share a row and chunks of eight columns a thread: as few waves as keep a row
+// within four chunks a thread, which leaves room for several workgroups on a CU.
+struct NormShape {
+  int waves, chunks;
+};
+NormShape norm_shape(int K) {
+  const int chunks = K / 8;
+  for (int ch : {1, 2, 4})
+    if (chunks <= 64 * ch) return {1, ch};
+  if (chunks <= 4 * 64 * 4) return {4, 4};
+  return {16, chunks <= 16 * 64 * 4 ? 4 : 8};
+}
+
+bool norm_dtype(int t) { return t == FP8GEMM_QUANT_BF16 || t == FP8GEMM_QUANT_FP32; }
+// row stride of a [.., K] array of x_dtype elements whose rows are read 16 bytes at a time
+bool norm_rows(const void* p, int64_t ld, int K, int dtype) {
+  return aligned(p, 16) && ld >= K && ld % (dtype == FP8GEMM_QUANT_BF16 ? 8 : 4) == 0;
+}
+
+// Calls f(T{}, W{}, waves, chunks) with the types and the shape as compile-time values.
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <typename F>
+void with_types(int x_dtype, int w_dtype, F f) {
+  const bool xb = x_dtype == FP8GEMM_QUANT_BF16, wb = w_dtype == FP8GEMM_QUANT_BF16;
+  if (xb && wb) f(uint16_t{}, uint16_t{});
+  else if (xb) f(uint16_t{}, float{});
+  else if (wb) f(float{}, uint16_t{});
+  else f(float{}, float{});
+}
+template <typename F>
+void with_shape(NormShape s, F f) {
+  if (s.waves == 1) {
+    if (s.chunks == 1) f(Int<1>{}, Int<1>{});
+    else if (s.chunks == 2) f(Int<1>{}, Int<2>{});
+    else f(Int<1>{}, Int<4>{});
+  } else if (s.waves == 4) {
+    f(Int<4>{}, Int<4>{});
+  } else if (s.chunks == 4) {
+    f(Int<16>{}, Int<4>{});
+  } else {
+    f(Int<16>{}, Int<8>{});
+  }
+}
+
+int norm_grad_groups(int M, NormShape s, int cus) {
+  const int rows = s.waves > 4 ? 1 : 4 / s.waves;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(M, rows), cus * 2));
+}
+
+// ------------------------------------------------------------------- paged cache, attention
+
+bool cache_shape(int num_pages, int P, int Hkv, int D) {
+  return num_pages >= 1 && Hkv >= 1 && (P == 16 || P == 32 || P == 64 || P == 128 || P == 256) &&
+         (D == 64 || D == 128 || D == 256);
+}
+int log2_of(int P) {
+  int n = 0;
+  while ((1 << n) < P) ++n;
+  return n;
+}
+
+constexpr size_t kAttentionCounterBytes = fp8layer::kCounters * sizeof(int32_t);
+constexpr size_t kAttentionPartBytes = (size_t)64 << 20;
+
+}  // namespace
+
+extern "C" {
+
+int fp8_rmsnorm_quantize_1x128(const void* X, int64_t ldx, const void* R, int64_t ldr, int x_dtype, const void* w,
+                               int w_dtype, float eps, void* H, int64_t ldh, void* Y, int64_t ldy, float* rstd,
+                               void* Q, int64_t ldq, float* sa, int64_t ld_sa, int M, int K, hipStream_t stream) {
+  if (!w || (M != 0 && (!X || !Q || !sa || (R && !H)))) return FP8GEMM_ERR_NULL;
+  if (M < 0 || K <= 0 || K % 128 != 0 || K > kMaxNormCols || !(eps >= 0.f)) return FP8GEMM_ERR_SHAPE;
+  if (!norm_dtype(x_dtype) || !norm_dtype(w_dtype)) return FP8GEMM_ERR_LAYOUT;
+  if (M == 0) return FP8GEMM_OK;
+  if (!norm_rows(X, ldx, K, x_dtype) || !aligned(w, 16)) return FP8GEMM_ERR_LAYOUT;
+  if (R && (!norm_rows(R, ldr, K, x_dtype) || !norm_rows(H, ldh, K, x_dtype))) return FP8GEMM_ERR_LAYOUT;
+  if (Y && !norm_rows(Y, ldy, K, FP8GEMM_QUANT_BF16)) return FP8GEMM_ERR_LAYOUT;
+  if (!aligned(Q, 8) || ldq < K || ldq % 8 != 0 || !aligned(sa, 4) || ld_sa < M || ld_sa % 4 != 0 || !aligned(rstd, 4))
+    return FP8GEMM_ERR_LAYOUT;
+  int cus;
+  const int st = device(&cus);
+  if (st != FP8GEMM_OK) return st;
+  const fp8layer::NormParams p{X,   R,   w,   H,   Y,   rstd,  static_cast<uint8_t*>(Q), sa, ldx,
+                               ldr, ldh, ldy, ldq, ld_sa, eps, M, K};
+  const NormShape s = norm_shape(K);
+  with_types(x_dtype, w_dtype, [&](auto t, auto u) {
+    with_shape(s, [&](auto waves, auto chunks) {
+      constexpr int kWaves = decltype(waves)::value;
+      constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves;
+      hipLaunchKernelGGL((fp8layer::rmsnorm_quantize_kernel<decltype(t), decltype(u), kWaves, decltype(chunks)::value>),
+                         dim3((unsigned)ceil_div(M, kRows)), dim3(kWaves > 4 ? kWaves * 64 : 256), 0, stream, p);
+    });
+  });
+  return launched();
+}
+
+size_t fp8_rmsnorm_backward_workspace_size(int M, int K) {
+  if (M <= 0 || K <= 0 || K % 128 != 0 || K > kMaxNormCols) return 0;
+  int cus;  // without a device: the MI355X's own count
+  if (device(&cus) != FP8GEMM_OK) cus = 256;
+  return (size_t)norm_grad_groups(M, norm_shape(K), cus) * K * sizeof(float);
+}
+
+int fp8_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh, const void* dH, int64_t lddh,
+                         int dtype, const float* rstd, const void* w, int w_dtype, void* dX, int64_t lddx, float* dW,
+                         int M, int K, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!w || !dW || (M != 0 && (!dY || !H || !rstd || !dX))) return FP8GEMM_ERR_NULL;
+  if (M < 0 || K <= 0 || K % 128 != 0 || K > kMaxNormCols) return FP8GEMM_ERR_SHAPE;
+  if (!norm_dtype(dtype) || !norm_dtype(w_dtype)) return FP8GEMM_ERR_LAYOUT;
+  if (M != 0 && (!norm_rows(dY, lddy, K, dtype) || !norm_rows(H, ldh, K, dtype) || !norm_rows(dX, lddx, K, dtype) ||
+                 (dH && !norm_rows(dH, lddh, K, dtype)) || !aligned(rstd, 4)))
+    return FP8GEMM_ERR_LAYOUT;
+  if (!aligned(w, 16) || !aligned(dW, 4) || !aligned(workspace, 16)) return FP8GEMM_ERR_LAYOUT;
+  int cus;
+  const int st = device(&cus);
+  if (st != FP8GEMM_OK) return st;
+  const NormShape s = norm_shape(K);
+  const int groups = M > 0 ? norm_grad_groups(M, s, cus) : 0;
+  if (groups > 0 && (!workspace || workspace_bytes < (size_t)groups * K * sizeof(float))) return FP8GEMM_ERR_WORKSPACE;
+  float* part = static_cast<float*>(workspace);
+  if (M > 0) {
+    const fp8layer::NormGradParams p{dY, H, dH, w, rstd, dX, part, lddy, ldh, lddh, lddx, M, K};
+    with_types(dtype, w_dtype, [&](auto t, auto u) {
+      with_shape(s, [&](auto waves, auto chunks) {
+        constexpr int kWaves = decltype(waves)::value;
+        hipLaunchKernelGGL(
+            (fp8layer::rmsnorm_backward_kernel<decltype(t), decltype(u), kWaves, decltype(chunks)::value>), dim3(groups),
+            dim3(kWaves > 4 ? kWaves * 64 : 256), 0, stream, p);
+      });
+    });
+    const int rc = launched();
+    if (rc != FP8GEMM_OK) return rc;
+  }
+  hipLaunchKernelGGL(fp8layer::rmsnorm_weight_grad_kernel, dim3((unsigned)ceil_div(K, 64)), dim3(256), 0, stream, part,
+                     groups, K, dW);
+  return launched();
+}
+
+int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                             const float* cos_sin, int64_t ld_cs, int max_pos, int rot_dim, int interleaved,
+                             const int32_t* positions, const int32_t* block_table, int64_t ld_bt, int max_pages,
+                             const int32_t* seq_lens, const int32_t* cu_q, void* q_out, int64_t ldqo, void* k_cache,
+                             float* k_scale, void* v_cache, float* v_scale, int num_pages, int P, int B, int T, int Hq,
+                             int Hkv, int D, hipStream_t stream) {
+  if (!k_cache || !k_scale || !v_cache || !v_scale ||
+      (T != 0 && B != 0 && (!k || !v || !block_table || !seq_lens || !cu_q || (q == nullptr) != (q_out == nullptr) ||
+                            (rot_dim > 0 && !cos_sin))))
+    return FP8GEMM_ERR_NULL;
+  if (!cache_shape(num_pages, P, Hkv, D) || B < 0 || T < 0 || Hq < 1 || max_pages < 0 || rot_dim < 0 || rot_dim > D ||
+      rot_dim % 16 != 0 || (rot_dim > 0 && max_pos < 1) || (int64_t)T * std::max(Hq, Hkv) >= INT32_MAX - 256 ||
+      (int64_t)max_pages * P > INT32_MAX)
+    return FP8GEMM_ERR_SHAPE;
+  if (B == 0 || T == 0) return FP8GEMM_OK;
+  if (ldk < (int64_t)Hkv * D || ldk % 8 || ldv < (int64_t)Hkv * D || ldv % 8 || ld_bt < max_pages ||
+      (q && (ldq < (int64_t)Hq * D || ldq % 8 || ldqo < (int64_t)Hq * D || ldqo % 8)) ||
+      (rot_dim > 0 && (ld_cs < rot_dim || ld_cs % 4)))
+    return FP8GEMM_ERR_LAYOUT;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(cos_sin, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+      !aligned(positions, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4))
+    return FP8GEMM_ERR_LAYOUT;
+  int cus;
+  const int st = device(&cus);
+  if (st != FP8GEMM_OK) return st;
+  // Most pages that T new tokens of B sequences can fall in: whole pages, and an end of a
+  // page on either side for each sequence that has any.
+  const int64_t pages = std::min<int64_t>(T, ceil_div(T, P) + 2 * (int64_t)std::min(B, T));
+  const int64_t units = pages * Hkv * 2;
+  // A wave for each unit where units hold a token or two (decoding); four waves otherwise.
+  const bool small = T <= 2 * (int64_t)B;
+  const int64_t unit_groups = small ? ceil_div(units, 4) : units;
+  const int64_t q_groups = q ? ceil_div((int64_t)T * Hq * (D / 16), 256) : 0;
+  if (unit_groups + q_groups > INT32_MAX) return FP8GEMM_ERR_SHAPE;
+  const fp8layer::AppendParams p{static_cast<const uint16_t*>(q),
+                                 static_cast<const uint16_t*>(k),
+                                 static_cast<const uint16_t*>(v),
+                                 cos_sin,
+                                 positions,
+                                 block_table,
+                                 seq_lens,
+                                 cu_q,
+                                 static_cast<uint16_t*>(q_out),
+                                 static_cast<uint8_t*>(k_cache),
+                                 static_cast<uint8_t*>(v_cache),
+                                 k_scale,
+                                 v_scale,
+                                 ldq,
+                                 ldk,
+                                 ldv,
+                                 ld_cs,
+                                 ld_bt,
+                                 ldqo,
+                                 max_pos,
+                                 rot_dim,
+                                 interleaved ? 1 : 0,
+                                 max_pages,
+                                 num_pages,
+                                 log2_of(P),
+                                 B,
+                                 T,
+                                 Hq,
+                                 Hkv,
+                                 (int)unit_groups};
+  const dim3 grid((unsigned)(unit_groups + q_groups));
+  auto go = [&](auto d) {
+    constexpr int kD = decltype(d)::value;
+    if (small)
+      hipLaunchKernelGGL((fp8layer::rope_append_kernel<kD, 1>), grid, dim3(256), 0, stream, p);
+    else
+      hipLaunchKernelGGL((fp8layer::rope_append_kernel<kD, 4>), grid, dim3(256), 0, stream, p);
+  };
+  if (D == 64) go(Int<64>{});
+  else if (D == 128) go(Int<128>{});
+  else go(Int<256>{});
+  return launched();
+}
+
+size_t fp8_paged_attention_workspace_size(void) { return kAttentionCounterBytes + kAttentionPartBytes; }
+
+int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const float* k_scale, const void* v_cache,
+                        const float* v_scale, int num_pages, int P, const int32_t* block_table, int64_t ld_bt,
+                        int max_pages, const int32_t* seq_lens, const int32_t* cu_q, void* O, int64_t ldo, float* lse,
+                        float softmax_scale, int window, int B, int T, int Hq, int Hkv, int D, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream) {
+  if (!k_cache || !k_scale || !v_cache || !v_scale ||
+      (T != 0 && B != 0 && (!q || !block_table || !seq_lens || !cu_q || !O)))
+    return FP8GEMM_ERR_NULL;
+  if (!cache_shape(num_pages, P, Hkv, D) || B < 0 || T < 0 || Hq < 1 || Hq % Hkv != 0 || max_pages < 0 || window < 0 ||
+      !std::isfinite(softmax_scale) || (int64_t)T * Hq >= INT32_MAX - 256 || (int64_t)max_pages * P > INT32_MAX)
+    return FP8GEMM_ERR_SHAPE;
+  if (B == 0 || T == 0) return FP8GEMM_OK;
+  if (ldq < (int64_t)Hq * D || ldq % 8 || ldo < (int64_t)Hq * D || ldo % 8 || ld_bt < max_pages) return FP8GEMM_ERR_LAYOUT;
+  if (!aligned(q, 16) || !aligned(O, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(lse, 4) ||
+      !aligned(workspace, 16))
+    return FP8GEMM_ERR_LAYOUT;
+  int cus;
+  const int st = device(&cus);
+  if (st != FP8GEMM_OK) return st;
+  const int max_len = max_pages * P;
+  fp8layer::AttentionParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q;
+  p.O = static_cast<uint16_t*>(O);
+  p.lse = lse;
+  p.ldq = ldq;
+  p.ldo = ldo;
+  p.ld_bt = ld_bt;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.window = window >= max_len ? 0 : window;  // no key is that far back
+  p.B = B;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.group = Hq / Hkv;
+  p.num_pages = num_pages;
+  p.log_p = log2_of(P);
+  p.max_pages = max_pages;
+  // Most row tiles, times heads; most keys of one tile; units: one for each tile and head,
+  // and those that splitting adds.
+  const int64_t tiles = (std::min(B, T) + (int64_t)T * p.group / fp8layer::kRowTile) * Hkv;
+  const size_t slot = (size_t)fp8layer::kRowTile * (D + 1) * sizeof(float);
+  const size_t bytes = std::min<size_t>(workspace ? workspace_bytes : 0, (size_t)1 << 30);
+  const int64_t slots = bytes > kAttentionCounterBytes ? (int64_t)((bytes - kAttentionCounterBytes) / slot) : 0;
+  const int64_t wanted = std::min<int64_t>((int64_t)cus * 8, slots - tiles);
+  int64_t grid = tiles;
+  if (tiles <= fp8layer::kCounters && wanted > 0 && max_len > fp8layer::kMinChunk) {
+    p.units_wanted = (int)wanted;
+    p.counters = static_cast<int32_t*>(workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttentionCounterBytes);
+    grid = std::min(tiles + wanted, tiles * ceil_div(max_len, fp8layer::kMinChunk));
+  }
+  if (grid > INT32_MAX) return FP8GEMM_ERR_SHAPE;
+  auto go = [&](auto d) {
+    constexpr int kD = decltype(d)::value;
+    hipLaunchKernelGGL((fp8layer::attention_kernel<kD>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+  };
+  if (D == 64) go(Int<64>{});
+  else if (D == 128) go(Int<128>{});
+  else go(Int<256>{});
+  return launched();
+}
+
+}  // extern "C"
