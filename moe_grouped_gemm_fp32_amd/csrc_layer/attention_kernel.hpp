@@ -5,25 +5,34 @@
 //     o' = o 2^(m - m') + sum_j 2^(s_j - m') v_j,   s_j = (q . k_j) softmax_scale log2(e)
 //
 // Rows. The query heads that share a key head, and the tokens of a call, are the rows of
-// one product: row r of a sequence is token r / g, head r % g of the group of g. A tile is
-// 16 of them, the N side of a 16x16x32 matrix instruction whose M side is keys (first
-// product, S^T = K Q^T) or columns of V (second, O^T = V^T P^T). Taken this way round, a
-// lane holds logits of one row only, the running statistics of that row live in the same
-// lane, and the logits' layout is already the second product's operand: no transposition.
+// one product: row r of a sequence is token r / g, head r % g of the group of g. 16 of them
+// are the N side of a 16x16x32 matrix instruction whose M side is keys (first product,
+// S^T = K Q^T) or columns of V (second, O^T = V^T P^T). Taken this way round, a lane holds
+// logits of one row only, the running statistics of that row live in the same lane, and
+// the logits' layout is already the second product's operand: no transposition. A tile is
+// R times 16 rows, which share each key and value that is read and converted.
 // The order in which the 32 summands of a product are fed is free, so it is chosen for the
-// loads: a lane reads 16 consecutive bytes of a key, and D / 16 consecutive bytes of each
+// loads: a lane feeds 16 consecutive bytes of a key, and D / 16 consecutive bytes of each
 // of eight values.
 //
+// Loads. Each wave streams its own keys and values into a ring of two 32-key stages in LDS,
+// by loads that go there without passing registers, and refills the key half and the value
+// half of a stage as soon as it has read them: three quarters of the ring are in flight at
+// any time, without a barrier.
+//
 // Numbers. e4m3 codes convert exactly to BF16 and FP16; queries stay BF16, so the first
-// product's factors are exact. The second product is taken in FP16: probabilities are kept
-// relative to a maximum that may lag by 2^kLag, times 2^(15 - kLag), which fills FP16's
-// range from above and gives them 11 bits. The value scales (powers of two, one per page)
-// enter the probabilities relative to the largest scale so far, which is carried like m.
+// product's factors are exact. The second product is taken in FP16, whose 11 bits a
+// probability needs more than range. The value scales (powers of two, one per page) enter
+// by the exponent, w_j = 2^(s_j + log2 vscale_j - mo + 15 - kLag), relative to a maximum mo
+// of their own, so that whatever contributes most to o lies at the top of FP16's range;
+// l is summed from the same w, each 16-key group by its factor 2^(.. - m). Both maxima may
+// lag behind by 2^kLag before o and l are rescaled, which is rare after the first steps.
 //
 // Work. A unit is a tile, a key head and a chunk of the tile's keys; four waves share it,
-// each with its own run of keys. The chunk length follows from the call's total work, found
-// on the device, so that ragged batches and single long sequences both fill the GPU. The
-// last unit of a tile to arrive joins the parts in their order.
+// each with its own run of keys. The chunk length follows from the call's total work,
+// found on the device (Plan), so that ragged batches and single long sequences both fill
+// the GPU. The parts of a tile are joined in their order by whoever arrives last: first in
+// groups of kJoin neighbours, then the groups' results.
 #pragma once
 
 #include "common.hpp"
@@ -34,11 +43,16 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr int kLag = 8;                 // how far (base 2) logits may exceed m before m moves
+constexpr float kLag = 8.f;             // how far (base 2) logits may exceed m before m moves
 constexpr float kNone = -1e30f;         // m of a row that has seen no key
-constexpr int kCounters = 16384;        // arrival counters at the workspace's start
-constexpr int kRowTile = 16;            // rows of a tile
+constexpr int kTileCounters = 8192;     // arrival counters at the workspace's start: of tiles,
+constexpr int kPartCounters = 8192;     // and of groups of parts
+constexpr int kCounters = kTileCounters + kPartCounters;
 constexpr int kMinChunk = 128;          // least keys of a unit: one step for each wave
+constexpr int kJoin = 8;                // parts joined at a time, all loads in flight together
+// Where a page's values are so small that even the likeliest key adds less than 2^-60 of
+// what o holds, w keeps this much below the likeliest key's 2^0 instead, for l's sake.
+constexpr float kFar = -60.f;
 
 struct AttentionParams {
   const uint16_t* q;
@@ -50,9 +64,11 @@ struct AttentionParams {
   int32_t* counters;
   float* parts;
   int64_t ldq, ldo, ld_bt;
-  float scale_log2;
+  float scale_log2;  // |softmax_scale| log2(e)
+  uint32_t q_sign;   // the scale's sign, as the sign bits of two BF16 values
   int window, B, T, Hq, Hkv, group, num_pages, log_p, max_pages;
-  int units_wanted;  // units that the chunk length aims at; 0: no splitting
+  int residents;   // workgroups that the GPU holds at a time
+  int most_units;  // units that splitting may add; 0: no splitting
 };
 
 // What a sequence asks for: its row tiles, and the most keys that one of them reads.
@@ -67,8 +83,47 @@ __device__ __forceinline__ Demand demand(const Sequence& s, const AttentionParam
   return {tiles, (int)most};
 }
 
-// A unit of work, found by scanning the sequences' unit counts (every wave does it for
-// itself). Everything is wave-uniform.
+// How the call's work is cut. With q keys (over all tiles and heads) for each resident
+// workgroup: up to kOneRound, all units at once, one for each workgroup; beyond, units of
+// about kGoodChunk keys, several rounds of them, which even out ragged batches. (Every unit
+// costs ~5 us before its keys stream: measured on 2 x 131072 keys, a chunk length of 1024,
+// 512 and 256 keys took 62, 91 and 149 us.)
+constexpr float kOneRound = 2048.f;
+constexpr float kGoodChunk = 1024.f;
+template <int TILE, int STEP>
+struct Plan {
+  Sequence seq;   // the lane's sequence and demand, of the 64 looked at last
+  Demand want;
+  int chunk_len;
+
+  __device__ __forceinline__ void look(const AttentionParams& p, int base) {
+    const int b = base + (threadIdx.x & 63);
+    seq = {}, want = {};
+    if (b < p.B) {
+      seq = sequence(p.cu_q, p.seq_lens, b, p.T, p.max_pages << p.log_p);
+      want = demand<TILE, STEP>(seq, p);
+    }
+  }
+  __device__ __forceinline__ void make(const AttentionParams& p) {
+    chunk_len = 1 << 30;
+    if (p.most_units == 0) return;
+    // in FP32: every wave of the call gets the same sums
+    float keys = 0.f, tiles = 0.f;
+    for (int base = 0; base < p.B; base += 64) {
+      look(p, base);
+      keys += wave_sum((float)want.tiles * (float)want.keys);
+      tiles += wave_sum((float)want.tiles);
+    }
+    keys *= (float)p.Hkv, tiles *= (float)p.Hkv;
+    const float all = (float)p.residents;
+    float chunk = keys <= kOneRound * all ? keys / fmaxf(all - 0.5f * tiles, 0.5f * all) : kGoodChunk;
+    // a ten-thousandth more than the sums can be off: no more units than there are slots
+    chunk = fmaxf(chunk, keys / (float)p.most_units * 1.0001f);
+    chunk_len = max(kMinChunk, ((int)fminf(chunk, 1e9f) + 128) / 128 * 128);
+  }
+};
+
+// A unit of work. Everything is wave-uniform.
 struct Unit {
   Sequence seq;
   int b, h, tile, tiles;
@@ -81,47 +136,26 @@ struct Unit {
   int lo, hi;        // keys that some row of the tile sees, lo rounded down to a step
   int k0, k1;        // this unit's keys
 };
+// Unit `number`, found by scanning the sequences' unit counts (every wave does it for
+// itself); false if there is none.
 template <int TILE, int STEP>
-__device__ __forceinline__ bool find_unit(const AttentionParams& p, int number, int min_chunk, Unit& u) {
-  const int lane = threadIdx.x & 63;
-  const int max_len = p.max_pages << p.log_p;
-  int chunk_len = INT32_MAX;
-  if (p.units_wanted > 0) {
-    int64_t work = 0;  // keys over all tiles and heads
-    for (int base = 0; base < p.B; base += 64) {
-      int64_t mine = 0;
-      if (base + lane < p.B) {
-        const Demand d = demand<TILE, STEP>(sequence(p.cu_q, p.seq_lens, base + lane, p.T, max_len), p);
-        mine = (int64_t)d.tiles * d.keys;
-      }
-#pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) mine += __shfl_xor((long long)mine, o, 64);
-      work += mine;
-    }
-    const int64_t each = (work * p.Hkv + p.units_wanted - 1) / p.units_wanted;
-    chunk_len = (int)min((int64_t)(1 << 30), max((int64_t)min_chunk, (each + 127) / 128 * 128));
-  }
+__device__ __forceinline__ bool find_unit(const AttentionParams& p, Plan<TILE, STEP>& plan, int number, Unit& u) {
   u.slot = number;
   u.h = number % p.Hkv;
   const int want = number / p.Hkv;
   int before = 0, tiles_before = 0;
   for (int base = 0; base < p.B; base += 64) {
-    Sequence s{};
-    Demand d{};
-    int count = 0;
-    if (base + lane < p.B) {
-      s = sequence(p.cu_q, p.seq_lens, base + lane, p.T, max_len);
-      d = demand<TILE, STEP>(s, p);
-      count = d.tiles * max(1, (int)(((int64_t)d.keys + chunk_len - 1) / chunk_len));
-    }
-    const int incl = wave_scan(count, lane);
-    const int tiles_incl = wave_scan(d.tiles, lane);
+    if (p.B > 64 || p.most_units == 0) plan.look(p, base);
+    const Demand d = plan.want;
+    const int count = d.tiles * max(1, (int)(((int64_t)d.keys + plan.chunk_len - 1) / plan.chunk_len));
+    const int incl = wave_scan(count);
     const uint64_t hit = __ballot(want < before + incl);
     if (hit) {
       const int src = __ffsll((unsigned long long)hit) - 1;
       auto pick = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
+      const int tiles_incl = wave_scan(d.tiles);
       u.b = base + src;
-      u.seq = {pick(s.row0), pick(s.rows), pick(s.len)};
+      u.seq = {pick(plan.seq.row0), pick(plan.seq.rows), pick(plan.seq.len)};
       u.tiles = pick(d.tiles);
       const int within = want - (before + pick(incl - count));
       u.chunk = within / u.tiles;
@@ -135,24 +169,73 @@ __device__ __forceinline__ bool find_unit(const AttentionParams& p, int number, 
       u.pos1 = first + (u.row0 + u.rows - 1) / p.group;
       u.lo = p.window ? max(0, u.pos0 - p.window + 1) / STEP * STEP : 0;
       u.hi = max(u.lo, min(u.seq.len, u.pos1 + 1));
-      u.chunks = max(1, (int)(((int64_t)(u.hi - u.lo) + chunk_len - 1) / chunk_len));
+      // as many chunks as the length asks for, of equal length
+      const int keys = u.hi - u.lo;
+      const int wanted = max(1, (int)(((int64_t)keys + plan.chunk_len - 1) / plan.chunk_len));
+      const int len = max(128, ((keys + wanted - 1) / wanted + 127) / 128 * 128);
+      u.chunks = max(1, (keys + len - 1) / len);
       if (u.chunk >= u.chunks) return false;  // a tile that sees fewer keys than the sequence's last
-      u.k0 = (int)min((int64_t)u.hi, u.lo + (int64_t)u.chunk * chunk_len);
-      u.k1 = (int)min((int64_t)u.hi, u.k0 + (int64_t)chunk_len);
+      u.k0 = min(u.hi, u.lo + u.chunk * len);
+      u.k1 = min(u.hi, u.k0 + len);
       return true;
     }
-    before += __builtin_amdgcn_readlane(incl, 63);
-    tiles_before += __builtin_amdgcn_readlane(tiles_incl, 63);
+    before += last_lane(incl);
+    tiles_before += last_lane(wave_scan(d.tiles));
   }
   return false;  // the grid covers the most units that there can be
 }
 
-// The raw bytes of 32 keys and values that a lane feeds: keys kg of the 16-key groups'
-// rows `lane & 15`, and eight values (kg = lane >> 4).
+// Waits and loads into LDS. The compiler does not track these loads; each wait stands
+// between scheduling barriers, so that nothing written after it is done before it.
+__device__ __forceinline__ void fence_schedule() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {  // until at most N are outstanding
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  fence_schedule();
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+  fence_schedule();
+}
+__device__ __forceinline__ void wait_lds_reads() {
+  fence_schedule();
+  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));
+  fence_schedule();
+}
+// Every lane's 16 bytes at base + off, to LDS at lds + 16 * lane. base and lds are
+// wave-uniform.
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const uint8_t*)(uintptr_t)((uint64_t)hi << 32 | lo);
+}
+
+// One stage of a wave's ring: 32 keys in the order their lanes feed them ([16-key group]
+// [64-byte piece][lane][16 bytes]), then 32 values, row after row.
 template <int D>
-struct Raw {
-  uint4 k[2][D / 64];
-  uint32_t v[8][D / 64];
+struct Stage {
+  static constexpr int kPieces = D / 64;            // 64-byte pieces of a row
+  static constexpr int kLoads = 2 * kPieces;        // load instructions of a half
+  static constexpr int kHalf = 32 * D, kBytes = 2 * kHalf;
+  // base0, base1: first rows of the two 16-key groups
+  static __device__ __forceinline__ void load_keys(const uint8_t* base0, const uint8_t* base1, uint32_t lds, int lane) {
+    const uint32_t off = (lane & 15) * D + (lane >> 4) * 16;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      load_to_lds(i < kPieces ? base0 : base1, off + (i % kPieces) * 64, lds + i * 1024);
+  }
+  static __device__ __forceinline__ void load_values(const uint8_t* base0, const uint8_t* base1, uint32_t lds, int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      load_to_lds(i < kPieces ? base0 : base1, (i % kPieces) * 1024 + lane * 16, lds + kHalf + i * 1024);
+  }
 };
 
 template <int D>
@@ -165,26 +248,6 @@ __device__ __forceinline__ void load_value(uint32_t (&dst)[D / 64], const uint8_
   } else {
     const uint4 x = *reinterpret_cast<const uint4*>(src);
     dst[0] = x.x, dst[1] = x.y, dst[2] = x.z, dst[3] = x.w;
-  }
-}
-
-// base0, base1: token slots (over pages and heads) of the two 16-key groups.
-template <int D>
-__device__ __forceinline__ void load_raw(Raw<D>& r, const AttentionParams& p, int64_t base0, int64_t base1, int lane) {
-  const int n = lane & 15, kg = lane >> 4;
-  const uint8_t* k0 = p.k_cache + base0 * D + n * D + kg * 16;
-  const uint8_t* k1 = p.k_cache + base1 * D + n * D + kg * 16;
-  const uint8_t* v0 = p.v_cache + base0 * D + kg * 4 * D + n * (D / 16);
-  const uint8_t* v1 = p.v_cache + base1 * D + kg * 4 * D + n * (D / 16);
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    r.k[0][i] = *reinterpret_cast<const uint4*>(k0 + i * 64);
-    r.k[1][i] = *reinterpret_cast<const uint4*>(k1 + i * 64);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    load_value<D>(r.v[j], v0 + j * D);
-    load_value<D>(r.v[4 + j], v1 + j * D);
   }
 }
 
@@ -211,12 +274,11 @@ __device__ __forceinline__ void columns_f16(const uint32_t (&w)[8], bool upper, 
 }
 
 // Exponent field of a power of two.
-__device__ __forceinline__ int exponent(float x) { return (int)((__float_as_uint(x) >> 23) & 0xFF); }
+__device__ __forceinline__ int exponent(uint32_t bits) { return (int)((bits >> 23) & 0xFF); }
 // 2^e; 0 where that is below the normal range, infinity above.
 __device__ __forceinline__ float pow2(int e) {
   return e < -126 ? 0.f : e > 127 ? INFINITY : __uint_as_float((uint32_t)(e + 127) << 23);
 }
-// 2^x for a difference of two maxima: 0 for minus infinity.
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
 __device__ __forceinline__ bool any_nan_code(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
@@ -225,45 +287,221 @@ __device__ __forceinline__ bool any_nan_code(uint32_t w) { return (((w & 0x7F7F7
 constexpr int kDeviceScope = 16;        // buffer cache policy sc1
 constexpr int kRawDword3 = 0x00020000;  // buffer descriptor: 32-bit untyped
 
-template <int D>
-__global__ void __launch_bounds__(256) attention_kernel(const AttentionParams p) {
+// Arrives at a counter; true for the last of `expected`, who leaves it zero. Called by the
+// whole workgroup, after stores that the others' results must be seen through.
+__device__ __forceinline__ bool arrive_last(int32_t* counter, int expected, int* flag) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the stores have reached the device-coherent level
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const bool last = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == expected - 1;
+    if (last) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *flag = last;
+  }
+  __syncthreads();
+  return *flag != 0;
+}
+
+// C columns of one row of a result, normalised, with its log sum exp in base 2.
+template <int C>
+struct RowPart {
+  float out[C];
+  float lse2;
+};
+
+// Joins n parts of a row, `stride` bytes apart from `at` (columns) and `lse_at` (log sum).
+template <int C>
+__device__ __forceinline__ void join_parts(RowPart<C>& r, __amdgpu_buffer_rsrc_t rs, int at, int lse_at, int stride, int n) {
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int t = 0; t < C; ++t) r.out[t] = 0.f;
+  for (int base = 0; base < n; base += kJoin) {
+    float w[kJoin];
+    v4f y[kJoin][C / 4];
+#pragma unroll
+    for (int c = 0; c < kJoin; ++c) {
+      const int off = min(base + c, n - 1) * stride;
+      w[c] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, off + lse_at, 0, kDeviceScope));
+#pragma unroll
+      for (int t = 0; t < C / 4; ++t)
+        y[c][t] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off + at + t * 16, 0, kDeviceScope));
+    }
+    float most = top;
+#pragma unroll
+    for (int c = 0; c < kJoin; ++c) {
+      if (base + c >= n) w[c] = -INFINITY;
+      most = fmaxf(most, w[c]);
+    }
+    const float ref = most > -INFINITY ? most : 0.f;  // rows that have seen nothing stay at weight 0
+    const float a = exp2_of(top - ref);
+    sum *= a;
+#pragma unroll
+    for (int t = 0; t < C; ++t) r.out[t] *= a;
+#pragma unroll
+    for (int c = 0; c < kJoin; ++c) {
+      const float b = exp2_of(w[c] - ref);
+      if (base + c < n) {
+        sum += b;
+#pragma unroll
+        for (int t = 0; t < C; ++t) r.out[t] += b * y[c][t / 4][t % 4];
+      }
+    }
+    top = most;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+  for (int t = 0; t < C; ++t) r.out[t] *= inv;
+  r.lse2 = sum == 0.f ? -INFINITY : top + __log2f(sum);
+}
+
+// Publishes a unit's rows, joins the tile's parts if it is the last to arrive, and writes
+// the rows out. Thread (r, x) holds rows r + 16 i, columns x C .. x C + C - 1.
+template <int D, int R, int C>
+__device__ __forceinline__ void finish_unit(const AttentionParams& p, const Unit& u, RowPart<C> (&part)[R], int* flag) {
+  const int r = threadIdx.x >> 4, x = threadIdx.x & 15;
+  if (u.chunks > 1) {
+    constexpr int kSlotFloats = 16 * R * (D + 1);
+    const int step = u.tiles * p.Hkv;  // slots between neighbouring chunks of a tile
+    const int first = u.slot - u.chunk * step;
+    const int stride = step * kSlotFloats * 4;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        p.parts + (int64_t)first * kSlotFloats, 0, (u.chunks - 1) * stride + kSlotFloats * 4, kRawDword3);
+    auto publish = [&](int off) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int row = r + 16 * i;
+        if (row < u.rows) {
+#pragma unroll
+          for (int t = 0; t < C; t += 4)
+            __builtin_amdgcn_raw_buffer_store_b128(
+                __builtin_bit_cast(v4u, v4f{part[i].out[t], part[i].out[t + 1], part[i].out[t + 2], part[i].out[t + 3]}), rs,
+                off + (row * D + x * C + t) * 4, 0, kDeviceScope);
+          if (x == 0)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(part[i].lse2), rs, off + (16 * R * D + row) * 4, 0, kDeviceScope);
+        }
+      }
+    };
+    auto join = [&](int off, int gap, int n) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int row = r + 16 * i;
+        if (row < u.rows) join_parts<C>(part[i], rs, off + (row * D + x * C) * 4, off + (16 * R * D + row) * 4, gap, n);
+      }
+    };
+    const int group = u.chunk / kJoin, groups = (u.chunks + kJoin - 1) / kJoin;
+    const int in_group = min(kJoin, u.chunks - group * kJoin);
+    const int group_off = group * kJoin * stride;
+    if (in_group > 1) {
+      publish(u.chunk * stride);
+      if (!arrive_last(&p.counters[kTileCounters + first + group * kJoin * step], in_group, flag)) return;
+      join(group_off, stride, in_group);
+    }
+    if (groups > 1) {
+      __syncthreads();  // the flag is used again
+      publish(group_off);
+      if (!arrive_last(&p.counters[u.tile_id], groups, flag)) return;
+      join(0, kJoin * stride, groups);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int row = r + 16 * i;
+    if (row < u.rows) {
+      const int rr = u.row0 + row;
+      const int64_t token = u.seq.row0 + rr / p.group;
+      const int head = u.h * p.group + rr % p.group;
+      uint16_t* dst = p.O + token * p.ldo + head * D + x * C;
+#pragma unroll
+      for (int t = 0; t < C; t += 4)
+        *reinterpret_cast<uint2*>(dst + t) =
+            make_uint2(pack_bf16(part[i].out[t], part[i].out[t + 1]), pack_bf16(part[i].out[t + 2], part[i].out[t + 3]));
+      if (p.lse && x == 0) p.lse[token * p.Hq + head] = part[i].lse2 * 0.6931471805599453f;
+    }
+  }
+}
+
+// Eight weights of a row from a lane's logits s (times c), by exponent offsets a0 and a1 of
+// the two 16-key groups, as FP16; k0 and k1 turn their sums into l's terms.
+__device__ __forceinline__ v8h weights(const v4f& s0, const v4f& s1, float c0, float c1, float a0, float a1, float k0, float k1,
+                                       float& l) {
+  float w[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w[j] = exp2_of(__builtin_fmaf(s0[j], c0, a0));
+    w[4 + j] = exp2_of(__builtin_fmaf(s1[j], c1, a1));
+  }
+  l = __builtin_fmaf((w[0] + w[1]) + (w[2] + w[3]), k0, l);
+  l = __builtin_fmaf((w[4] + w[5]) + (w[6] + w[7]), k1, l);
+  v8h out;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) out[j] = (_Float16)w[j];
+  return out;
+}
+// Maximum of three, NaN ignored where another is a number (fmaxf costs an instruction more
+// for each operand that might be a signalling NaN).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+__device__ __forceinline__ float max4(const v4f& s) { return max3(max3(s[0], s[1], s[2]), s[3], s[3]); }
+__device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); }
+
+// Workgroups that registers leave room for on a CU.
+constexpr int attention_residents(int D, int R) { return D == 64 ? (R == 1 ? 4 : 3) : D == 128 ? 2 : 1; }
+
+template <int D, int R>
+__global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kernel(const AttentionParams p) {
+  using Ring = Stage<D>;
   constexpr int kWords = D / 64;       // 32-bit words of one value a lane feeds
   constexpr int kTiles = D / 16;       // 16-column tiles of V
   constexpr int kStride = D + 4;       // of a row of O in LDS
-  constexpr int kSlotFloats = kRowTile * (D + 1);
-  __shared__ float o_sh[4][kRowTile][kStride];
-  __shared__ float m_sh[4][kRowTile], l_sh[4][kRowTile];
-  __shared__ int e_sh[4], last_sh;
+  // the ring, and after the loop the waves' results
+  constexpr int kRingBytes = 4 * 2 * Ring::kBytes, kResultBytes = 4 * 16 * R * kStride * 4;
+  __shared__ __align__(16) uint8_t shared[kRingBytes > kResultBytes ? kRingBytes : kResultBytes];
+  __shared__ float m_sh[4][16 * R], mo_sh[4][16 * R], l_sh[4][16 * R];
+  __shared__ int flag;
+  auto o_sh = reinterpret_cast<float(*)[16 * R][kStride]>(shared);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, kg = lane >> 4;
+  Plan<16 * R, 32> plan;
+  plan.make(p);
   Unit u;
-  if (!find_unit<kRowTile, 32>(p, blockIdx.x, kMinChunk, u)) return;
+  if (!find_unit(p, plan, blockIdx.x, u)) return;
 
-  // this lane's row: query fragments, and the keys that it sees, [key_lo, key_hi)
-  const bool live = n < u.rows;
-  const int row = u.row0 + (live ? n : 0);
-  const int token = row / p.group, head = u.h * p.group + row % p.group;
-  const int pos = u.seq.len - u.seq.rows + token;
-  const int key_hi = min(u.seq.len, pos + 1);
-  const int key_lo = p.window ? max(0, pos - p.window + 1) : 0;
-  v8bf qf[D / 32];
-  {
+  // this lane's rows: query fragments, and the keys that each sees, [key_lo, key_hi)
+  int key_lo[R], key_hi[R];
+  v8bf qf[R][D / 32];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const bool live = n + 16 * i < u.rows;
+    const int row = u.row0 + (live ? n + 16 * i : 0);
+    const int token = row / p.group, head = u.h * p.group + row % p.group;
+    const int pos = u.seq.len - u.seq.rows + token;
+    key_hi[i] = min(u.seq.len, pos + 1);
+    key_lo[i] = p.window ? max(0, pos - p.window + 1) : 0;
     const uint16_t* src = p.q + (int64_t)(u.seq.row0 + token) * p.ldq + head * D;
 #pragma unroll
     for (int s = 0; s < D / 32; ++s) {
       uint4 x = make_uint4(0, 0, 0, 0);
       if (live) x = *reinterpret_cast<const uint4*>(src + (s >> 1) * 64 + kg * 16 + (s & 1) * 8);
-      qf[s] = __builtin_bit_cast(v8bf, x);
+      // the scale's sign is taken here, so that the factors of logits are not negative
+      x.x ^= p.q_sign, x.y ^= p.q_sign, x.z ^= p.q_sign, x.w ^= p.q_sign;
+      qf[i][s] = __builtin_bit_cast(v8bf, x);
     }
   }
   // keys that every row of the tile sees
   const int all_hi = min(u.seq.len, u.pos0 + 1), all_lo = p.window ? u.pos1 - p.window + 1 : 0;
 
-  v4f o[kTiles];
+  v4f o[R][kTiles];
+  float m[R], mo[R], l[R];
+  float a0[R], a1[R], k0[R], k1[R];  // offsets and factors of the step's two 16-key groups
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) o[t] = v4f{0.f, 0.f, 0.f, 0.f};
-  float m = kNone, l = 0.f;
-  int ev = 0;  // exponent field of the largest value scale so far
+  for (int i = 0; i < R; ++i) {
+    m[i] = mo[i] = kNone, l[i] = 0.f;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) o[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+  int e0 = -1, e1 = -1;  // the groups' value scales (exponent fields) that these belong to
 
   const int steps = (u.k1 - u.k0 + 31) >> 5, share = (steps + 3) >> 2;
   const int step0 = min(steps, wave * share), step1 = min(steps, step0 + share);
@@ -284,205 +522,217 @@ __global__ void __launch_bounds__(256) attention_kernel(const AttentionParams p)
       }
     }
     const int count = min(32, step1 - seg);
-    auto fetch = [&](int s, Raw<D>& r) {
-      const int key = u.k0 + (seg + s) * 32;
-      const int p0 = __builtin_amdgcn_readlane(page, 2 * s), p1 = __builtin_amdgcn_readlane(page, 2 * s + 1);
-      const int mask = (1 << p.log_p) - 1;
-      const int64_t b0 = (((int64_t)max(p0, 0) * p.Hkv + u.h) << p.log_p) + (key & mask);
-      const int64_t b1 = (((int64_t)max(p1, 0) * p.Hkv + u.h) << p.log_p) + ((key + 16) & mask);
-      load_raw<D>(r, p, b0, b1, lane);
+    const uint8_t* ring = shared + wave * 2 * Ring::kBytes;
+    const uint32_t ring_lds = __builtin_amdgcn_readfirstlane(lds_address(ring));
+    // first byte of the rows of 16-key group g of this segment (page 0 stands in for none)
+    auto rows_of = [&](const uint8_t* cache, int g) {
+      const int at = (u.k0 + seg * 32 + 16 * g) & ((1 << p.log_p) - 1);
+      const int pg = max(__builtin_amdgcn_readlane(page, g), 0);
+      return uniform(cache + (((((int64_t)pg * p.Hkv + u.h) << p.log_p) + at) * D));
     };
-    Raw<D> next;
-    fetch(0, next);
+    auto fetch_keys = [&](int s) {
+      Ring::load_keys(rows_of(p.k_cache, 2 * s), rows_of(p.k_cache, 2 * s + 1), ring_lds + (s & 1) * Ring::kBytes, lane);
+    };
+    auto fetch_values = [&](int s) {
+      Ring::load_values(rows_of(p.v_cache, 2 * s), rows_of(p.v_cache, 2 * s + 1), ring_lds + (s & 1) * Ring::kBytes, lane);
+    };
+    wait_loads<0>();  // the pages and scales
+    fetch_keys(0);
+    fetch_values(0);
+    if (count > 1) {
+      fetch_keys(1);
+      fetch_values(1);
+    }
     for (int s = 0; s < count; ++s) {
-      Raw<D> r = next;
-      if (s + 1 < count) fetch(s + 1, next);
+      const int left = count - 1 - s;  // steps after this one
+      const uint8_t* stage = ring + (s & 1) * Ring::kBytes;
       const int key = u.k0 + (seg + s) * 32;
       const int pg0 = __builtin_amdgcn_readlane(page, 2 * s), pg1 = __builtin_amdgcn_readlane(page, 2 * s + 1);
-      const float c0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 2 * s));
-      const float c1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 2 * s + 1));
-      const int e0 = exponent(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), 2 * s)));
-      const int e1 = exponent(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), 2 * s + 1)));
+      float c0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 2 * s));
+      float c1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 2 * s + 1));
+      const int now0 = exponent(__builtin_amdgcn_readlane(__float_as_uint(vs), 2 * s));
+      const int now1 = exponent(__builtin_amdgcn_readlane(__float_as_uint(vs), 2 * s + 1));
 
-      v4f s0{0.f, 0.f, 0.f, 0.f}, s1{0.f, 0.f, 0.f, 0.f};
+      v4f s0[R], s1[R];
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(r.k[0][i].x, r.k[0][i].y), qf[2 * i], s0, 0, 0, 0);
-        s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(r.k[1][i].x, r.k[1][i].y), qf[2 * i], s1, 0, 0, 0);
-        s0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(r.k[0][i].z, r.k[0][i].w), qf[2 * i + 1], s0, 0, 0, 0);
-        s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(r.k[1][i].z, r.k[1][i].w), qf[2 * i + 1], s1, 0, 0, 0);
+      for (int i = 0; i < R; ++i) s0[i] = s1[i] = v4f{0.f, 0.f, 0.f, 0.f};
+      if (left >= 1) wait_loads<3 * Ring::kLoads>();
+      else wait_loads<Ring::kLoads>();
+      uint4 kx[2][D / 64];
+#pragma unroll
+      for (int i = 0; i < Ring::kLoads; ++i)
+        kx[i / Ring::kPieces][i % Ring::kPieces] = *reinterpret_cast<const uint4*>(stage + i * 1024 + lane * 16);
+      if (left >= 2) {
+        wait_lds_reads();
+        fetch_keys(s + 2);
       }
-      float x[8];  // this lane's keys: key + 4 kg + j, and 16 further for j >= 4
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = s0[j] * c0, x[4 + j] = s1[j] * c1;
+      for (int d = 0; d < D / 32; ++d) {
+        const uint4 x = kx[0][d >> 1], y = kx[1][d >> 1];
+        const v8bf a = (d & 1) ? codes_bf16(x.z, x.w) : codes_bf16(x.x, x.y);
+        const v8bf b = (d & 1) ? codes_bf16(y.z, y.w) : codes_bf16(y.x, y.y);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          s0[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, qf[i][d], s0[i], 0, 0, 0);
+          s1[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, qf[i][d], s1[i], 0, 0, 0);
+        }
+      }
+      if (left >= 2) wait_loads<3 * Ring::kLoads>();
+      else if (left == 1) wait_loads<2 * Ring::kLoads>();
+      else wait_loads<0>();
+      uint32_t v[8][kWords];  // this lane's values: key + 4 kg + j, and 16 further for j >= 4
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        load_value<D>(v[j], stage + Ring::kHalf + ((j >> 2) * 16 + kg * 4 + (j & 3)) * D + n * (D / 16));
+      if (left >= 2) {
+        wait_lds_reads();
+        fetch_values(s + 2);
+      }
       uint32_t nan_keys = 0;
-      if (key < all_lo || key + 32 > all_hi || pg0 < 0 || pg1 < 0) {  // some row does not see all of the step
+      bool any_nan = false;
+      // some row does not see all of the step
+      if (rarely(key < all_lo || key + 32 > all_hi || pg0 < 0 || pg1 < 0)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int at = key + (j >> 2) * 16 + kg * 4 + (j & 3);
           const bool there = (j < 4 ? pg0 : pg1) >= 0;
-          if (!there || at < key_lo || at >= key_hi) x[j] = -INFINITY;
           // values that no row sees may be anything: they count as 0. Where a row sees a
           // NaN code and another does not, the product gets 0 and the rows that see it NaN
           // by their probability.
           if (!there || at < u.lo || at >= u.hi) {
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) r.v[j][w] = 0;
+            for (int w = 0; w < kWords; ++w) v[j][w] = 0;
           } else {
             bool bad = false;
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) bad |= any_nan_code(r.v[j][w]);
+            for (int w = 0; w < kWords; ++w) bad |= any_nan_code(v[j][w]);
             if (bad) {
               nan_keys |= 1u << j;
 #pragma unroll
-              for (int w = 0; w < kWords; ++w) r.v[j][w] = 0;
+              for (int w = 0; w < kWords; ++w) v[j][w] = 0;
             }
           }
         }
-        if (__any(nan_keys != 0)) {  // over the 16 lanes that feed the same keys
+        any_nan = __any(nan_keys != 0);
+        if (rarely(any_nan)) {  // over the 16 lanes that feed the same keys
 #pragma unroll
           for (int off = 1; off < 16; off <<= 1) nan_keys |= __shfl_xor((int)nan_keys, off, 64);
         }
-      }
-      float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      if (__any(top > m + kLag) || max(e0, e1) > ev) {  // rare after a row's first steps
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float now = fmaxf(m, top);
-        const int e_now = max(ev, max(e0, e1));
-        const float a = exp2_of(m - now), b = a * pow2(ev - e_now);
-        m = now, ev = e_now;
-        l *= a;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) o[t] *= b;
-      }
-      const float f0 = pow2(15 - kLag + e0 - ev), f1 = pow2(15 - kLag + e1 - ev);
-      v8h pf;
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float pr = exp2_of(x[j] - m);
-        l += pr;
-        float w = pr * (j < 4 ? f0 : f1);
-        if ((nan_keys >> j & 1) && x[j] > -INFINITY) w = __builtin_nanf("");
-        pf[j] = (_Float16)w;
+          for (int j = 0; j < 8; ++j) {
+            const int at = key + (j >> 2) * 16 + kg * 4 + (j & 3);
+            const bool seen = (j < 4 ? pg0 : pg1) >= 0 && at >= key_lo[i] && at < key_hi[i];
+            if (j < 4) s0[i][j] = seen ? s0[i][j] * c0 : -INFINITY;  // factors may be 0: they come before the mask
+            else s1[i][j - 4] = seen ? s1[i][j - 4] * c1 : -INFINITY;
+          }
+        c0 = c1 = 1.f;
+      }
+      const float v0 = (float)(now0 - 127), v1 = (float)(now1 - 127);
+      float top[R], top_o[R];
+      bool move = false;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float t0 = max4(s0[i]) * c0, t1 = max4(s1[i]) * c1;
+        top[i] = max3(t0, t1, t1), top_o[i] = max3(t0 + v0, t1 + v1, t1 + v1);
+        move |= max3(top[i] - m[i], top_o[i] - mo[i], top_o[i] - mo[i]) > kLag;
+      }
+      const bool moved = __any(move);
+      if (rarely(moved)) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          float t = fmaxf(top[i], __shfl_xor(top[i], 16, 64)), to = fmaxf(top_o[i], __shfl_xor(top_o[i], 16, 64));
+          t = fmaxf(m[i], fmaxf(t, __shfl_xor(t, 32, 64))), to = fmaxf(mo[i], fmaxf(to, __shfl_xor(to, 32, 64)));
+          l[i] *= exp2_of(m[i] - t);
+          const float b = exp2_of(mo[i] - to);
+          m[i] = t, mo[i] = to;
+#pragma unroll
+          for (int t2 = 0; t2 < kTiles; ++t2) o[i][t2] *= b;
+        }
+      }
+      if (rarely(moved || now0 != e0 || now1 != e1)) {
+        e0 = now0, e1 = now1;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          a0[i] = fmaxf(v0 + (15 - kLag) - mo[i], kFar - m[i]), k0[i] = exp2_of(-(a0[i] + m[i]));
+          a1[i] = fmaxf(v1 + (15 - kLag) - mo[i], kFar - m[i]), k1[i] = exp2_of(-(a1[i] + m[i]));
+        }
+      }
+      v8h pf[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        pf[i] = weights(s0[i], s1[i], c0, c1, a0[i], a1[i], k0[i], k1[i], l[i]);
+        if (rarely(any_nan)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if ((nan_keys >> j & 1) && (j < 4 ? s0[i][j] : s1[i][j - 4]) > -INFINITY) pf[i][j] = (_Float16)__builtin_nanf("");
+        }
       }
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
         uint32_t words[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) words[j] = r.v[j][w];
-        v8h a, b;
-        columns_f16(words, false, a, b);
-        o[4 * w] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf, o[4 * w], 0, 0, 0);
-        o[4 * w + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pf, o[4 * w + 1], 0, 0, 0);
-        columns_f16(words, true, a, b);
-        o[4 * w + 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf, o[4 * w + 2], 0, 0, 0);
-        o[4 * w + 3] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pf, o[4 * w + 3], 0, 0, 0);
-      }
-    }
-  }
-
-  // join the four waves: row n's column (4 kg + i) (D / 16) + t is o[t][i]
-  l += __shfl_xor(l, 16, 64);
-  l += __shfl_xor(l, 32, 64);
+        for (int j = 0; j < 8; ++j) words[j] = v[j][w];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+        for (int half = 0; half < 2; ++half) {
+          v8h a, b;
+          columns_f16(words, half != 0, a, b);
 #pragma unroll
-    for (int t = 0; t < kTiles; t += 4)
-      *reinterpret_cast<float4*>(&o_sh[wave][n][(4 * kg + i) * kTiles + t]) =
-          make_float4(o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]);
-  if (kg == 0) m_sh[wave][n] = m, l_sh[wave][n] = l;
-  if (lane == 0) e_sh[wave] = ev;
-  __syncthreads();
-
-  // thread (r, x): row r, columns x D / 16 .. + D / 16
-  const int r = threadIdx.x >> 4, x = threadIdx.x & 15;
-  float top = kNone, sum = 0.f, out[kTiles];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, m_sh[w][r]);
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) out[t] = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float a = exp2_of(m_sh[w][r] - top);
-    sum += a * l_sh[w][r];
-    // a wave's sums stand for themselves times 2^(its value exponent) / 2^(15 - kLag)
-    const int e = e_sh[w] - 127 - (15 - kLag);
-    const float b = a * pow2(e / 2), c = pow2(e - e / 2);  // in two steps: each in range
-#pragma unroll
-    for (int t = 0; t < kTiles; t += 4) {
-      const float4 y = *reinterpret_cast<const float4*>(&o_sh[w][r][x * kTiles + t]);
-      out[t] += y.x * b * c, out[t + 1] += y.y * b * c, out[t + 2] += y.z * b * c, out[t + 3] += y.w * b * c;
-    }
-  }
-  // a row that saw no key: 0, and minus infinity
-  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) out[t] *= inv;
-  float lse2 = sum == 0.f ? -INFINITY : top + __log2f(sum);
-
-  if (u.chunks > 1) {
-    const int slot_bytes = kSlotFloats * 4;
-    const int stride = u.tiles * p.Hkv;  // slots between chunks of a tile
-    const int first = u.slot - u.chunk * stride;
-    float* base = p.parts + (int64_t)first * kSlotFloats;
-    const __amdgpu_buffer_rsrc_t rs =
-        __builtin_amdgcn_make_buffer_rsrc(base, 0, ((u.chunks - 1) * stride + 1) * slot_bytes, kRawDword3);
-    const int at = r * D * 4 + x * kTiles * 4, lse_at = (kRowTile * D + r) * 4;
-    if (r < u.rows) {
-#pragma unroll
-      for (int t = 0; t < kTiles; t += 4)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v4f{out[t], out[t + 1], out[t + 2], out[t + 3]}),
-                                               rs, u.chunk * stride * slot_bytes + at + t * 4, 0, kDeviceScope);
-      if (x == 0)
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lse2), rs, u.chunk * stride * slot_bytes + lse_at, 0,
-                                              kDeviceScope);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the part has reached the device-coherent level
-    __syncthreads();
-    if (threadIdx.x == 0)
-      last_sh = __hip_atomic_fetch_add(&p.counters[u.tile_id], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                u.chunks - 1;
-    __syncthreads();
-    if (!last_sh) return;
-    if (threadIdx.x == 0) __hip_atomic_store(&p.counters[u.tile_id], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (r < u.rows) {
-      float most = -INFINITY;
-      for (int c = 0; c < u.chunks; ++c)
-        most = fmaxf(most, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, c * stride * slot_bytes + lse_at, 0,
-                                                                                kDeviceScope)));
-      if (!(most > -INFINITY)) most = 0.f;
-      sum = 0.f;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) out[t] = 0.f;
-      for (int c = 0; c < u.chunks; ++c) {
-        const int off = c * stride * slot_bytes;
-        const float part = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, off + lse_at, 0, kDeviceScope));
-        const float a = exp2_of(part - most);
-        sum += a;
-#pragma unroll
-        for (int t = 0; t < kTiles; t += 4) {
-          const v4f y = __builtin_bit_cast(
-              v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off + at + t * 4, 0, kDeviceScope));
-          out[t] += a * y.x, out[t + 1] += a * y.y, out[t + 2] += a * y.z, out[t + 3] += a * y.w;
+          for (int i = 0; i < R; ++i) {
+            o[i][4 * w + 2 * half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[i], o[i][4 * w + 2 * half], 0, 0, 0);
+            o[i][4 * w + 2 * half + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pf[i], o[i][4 * w + 2 * half + 1], 0, 0, 0);
+          }
         }
       }
-      const float scale = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) out[t] *= scale;
-      lse2 = sum == 0.f ? -INFINITY : most + __log2f(sum);
     }
   }
-  if (r < u.rows) {
-    const int rr = u.row0 + r;
-    const int64_t tok = u.seq.row0 + rr / p.group;
-    const int hd = u.h * p.group + rr % p.group;
-    uint16_t* dst = p.O + tok * p.ldo + hd * D + x * kTiles;
+
+  __syncthreads();  // the ring becomes the waves' results
+  // join the four waves: row n + 16 i's column (4 kg + j) (D / 16) + t is o[i][t][j]
 #pragma unroll
-    for (int t = 0; t < kTiles; t += 4)
-      *reinterpret_cast<uint2*>(dst + t) = make_uint2(pack_bf16(out[t], out[t + 1]), pack_bf16(out[t + 2], out[t + 3]));
-    if (p.lse && x == 0) p.lse[tok * p.Hq + hd] = lse2 * 0.6931471805599453f;
+  for (int i = 0; i < R; ++i) {
+    l[i] += __shfl_xor(l[i], 16, 64);
+    l[i] += __shfl_xor(l[i], 32, 64);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int t = 0; t < kTiles; t += 4)
+        *reinterpret_cast<float4*>(&o_sh[wave][n + 16 * i][(4 * kg + j) * kTiles + t]) =
+            make_float4(o[i][t][j], o[i][t + 1][j], o[i][t + 2][j], o[i][t + 3][j]);
+    if (kg == 0) m_sh[wave][n + 16 * i] = m[i], mo_sh[wave][n + 16 * i] = mo[i], l_sh[wave][n + 16 * i] = l[i];
   }
+  __syncthreads();
+
+  // thread (r, x): rows r + 16 i, columns x D / 16 .. + D / 16
+  RowPart<kTiles> part[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int r = (threadIdx.x >> 4) + 16 * i, x = threadIdx.x & 15;
+    float top = kNone, top_o = kNone, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, m_sh[w][r]), top_o = fmaxf(top_o, mo_sh[w][r]);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) part[i].out[t] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      sum += exp2_of(m_sh[w][r] - top) * l_sh[w][r];
+      const float b = exp2_of(mo_sh[w][r] - top_o);
+#pragma unroll
+      for (int t = 0; t < kTiles; t += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(&o_sh[w][r][x * kTiles + t]);
+        part[i].out[t] += y.x * b, part[i].out[t + 1] += y.y * b, part[i].out[t + 2] += y.z * b, part[i].out[t + 3] += y.w * b;
+      }
+    }
+    // o stands for itself times 2^(mo - m - (15 - kLag)), in two factors so that each is in
+    // range; a row that saw no key gives 0, and minus infinity
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    const float shift = fminf(fmaxf(0.5f * (top_o - top - (15 - kLag)), -126.f), 126.f), half = exp2_of(shift);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) part[i].out[t] = part[i].out[t] * inv * half * half;
+    part[i].lse2 = sum == 0.f ? -INFINITY : top + __log2f(sum);
+  }
+  finish_unit<D, R, kTiles>(p, u, part, &flag);
 }
 
 }  // namespace fp8layer

@@ -67,26 +67,52 @@ __device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8]) {
   return make_uint2((uint32_t)a, (uint32_t)b);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+// Reductions and prefix sums over the wave's lanes, by data-parallel primitives (a few
+// cycles a step, where a shuffle goes through LDS). Within a row of 16 lanes: quad
+// permutations, then mirrored halves and rows; over rows: the last lane of a row
+// broadcast into the next ones.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int dpp(int old, int v) {
+  return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __int_as_float(dpp<CTRL, ROWS>(__float_as_int(old), __float_as_int(v)));
+}
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;  // of a row's lanes
+constexpr int kShift = 0x110, kLast15 = 0x142, kLast31 = 0x143;
+
+// Inclusive prefix sum.
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) {
+  v += dpp<kShift + 1>(T(0), v);
+  v += dpp<kShift + 2>(T(0), v);
+  v += dpp<kShift + 4>(T(0), v);
+  v += dpp<kShift + 8>(T(0), v);
+  v += dpp<kLast15, 0xA>(T(0), v);
+  v += dpp<kLast31, 0xC>(T(0), v);
   return v;
 }
 
+__device__ __forceinline__ float last_lane(float v) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63)); }
+__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+
+__device__ __forceinline__ float wave_sum(float v) { return last_lane(wave_scan(v)); }
+
+// Maximum over the lane's row of 16, in every lane of it.
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp<kSwap1>(v, v));
+  v = fmaxf(v, dpp<kSwap2>(v, v));
+  v = fmaxf(v, dpp<kHalfMirror>(v, v));
+  return fmaxf(v, dpp<kMirror>(v, v));
+}
+
+// Maximum over the wave.
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
-}
-
-// Inclusive prefix sum over the wave's lanes.
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(v, o, 64);
-    if (lane >= o) v += u;
-  }
-  return v;
+  v = row_max(v);
+  v = fmaxf(v, dpp<kLast15, 0xA>(v, v));
+  v = fmaxf(v, dpp<kLast31, 0xC>(v, v));
+  return last_lane(v);
 }
 
 // The part of a sequence that a call concerns, from its device arrays, clamped to what

@@ -305,7 +305,8 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
   p.ldq = ldq;
   p.ldo = ldo;
   p.ld_bt = ld_bt;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.scale_log2 = std::fabs(softmax_scale) * 1.4426950408889634f;
+  p.q_sign = softmax_scale < 0.f ? 0x80008000u : 0u;
   p.window = window >= max_len ? 0 : window;  // no key is that far back
   p.B = B;
   p.T = T;
@@ -315,24 +316,36 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
   p.num_pages = num_pages;
   p.log_p = log2_of(P);
   p.max_pages = max_pages;
-  // Most row tiles, times heads; most keys of one tile; units: one for each tile and head,
-  // and those that splitting adds.
-  const int64_t tiles = (std::min(B, T) + (int64_t)T * p.group / fp8layer::kRowTile) * Hkv;
-  const size_t slot = (size_t)fp8layer::kRowTile * (D + 1) * sizeof(float);
+  // Sixteen rows a tile where the calls' sequences have no more on average, 32 otherwise.
+  const int row_blocks = D == 256 || (int64_t)T * p.group <= 16 * (int64_t)B ? 1 : 2;
+  const int tile = 16 * row_blocks;
+  // Most row tiles, times heads. Splitting adds units up to a number that gives every CU
+  // a few: that many are wanted, and the workspace has a slot for each unit.
+  const int64_t tiles = (std::min(B, T) + (int64_t)T * p.group / tile) * Hkv;
+  const size_t slot = (size_t)tile * (D + 1) * sizeof(float);
   const size_t bytes = std::min<size_t>(workspace ? workspace_bytes : 0, (size_t)1 << 30);
   const int64_t slots = bytes > kAttentionCounterBytes ? (int64_t)((bytes - kAttentionCounterBytes) / slot) : 0;
-  const int64_t wanted = std::min<int64_t>((int64_t)cus * 8, slots - tiles);
+  p.residents = cus * fp8layer::attention_residents(D, row_blocks);
+  // Units that splitting may add: as many as are resident where the longest sequences that
+  // the table allows make one round of work, four times that otherwise (workgroups
+  // without a unit end at once, but they cost a microsecond a round).
+  const int64_t keys = tiles * max_len;
+  const int64_t rounds = keys <= fp8layer::kOneRound * p.residents ? 1 : 4;
+  const int64_t added = std::min(rounds * p.residents, std::min<int64_t>(slots, fp8layer::kPartCounters) - tiles);
   int64_t grid = tiles;
-  if (tiles <= fp8layer::kCounters && wanted > 0 && max_len > fp8layer::kMinChunk) {
-    p.units_wanted = (int)wanted;
+  if (tiles <= fp8layer::kTileCounters && added > 0 && max_len > fp8layer::kMinChunk) {
+    p.most_units = (int)added;
     p.counters = static_cast<int32_t*>(workspace);
     p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttentionCounterBytes);
-    grid = std::min(tiles + wanted, tiles * ceil_div(max_len, fp8layer::kMinChunk));
+    grid = std::min(tiles + added, tiles * ceil_div(max_len, fp8layer::kMinChunk));
   }
   if (grid > INT32_MAX) return FP8GEMM_ERR_SHAPE;
   auto go = [&](auto d) {
     constexpr int kD = decltype(d)::value;
-    hipLaunchKernelGGL((fp8layer::attention_kernel<kD>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+    if (row_blocks == 1)
+      hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+    else if constexpr (kD < 256)
+      hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2>), dim3((unsigned)grid), dim3(256), 0, stream, p);
   };
   if (D == 64) go(Int<64>{});
   else if (D == 128) go(Int<128>{});

@@ -137,18 +137,17 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
       page0 = max(mine.len - mine.rows, 0) >> p.log_p;
       if (mine.rows > 0 && mine.len > 0) count = ((mine.len - 1) >> p.log_p) - page0 + 1;
     }
-    const int incl = wave_scan(count, lane);
+    const int incl = wave_scan(count);
     const uint64_t hit = __ballot(want < done + incl);
     if (hit) {
       const int src = __ffsll((unsigned long long)hit) - 1;
-      sq.row0 = __shfl(mine.row0, src, 64);
-      sq.rows = __shfl(mine.rows, src, 64);
-      sq.len = __shfl(mine.len, src, 64);
-      first_page = __shfl(page0, src, 64) + want - (done + __shfl(incl - count, src, 64));
+      auto pick = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
+      sq = {pick(mine.row0), pick(mine.rows), pick(mine.len)};
+      first_page = pick(page0) + want - (done + pick(incl - count));
       done = base + src;  // the sequence, from here on
       found = true;
     } else {
-      done += __shfl(incl, 63, 64);
+      done += last_lane(incl);
     }
   }
   if (!found) return;  // the grid covers the most units that there can be (all waves of a shared unit agree)

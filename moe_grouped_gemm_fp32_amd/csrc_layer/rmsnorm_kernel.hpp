@@ -80,8 +80,7 @@ __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quantize_ker
         amax = fmaxf(amax, fabsf(y[j]));
       }
       if (p.Y) store8(static_cast<uint16_t*>(p.Y) + (int64_t)row * p.ldy + c * 8, y);
-#pragma unroll
-      for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 16));
+      amax = row_max(amax);
       float s = amax / kE4m3Max;
       if (!(s > 0.f)) s = 1.0f;
 #pragma unroll
