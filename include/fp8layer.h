@@ -19,8 +19,8 @@
  *           page and head lie together. P (the page size) is 16, 32, 64, 128 or 256, D
  *           (the head size) 64, 128 or 256.
  *   scales  fp32 [num_pages][Hkv], contiguous: one power of two per page and head (a UE8M0
- *           value held as FP32; only its exponent is read where noted). A code c of page p
- *           and head h stands for c * scales[p][h].
+ *           value held as FP32; only its exponent is read). A code c of page p and head h
+ *           stands for c * scales[p][h].
  * Which pages hold a sequence is its row of the block table:
  *   block_table  int32 [B][ld_bt]: entry j < max_pages is the page of token slots
  *           j P .. j P + P - 1. Entries past a sequence's length are not read.
@@ -138,7 +138,7 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
  * rounded to 11 bits for the second product, whose sum is FP32; statistics are FP32.
  *   q    BF16 [T, Hq, D], row stride ldq; O BF16 [T, Hq, D], row stride ldo; lse optional
  *        fp32 [T, Hq], contiguous.
- *   Of the value scales only the exponents are read.
+ *   Of the cache's scales only the exponents are read.
  *   workspace  optional, 16-byte aligned: lets long sequences be split over workgroups,
  *        whose results are joined in a fixed order. Its first 64 KiB (arrival counters)
  *        must be zero before its first use, and are zero again when a call completes. Any

@@ -316,16 +316,19 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
   p.num_pages = num_pages;
   p.log_p = log2_of(P);
   p.max_pages = max_pages;
-  // Sixteen rows a tile where the calls' sequences have no more on average, 32 otherwise.
-  const int row_blocks = D == 256 || (int64_t)T * p.group <= 16 * (int64_t)B ? 1 : 2;
-  const int tile = 16 * row_blocks;
+  // Rows that share a key head, on average over the sequences: sixteen a tile if there are
+  // no more, 32 otherwise (registers allow 16 where heads are 256 wide). Up to one tile, the
+  // tile is the only reader of its keys and values.
+  const int64_t rows = ceil_div((int64_t)T * p.group, B);
+  const int tile = rows <= 16 || D == 256 ? 16 : 32;
+  const bool stream_kv = rows <= tile;
   // Most row tiles, times heads. Splitting adds units up to a number that gives every CU
   // a few: that many are wanted, and the workspace has a slot for each unit.
   const int64_t tiles = (std::min(B, T) + (int64_t)T * p.group / tile) * Hkv;
   const size_t slot = (size_t)tile * (D + 1) * sizeof(float);
   const size_t bytes = std::min<size_t>(workspace ? workspace_bytes : 0, (size_t)1 << 30);
   const int64_t slots = bytes > kAttentionCounterBytes ? (int64_t)((bytes - kAttentionCounterBytes) / slot) : 0;
-  p.residents = cus * fp8layer::attention_residents(D, row_blocks);
+  p.residents = cus * fp8layer::attention_residents(D, tile / 16);
   // Units that splitting may add: as many as are resident where the longest sequences that
   // the table allows make one round of work, four times that otherwise (workgroups
   // without a unit end at once, but they cost a microsecond a round).
@@ -342,10 +345,15 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
   if (grid > INT32_MAX) return FP8GEMM_ERR_SHAPE;
   auto go = [&](auto d) {
     constexpr int kD = decltype(d)::value;
-    if (row_blocks == 1)
-      hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1>), dim3((unsigned)grid), dim3(256), 0, stream, p);
-    else if constexpr (kD < 256)
-      hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+    const dim3 groups((unsigned)grid);
+    if constexpr (kD == 256) {
+      if (stream_kv) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true>), groups, dim3(256), 0, stream, p);
+      else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, false>), groups, dim3(256), 0, stream, p);
+    } else {
+      if (tile == 16) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true>), groups, dim3(256), 0, stream, p);
+      else if (stream_kv) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, true>), groups, dim3(256), 0, stream, p);
+      else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, false>), groups, dim3(256), 0, stream, p);
+    }
   };
   if (D == 64) go(Int<64>{});
   else if (D == 128) go(Int<128>{});
