@@ -19,7 +19,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import _bytes_view, _check, _ld, _ptr, _require, _stream, lib, scale_ld, QUANT_BF16, QUANT_FP32
+from . import _check, _ld, _require, lib, scale_ld, QUANT_BF16, QUANT_FP32
 
 __all__ = ["PagedKVCache", "make_paged_kv_cache", "rmsnorm_quantize_1x128", "rmsnorm_backward", "rope_append_paged_kv",
            "paged_attention", "attention_workspace_size", "make_attention_workspace"]
@@ -39,9 +39,14 @@ _SIGS = {
                _INT, _INT, _P, _SZ, _P]),
     "fp8_paged_attention_workspace_size": (_SZ, []),
 }
+_BF16, _FP32, _U8, _I32, _FP8 = torch.bfloat16, torch.float32, torch.uint8, torch.int32, torch.float8_e4m3fn
+_DTYPES = {_BF16: QUANT_BF16, _FP32: QUANT_FP32}
 _fns: dict = {}
 
 
+# A decode step calls these operators for microseconds of GPU work each, so the checks below
+# are plain comparisons: a message is only put together when one fails, and pointers go to
+# the library as integers.
 def _fn(name: str):
     fn = _fns.get(name)
     if fn is None:
@@ -51,16 +56,37 @@ def _fn(name: str):
     return fn
 
 
-def _dtype_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
-        return QUANT_BF16
-    _require(t.dtype == torch.float32, f"{name} must be bfloat16 or float32")
-    return QUANT_FP32
+_current_stream = torch._C._cuda_getCurrentRawStream  # current_stream(dev).cuda_stream without a Stream object: 0.1 us, not 1.9
 
 
-def _rows(t: torch.Tensor, name: str, M: int, K: int, dtype, dev):
-    _require(t.shape == (M, K) and t.dtype == dtype and t.device == dev and t.stride(1) == 1,
-             f"{name} must be {dtype} [{M}, {K}] on {dev} with a unit inner stride")
+def _raw_stream(dev: torch.device, stream) -> int:
+    return _current_stream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _refuse(msg: str):
+    raise ValueError(msg)
+
+
+def _matrix(t: torch.Tensor, name: str, shape, dtype, dev) -> int:
+    """Row stride of a tensor that must be `dtype` of `shape` [M, K] with a unit inner stride."""
+    if t.shape != shape or t.dtype is not dtype or t.device != dev or t.stride(1) != 1:
+        _refuse(f"{name} must be {dtype} {list(shape)} on {dev} with a unit inner stride")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _vector(t: torch.Tensor, name: str, n: int, dtype, dev) -> int:
+    """Address of a tensor that must be contiguous `dtype` [n]."""
+    if t.dim() != 1 or t.shape[0] != n or t.dtype is not dtype or t.device != dev or (n > 1 and t.stride(0) != 1):
+        _refuse(f"{name} must be contiguous {dtype} [{n}] on {dev}")
+    return t.data_ptr()
+
+
+def _rows_of(X: torch.Tensor, name: str):
+    """(dtype code, M, K) of the 2-D GPU tensor that a norm call is about."""
+    code = _DTYPES.get(X.dtype)
+    if not X.is_cuda or X.dim() != 2 or X.stride(1) != 1 or code is None or X.shape[1] % 128 != 0:
+        _refuse(f"{name} must be a 2-D bfloat16 or float32 GPU tensor with a unit inner stride and a multiple of 128 columns")
+    return code, X.shape[0], X.shape[1]
 
 
 def rmsnorm_quantize_1x128(X: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -76,40 +102,37 @@ def rmsnorm_quantize_1x128(X: torch.Tensor, weight: torch.Tensor, residual: Opti
     for rmsnorm_backward. Y: optional bfloat16 [M, K], receives the norm unquantised.
     weight: [K], bfloat16 or float32. K: a multiple of 128, at most 65536. Outputs may be
     given (written in place)."""
-    _require(X.device.type == "cuda" and X.dim() == 2 and X.stride(1) == 1,
-             "X must be a 2-D GPU tensor with a unit inner stride")
-    code, dev = _dtype_code(X, "X"), X.device
-    M, K = X.shape
-    _require(K % 128 == 0, "K must be a multiple of 128")
-    wcode = _dtype_code(weight, "weight")
-    _require(weight.shape == (K,) and weight.device == dev and weight.stride(0) == 1, "weight must be contiguous [K]")
+    code, M, K = _rows_of(X, "X")
+    dev, shape = X.device, (M, K)
+    w = _vector(weight, "weight", K, weight.dtype if weight.dtype in _DTYPES else _FP32, dev)
+    r = h = y = 0
+    ldr = ldh = ldy = 0
     if residual is not None:
-        _rows(residual, "residual", M, K, X.dtype, dev)
+        ldr, r = _matrix(residual, "residual", shape, X.dtype, dev), residual.data_ptr()
         if H is None:
-            H = torch.empty_like(X, memory_format=torch.contiguous_format)
-        _rows(H, "H", M, K, X.dtype, dev)
+            H = torch.empty(shape, dtype=X.dtype, device=dev)
+        ldh, h = _matrix(H, "H", shape, X.dtype, dev), H.data_ptr()
     else:
-        _require(H is None or H is X, "H is written only with a residual")
+        if H is not None and H is not X:
+            _refuse("H is written only with a residual")
+        H = X
     if Q is None:
-        Q = torch.empty(M, K, dtype=torch.uint8, device=dev)
+        Q = torch.empty(shape, dtype=_U8, device=dev)
     if sa is None:
-        sa = torch.empty(K // 128, scale_ld(M), dtype=torch.float32, device=dev)
+        sa = torch.empty(K // 128, scale_ld(M), dtype=_FP32, device=dev)
     if rstd is None:
-        rstd = torch.empty(M, dtype=torch.float32, device=dev)
-    Q = _bytes_view(Q)
-    _rows(Q, "Q", M, K, torch.uint8, dev)
-    _require(sa.dtype == torch.float32 and sa.dim() == 2 and sa.shape[0] == K // 128 and sa.stride(1) == 1
-             and sa.device == dev and sa.shape[1] >= M, "sa must be float32 [K/128, >=M]")
-    _require(rstd.shape == (M,) and rstd.dtype == torch.float32 and rstd.is_contiguous() and rstd.device == dev,
-             "rstd must be contiguous float32 [M]")
+        rstd = torch.empty(M, dtype=_FP32, device=dev)
+    ldq = _matrix(Q, "Q", shape, _FP8 if Q.dtype is _FP8 else _U8, dev)
+    if sa.dtype is not _FP32 or sa.dim() != 2 or sa.shape[0] != K // 128 or sa.shape[1] < M or sa.stride(1) != 1 or sa.device != dev:
+        _refuse(f"sa must be float32 [{K // 128}, >= {M}] on {dev} with a unit inner stride")
     if Y is not None:
-        _rows(Y, "Y", M, K, torch.bfloat16, dev)
+        ldy, y = _matrix(Y, "Y", shape, _BF16, dev), Y.data_ptr()
     st = _fn("fp8_rmsnorm_quantize_1x128")(
-        _ptr(X), _ld(X), _ptr(residual), 0 if residual is None else _ld(residual), code, _ptr(weight), wcode, float(eps),
-        _ptr(H if residual is not None else None), 0 if residual is None else _ld(H), _ptr(Y), 0 if Y is None else _ld(Y),
-        _ptr(rstd), _ptr(Q), _ld(Q), _ptr(sa), _ld(sa), M, K, _stream(dev, stream))
-    _check(st, "fp8_rmsnorm_quantize_1x128")
-    return Q, sa, X if residual is None else H, rstd
+        X.data_ptr(), _ld(X), r, ldr, code, w, _DTYPES[weight.dtype], eps, h, ldh, y, ldy, _vector(rstd, "rstd", M, _FP32, dev),
+        Q.data_ptr(), ldq, sa.data_ptr(), _ld(sa), M, K, _raw_stream(dev, stream))
+    if st:
+        _check(st, "fp8_rmsnorm_quantize_1x128")
+    return Q, sa, H, rstd
 
 
 def rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
@@ -121,36 +144,30 @@ def rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, weig
     gradient of X and of the residual alike, and may be dY or dH itself; dW is float32 [K].
     workspace: optional uint8 buffer, fp8_rmsnorm_backward_workspace_size(M, K) bytes;
     allocated if not given."""
-    _require(dY.device.type == "cuda" and dY.dim() == 2 and dY.stride(1) == 1,
-             "dY must be a 2-D GPU tensor with a unit inner stride")
-    code, dev = _dtype_code(dY, "dY"), dY.device
-    M, K = dY.shape
-    _require(K % 128 == 0, "K must be a multiple of 128")
-    wcode = _dtype_code(weight, "weight")
-    _require(weight.shape == (K,) and weight.device == dev and weight.stride(0) == 1, "weight must be contiguous [K]")
-    _rows(H, "H", M, K, dY.dtype, dev)
-    _require(rstd.shape == (M,) and rstd.dtype == torch.float32 and rstd.is_contiguous() and rstd.device == dev,
-             "rstd must be contiguous float32 [M]")
+    code, M, K = _rows_of(dY, "dY")
+    dev, shape, dt = dY.device, (M, K), dY.dtype
+    w = _vector(weight, "weight", K, weight.dtype if weight.dtype in _DTYPES else _FP32, dev)
+    ldh = _matrix(H, "H", shape, dt, dev)
+    d, ldd = 0, 0
     if dH is not None:
-        _rows(dH, "dH", M, K, dY.dtype, dev)
+        ldd, d = _matrix(dH, "dH", shape, dt, dev), dH.data_ptr()
     if dX is None:
-        dX = torch.empty_like(dY, memory_format=torch.contiguous_format)
-    _rows(dX, "dX", M, K, dY.dtype, dev)
+        dX = torch.empty(shape, dtype=dt, device=dev)
     if dW is None:
-        dW = torch.empty(K, dtype=torch.float32, device=dev)
-    _require(dW.shape == (K,) and dW.dtype == torch.float32 and dW.is_contiguous() and dW.device == dev,
-             "dW must be contiguous float32 [K]")
+        dW = torch.empty(K, dtype=_FP32, device=dev)
     if workspace is None:
         with torch.cuda.device(dev):
-            workspace = torch.empty(_fn("fp8_rmsnorm_backward_workspace_size")(M, K), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(_fn("fp8_rmsnorm_backward_workspace_size")(M, K), dtype=_U8, device=dev)
         if stream is not None:  # used there after this function has let go of it
             workspace.record_stream(stream)
-    _require(workspace.device == dev and workspace.is_contiguous(), "workspace must be contiguous on dY's device")
+    elif workspace.device != dev or not workspace.is_contiguous():
+        _refuse("workspace must be contiguous on dY's device")
     st = _fn("fp8_rmsnorm_backward")(
-        _ptr(dY), _ld(dY), _ptr(H), _ld(H), _ptr(dH), 0 if dH is None else _ld(dH), code, _ptr(rstd), _ptr(weight), wcode,
-        _ptr(dX), _ld(dX), _ptr(dW), M, K, _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(dev, stream))
-    _check(st, "fp8_rmsnorm_backward")
+        dY.data_ptr(), _ld(dY), H.data_ptr(), ldh, d, ldd, code, _vector(rstd, "rstd", M, _FP32, dev), w, _DTYPES[weight.dtype],
+        dX.data_ptr(), _matrix(dX, "dX", shape, dt, dev), _vector(dW, "dW", K, _FP32, dev), M, K, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(dev, stream))
+    if st:
+        _check(st, "fp8_rmsnorm_backward")
     return dX, dW
 
 
@@ -174,33 +191,36 @@ def make_paged_kv_cache(num_pages: int, num_kv_heads: int, page_size: int, head_
     return PagedKVCache(codes[0], scales[0], codes[1], scales[1])
 
 
-def _check_cache(c: PagedKVCache, dev):
-    k, v = _bytes_view(c.k), _bytes_view(c.v)
-    _require(k.dim() == 4 and k.shape == v.shape and k.is_contiguous() and v.is_contiguous(),
-             "cache codes must be contiguous [num_pages, Hkv, page_size, D], keys and values alike")
-    for t in (c.k_scale, c.v_scale):
-        _require(t.dtype == torch.float32 and t.shape == k.shape[:2] and t.is_contiguous(),
-                 "cache scales must be contiguous float32 [num_pages, Hkv]")
-    _require(k.device == dev and v.device == dev and c.k_scale.device == dev and c.v_scale.device == dev,
-             "the cache is on another device")
-    return k, v
+def _cache_shape(c: PagedKVCache, dev):
+    """(num_pages, Hkv, page_size, D) of a cache that must be whole."""
+    k, ks, v, vs = c
+    shape = k.shape
+    if (len(shape) != 4 or v.shape != shape or k.dtype not in (_U8, _FP8) or v.dtype not in (_U8, _FP8) or not k.is_contiguous()
+            or not v.is_contiguous() or k.device != dev or v.device != dev):
+        _refuse(f"cache codes must be contiguous uint8 or float8_e4m3fn [num_pages, Hkv, page_size, D] on {dev}, keys and values alike")
+    if (ks.shape != shape[:2] or vs.shape != shape[:2] or ks.dtype is not _FP32 or vs.dtype is not _FP32 or not ks.is_contiguous()
+            or not vs.is_contiguous() or ks.device != dev or vs.device != dev):
+        _refuse(f"cache scales must be contiguous float32 [num_pages, Hkv] on {dev}")
+    return shape
 
 
 def _heads(t: torch.Tensor, name: str, T: int, H: int, D: int, dev) -> int:
-    """Row stride of a bfloat16 [T, H, D] tensor whose rows are contiguous."""
-    _require(t.dtype == torch.bfloat16 and t.shape == (T, H, D) and t.device == dev
-             and (D == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == D),
-             f"{name} must be bfloat16 [{T}, {H}, {D}] on {dev} with contiguous rows")
+    """Row stride of a tensor that must be bfloat16 [T, H, D] with contiguous rows."""
+    if t.shape != (T, H, D) or t.dtype is not _BF16 or t.device != dev or t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        _refuse(f"{name} must be bfloat16 [{T}, {H}, {D}] on {dev} with contiguous rows")
     return t.stride(0) if T > 1 else H * D
 
 
-def _check_sequences(block_table, seq_lens, cu_q, dev):
-    for t, d, name in ((block_table, 2, "block_table"), (seq_lens, 1, "seq_lens"), (cu_q, 1, "cu_q")):
-        _require(t.dtype == torch.int32 and t.dim() == d and t.device == dev and (t.shape[-1] <= 1 or t.stride(-1) == 1),
-                 f"{name} must be an int32 tensor on {dev} with a unit inner stride")
+def _sequences(block_table, seq_lens, cu_q, dev):
+    """(B, max_pages, row stride of the table)."""
     B = seq_lens.shape[0]
-    _require(block_table.shape[0] == B and cu_q.shape[0] == B + 1, "block_table must be [B, max_pages] and cu_q [B + 1]")
-    return B
+    if (block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype is not _I32 or block_table.device != dev
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+        _refuse(f"block_table must be int32 [{B}, max_pages] on {dev} with a unit inner stride")
+    _vector(seq_lens, "seq_lens", B, _I32, dev)
+    _vector(cu_q, "cu_q", B + 1, _I32, dev)
+    pages = block_table.shape[1]
+    return B, pages, block_table.stride(0) if B > 1 else pages
 
 
 def rope_append_paged_kv(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, cos_sin: Optional[torch.Tensor],
@@ -220,36 +240,37 @@ def rope_append_paged_kv(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Te
     it has to grow, the page's earlier codes are re-encoded. block_table, seq_lens, cu_q:
     see the module's text; seq_lens counts the new tokens."""
     dev = k.device
-    _require(dev.type == "cuda" and k.dim() == 3, "k must be a 3-D GPU tensor")
+    if not k.is_cuda or k.dim() != 3:
+        _refuse("k must be a 3-D GPU tensor")
     T, Hkv, D = k.shape
-    kc, vc = _check_cache(cache, dev)
-    num_pages, P = kc.shape[0], kc.shape[2]
-    _require(kc.shape[1] == Hkv and kc.shape[3] == D, "the cache has other heads than k")
+    num_pages, heads, P, dim = _cache_shape(cache, dev)
+    if heads != Hkv or dim != D:
+        _refuse("the cache has other heads than k")
     ldk, ldv = _heads(k, "k", T, Hkv, D, dev), _heads(v, "v", T, Hkv, D, dev)
-    Hq, ldq, ldqo = Hkv, 0, 0
+    Hq, ldq, ldqo, qp, qop = Hkv, 0, 0, 0, 0
     if q is not None:
-        _require(q.dim() == 3, "q must be [T, Hq, D]")
+        if q.dim() != 3:
+            _refuse("q must be [T, Hq, D]")
         Hq = q.shape[1]
-        ldq = _heads(q, "q", T, Hq, D, dev)
+        ldq, qp = _heads(q, "q", T, Hq, D, dev), q.data_ptr()
         if q_out is None:
-            q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
-        ldqo = _heads(q_out, "q_out", T, Hq, D, dev)
-    else:
-        _require(q_out is None, "q_out without q")
-    max_pos = rot_dim = ld_cs = 0
+            q_out = torch.empty((T, Hq, D), dtype=_BF16, device=dev)
+        ldqo, qop = _heads(q_out, "q_out", T, Hq, D, dev), q_out.data_ptr()
+    elif q_out is not None:
+        _refuse("q_out without q")
+    max_pos = rot_dim = ld_cs = table = 0
     if cos_sin is not None:
-        _require(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.device == dev and cos_sin.stride(1) == 1,
-                 "cos_sin must be float32 [max_pos, rot_dim] with a unit inner stride")
-        (max_pos, rot_dim), ld_cs = cos_sin.shape, _ld(cos_sin)
-    B = _check_sequences(block_table, seq_lens, cu_q, dev)
-    _require(positions is None or (positions.dtype == torch.int32 and positions.shape == (T,) and positions.device == dev
-                                   and positions.is_contiguous()), "positions must be contiguous int32 [T]")
+        if cos_sin.dtype is not _FP32 or cos_sin.dim() != 2 or cos_sin.device != dev or cos_sin.stride(1) != 1:
+            _refuse(f"cos_sin must be float32 [max_pos, rot_dim] on {dev} with a unit inner stride")
+        (max_pos, rot_dim), ld_cs, table = cos_sin.shape, _ld(cos_sin), cos_sin.data_ptr()
+    B, pages, ld_bt = _sequences(block_table, seq_lens, cu_q, dev)
     st = _fn("fp8_rope_append_paged_kv")(
-        _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(cos_sin), ld_cs, max_pos, rot_dim, int(bool(interleaved)),
-        _ptr(positions), _ptr(block_table), _ld(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(cu_q), _ptr(q_out),
-        ldqo, _ptr(kc), _ptr(cache.k_scale), _ptr(vc), _ptr(cache.v_scale), num_pages, P, B, T, Hq, Hkv, D,
-        _stream(dev, stream))
-    _check(st, "fp8_rope_append_paged_kv")
+        qp, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, table, ld_cs, max_pos, rot_dim, 1 if interleaved else 0,
+        0 if positions is None else _vector(positions, "positions", T, _I32, dev), block_table.data_ptr(), ld_bt, pages,
+        seq_lens.data_ptr(), cu_q.data_ptr(), qop, ldqo, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+        cache[3].data_ptr(), num_pages, P, B, T, Hq, Hkv, D, _raw_stream(dev, stream))
+    if st:
+        _check(st, "fp8_rope_append_paged_kv")
     return q_out
 
 
@@ -276,24 +297,30 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Ten
     0 and -inf. workspace: optional (make_attention_workspace), lets sequences be split over
     workgroups; calls that may overlap in time must not share one."""
     dev = q.device
-    _require(dev.type == "cuda" and q.dim() == 3, "q must be a 3-D GPU tensor")
+    if not q.is_cuda or q.dim() != 3:
+        _refuse("q must be a 3-D GPU tensor")
     T, Hq, D = q.shape
-    kc, vc = _check_cache(cache, dev)
-    num_pages, Hkv, P = kc.shape[0], kc.shape[1], kc.shape[2]
-    _require(kc.shape[3] == D and Hkv > 0 and Hq % Hkv == 0, "q's heads do not match the cache's")
+    num_pages, Hkv, P, dim = _cache_shape(cache, dev)
+    if dim != D or Hkv == 0 or Hq % Hkv != 0:
+        _refuse("q's heads do not match the cache's")
     ldq = _heads(q, "q", T, Hq, D, dev)
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, Hq, D), dtype=_BF16, device=dev)
     ldo = _heads(out, "out", T, Hq, D, dev)
-    _require(lse is None or (lse.dtype == torch.float32 and lse.shape == (T, Hq) and lse.is_contiguous()
-                             and lse.device == dev), "lse must be contiguous float32 [T, Hq]")
-    B = _check_sequences(block_table, seq_lens, cu_q, dev)
-    _require(workspace is None or (workspace.device == dev and workspace.is_contiguous()),
-             "workspace must be contiguous on q's device")
+    lp = wp = wbytes = 0
+    if lse is not None:
+        if lse.dtype is not _FP32 or lse.shape != (T, Hq) or not lse.is_contiguous() or lse.device != dev:
+            _refuse(f"lse must be contiguous float32 [{T}, {Hq}] on {dev}")
+        lp = lse.data_ptr()
+    B, pages, ld_bt = _sequences(block_table, seq_lens, cu_q, dev)
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            _refuse("workspace must be contiguous on q's device")
+        wp, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = _fn("fp8_paged_attention")(
-        _ptr(q), ldq, _ptr(kc), _ptr(cache.k_scale), _ptr(vc), _ptr(cache.v_scale), num_pages, P, _ptr(block_table),
-        _ld(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(cu_q), _ptr(out), ldo, _ptr(lse),
-        D ** -0.5 if softmax_scale is None else float(softmax_scale), int(window), B, T, Hq, Hkv, D, _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(dev, stream))
-    _check(st, "fp8_paged_attention")
+        q.data_ptr(), ldq, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), num_pages, P,
+        block_table.data_ptr(), ld_bt, pages, seq_lens.data_ptr(), cu_q.data_ptr(), out.data_ptr(), ldo, lp,
+        D ** -0.5 if softmax_scale is None else softmax_scale, window, B, T, Hq, Hkv, D, wp, wbytes, _raw_stream(dev, stream))
+    if st:
+        _check(st, "fp8_paged_attention")
     return out
