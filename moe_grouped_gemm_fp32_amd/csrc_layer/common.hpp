@@ -13,23 +13,39 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 constexpr float kE4m3Max = 448.0f;
 
-// Eight consecutive elements (BF16 bits or FP32), 16-byte aligned, as FP32.
+// Eight consecutive elements as they are in memory (BF16 bits or FP32), 16-byte aligned.
+template <typename T>
+struct Eight {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* src) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(src)[i];
+  }
+  __device__ __forceinline__ void store(T* dst) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(dst)[i] = v[i];
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+      x[0] = __uint_as_float(v[0].x), x[1] = __uint_as_float(v[0].y), x[2] = __uint_as_float(v[0].z), x[3] = __uint_as_float(v[0].w);
+      x[4] = __uint_as_float(v[1].x), x[5] = __uint_as_float(v[1].y), x[6] = __uint_as_float(v[1].z), x[7] = __uint_as_float(v[1].w);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&x)[8]);
+};
+
 template <typename T>
 __device__ __forceinline__ void load8(const T* src, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 v = *reinterpret_cast<const uint4*>(src);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-    const float4 a = *reinterpret_cast<const float4*>(src);
-    const float4 b = *reinterpret_cast<const float4*>(src + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
+  Eight<T> e;
+  e.load(src);
+  e.get(x);
 }
 
 // Two FP32 values rounded to nearest even BF16, packed.
@@ -37,24 +53,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2bf));
 }
 
+// Rounds eight FP32 values to T.
 template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float (&x)[8]) {
+__device__ __forceinline__ void Eight<T>::set(const float (&x)[8]) {
   if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(dst) =
-        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    v[0] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
   } else {
-    reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    v[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    v[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
   }
 }
 
-// x rounded to T and back: what a T in memory will hold.
 template <typename T>
-__device__ __forceinline__ float rounded(float x) {
-  if constexpr (sizeof(T) == 2)
-    return (float)(__bf16)x;
-  else
-    return x;
+__device__ __forceinline__ void store8(T* dst, const float (&x)[8]) {
+  Eight<T> e;
+  e.set(x);
+  e.store(dst);
 }
 
 // Eight FP32 values to e4m3 codes, round to nearest even.

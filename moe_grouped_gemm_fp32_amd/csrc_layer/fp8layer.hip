@@ -49,17 +49,32 @@ int launched() { return hipGetLastError() == hipSuccess ? FP8GEMM_OK : FP8GEMM_E
 
 constexpr int kMaxNormCols = 65536;
 
-// Waves that share a row and chunks of eight columns a thread: as few waves as keep a row
-// within four chunks a thread, which leaves room for several workgroups on a CU.
+// Waves that share a row, and most chunks of eight columns a thread. Forward: where rows
+// are many, as few waves as keep a row within four chunks a thread (K = 7168: 8 workgroups
+// of 4 waves on a CU); where they would not fill the GPU, one chunk a thread, for latency.
 struct NormShape {
   int waves, chunks;
 };
-NormShape norm_shape(int K) {
+NormShape norm_shape(int M, int K, int cus) {
   const int chunks = K / 8;
+  if (M < 2 * cus) {
+    if (chunks <= 64) return {1, 1};
+    if (chunks <= 4 * 64) return {4, 1};
+    if (chunks <= 16 * 64) return {16, 1};
+  }
   for (int ch : {1, 2, 4})
     if (chunks <= 64 * ch) return {1, ch};
   if (chunks <= 4 * 64 * 4) return {4, 4};
   return {16, chunks <= 16 * 64 * 4 ? 4 : 8};
+}
+// Backward: one chunk a thread up to 16 waves a row.
+NormShape norm_grad_shape(int K) {
+  const int chunks = K / 8;
+  for (int waves : {1, 2, 4, 8})
+    if (chunks <= waves * 64) return {waves, 1};
+  for (int ch : {1, 2, 4})
+    if (chunks <= 16 * 64 * ch) return {16, ch};
+  return {16, 8};
 }
 
 bool norm_dtype(int t) { return t == FP8GEMM_QUANT_BF16 || t == FP8GEMM_QUANT_FP32; }
@@ -68,16 +83,13 @@ bool norm_rows(const void* p, int64_t ld, int K, int dtype) {
   return aligned(p, 16) && ld >= K && ld % (dtype == FP8GEMM_QUANT_BF16 ? 8 : 4) == 0;
 }
 
-// Calls f(T{}, W{}, waves, chunks) with the types and the shape as compile-time values.
+// Calls f(T{}, waves, chunks) with the rows' type and the shape as compile-time values.
 template <int N>
 using Int = std::integral_constant<int, N>;
 template <typename F>
-void with_types(int x_dtype, int w_dtype, F f) {
-  const bool xb = x_dtype == FP8GEMM_QUANT_BF16, wb = w_dtype == FP8GEMM_QUANT_BF16;
-  if (xb && wb) f(uint16_t{}, uint16_t{});
-  else if (xb) f(uint16_t{}, float{});
-  else if (wb) f(float{}, uint16_t{});
-  else f(float{}, float{});
+void with_type(int dtype, F f) {
+  if (dtype == FP8GEMM_QUANT_BF16) f(uint16_t{});
+  else f(float{});
 }
 template <typename F>
 void with_shape(NormShape s, F f) {
@@ -86,17 +98,30 @@ void with_shape(NormShape s, F f) {
     else if (s.chunks == 2) f(Int<1>{}, Int<2>{});
     else f(Int<1>{}, Int<4>{});
   } else if (s.waves == 4) {
-    f(Int<4>{}, Int<4>{});
+    if (s.chunks == 1) f(Int<4>{}, Int<1>{});
+    else f(Int<4>{}, Int<4>{});
+  } else if (s.chunks == 1) {
+    f(Int<16>{}, Int<1>{});
   } else if (s.chunks == 4) {
     f(Int<16>{}, Int<4>{});
   } else {
     f(Int<16>{}, Int<8>{});
   }
 }
+template <typename F>
+void with_grad_shape(NormShape s, F f) {
+  if (s.waves == 1) f(Int<1>{}, Int<1>{});
+  else if (s.waves == 2) f(Int<2>{}, Int<1>{});
+  else if (s.waves == 4) f(Int<4>{}, Int<1>{});
+  else if (s.waves == 8) f(Int<8>{}, Int<1>{});
+  else if (s.chunks == 1) f(Int<16>{}, Int<1>{});
+  else if (s.chunks == 2) f(Int<16>{}, Int<2>{});
+  else if (s.chunks == 4) f(Int<16>{}, Int<4>{});
+  else f(Int<16>{}, Int<8>{});
+}
 
 int norm_grad_groups(int M, NormShape s, int cus) {
-  const int rows = s.waves > 4 ? 1 : 4 / s.waves;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(M, rows), cus * 2));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(M, 16 / s.waves), cus));
 }
 
 // ------------------------------------------------------------------- paged cache, attention
@@ -134,13 +159,12 @@ int fp8_rmsnorm_quantize_1x128(const void* X, int64_t ldx, const void* R, int64_
   const int st = device(&cus);
   if (st != FP8GEMM_OK) return st;
   const fp8layer::NormParams p{X,   R,   w,   H,   Y,   rstd,  static_cast<uint8_t*>(Q), sa, ldx,
-                               ldr, ldh, ldy, ldq, ld_sa, eps, M, K};
-  const NormShape s = norm_shape(K);
-  with_types(x_dtype, w_dtype, [&](auto t, auto u) {
-    with_shape(s, [&](auto waves, auto chunks) {
+                               ldr, ldh, ldy, ldq, ld_sa, eps, M, K, w_dtype == FP8GEMM_QUANT_FP32};
+  with_type(x_dtype, [&](auto t) {
+    with_shape(norm_shape(M, K, cus), [&](auto waves, auto chunks) {
       constexpr int kWaves = decltype(waves)::value;
       constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves;
-      hipLaunchKernelGGL((fp8layer::rmsnorm_quantize_kernel<decltype(t), decltype(u), kWaves, decltype(chunks)::value>),
+      hipLaunchKernelGGL((fp8layer::rmsnorm_quantize_kernel<decltype(t), kWaves, decltype(chunks)::value>),
                          dim3((unsigned)ceil_div(M, kRows)), dim3(kWaves > 4 ? kWaves * 64 : 256), 0, stream, p);
     });
   });
@@ -151,7 +175,7 @@ size_t fp8_rmsnorm_backward_workspace_size(int M, int K) {
   if (M <= 0 || K <= 0 || K % 128 != 0 || K > kMaxNormCols) return 0;
   int cus;  // without a device: the MI355X's own count
   if (device(&cus) != FP8GEMM_OK) cus = 256;
-  return (size_t)norm_grad_groups(M, norm_shape(K), cus) * K * sizeof(float);
+  return (size_t)norm_grad_groups(M, norm_grad_shape(K), cus) * K * sizeof(float);
 }
 
 int fp8_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh, const void* dH, int64_t lddh,
@@ -167,24 +191,23 @@ int fp8_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int64_t ld
   int cus;
   const int st = device(&cus);
   if (st != FP8GEMM_OK) return st;
-  const NormShape s = norm_shape(K);
+  const NormShape s = norm_grad_shape(K);
   const int groups = M > 0 ? norm_grad_groups(M, s, cus) : 0;
   if (groups > 0 && (!workspace || workspace_bytes < (size_t)groups * K * sizeof(float))) return FP8GEMM_ERR_WORKSPACE;
   float* part = static_cast<float*>(workspace);
   if (M > 0) {
-    const fp8layer::NormGradParams p{dY, H, dH, w, rstd, dX, part, lddy, ldh, lddh, lddx, M, K};
-    with_types(dtype, w_dtype, [&](auto t, auto u) {
-      with_shape(s, [&](auto waves, auto chunks) {
-        constexpr int kWaves = decltype(waves)::value;
-        hipLaunchKernelGGL(
-            (fp8layer::rmsnorm_backward_kernel<decltype(t), decltype(u), kWaves, decltype(chunks)::value>), dim3(groups),
-            dim3(kWaves > 4 ? kWaves * 64 : 256), 0, stream, p);
+    const fp8layer::NormGradParams p{dY, H, dH, w, rstd, dX, part, lddy, ldh, lddh, lddx, M, K, w_dtype == FP8GEMM_QUANT_FP32};
+    const size_t merge = (size_t)(16 / s.waves - 1) * K * sizeof(float);  // at most 30 KB
+    with_type(dtype, [&](auto t) {
+      with_grad_shape(s, [&](auto waves, auto chunks) {
+        hipLaunchKernelGGL((fp8layer::rmsnorm_backward_kernel<decltype(t), decltype(waves)::value, decltype(chunks)::value>),
+                           dim3(groups), dim3(1024), merge, stream, p);
       });
     });
     const int rc = launched();
     if (rc != FP8GEMM_OK) return rc;
   }
-  hipLaunchKernelGGL(fp8layer::rmsnorm_weight_grad_kernel, dim3((unsigned)ceil_div(K, 64)), dim3(256), 0, stream, part,
+  hipLaunchKernelGGL(fp8layer::rmsnorm_weight_grad_kernel, dim3((unsigned)(K / 16)), dim3(256), 0, stream, part,
                      groups, K, dW);
   return launched();
 }

@@ -1,16 +1,17 @@
 // Device code of the residual RMS norm with 8-bit output, and of its gradient.
 //
-// A row is held in registers from its one read to its last write. A thread owns chunks of
-// eight consecutive columns, chunk i of thread t at column 8 (t + i * threads), so that a
-// wave reads and writes whole lines and the 16 lanes of one 128-column quantisation block
-// are neighbours. WPR waves share a row.
+// A row is held in registers, as it is in memory, from its one read to its last write. A
+// thread owns chunks of eight consecutive columns, chunk i of thread t at column
+// 8 (t + i * threads), so that a wave reads and writes whole lines and the 16 lanes of one
+// 128-column quantisation block are neighbours. WPR waves share a row, at most CH chunks a
+// thread.
 #pragma once
 
 #include "common.hpp"
 
 namespace fp8layer {
 
-// A row of K columns over WPR waves: at most CH chunks a thread.
+// Sum over a row's waves: `part` has a place for each wave of the workgroup.
 template <int WPR>
 __device__ __forceinline__ float row_sum(float v, float* part, int wave) {
   v = wave_sum(v);
@@ -19,9 +20,15 @@ __device__ __forceinline__ float row_sum(float v, float* part, int wave) {
     __syncthreads();
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < WPR; ++i) v += part[i];
+    for (int i = 0; i < WPR; ++i) v += part[wave / WPR * WPR + i];
   }
   return v;
+}
+
+// Weights are BF16 or FP32, whatever the rows are.
+__device__ __forceinline__ void load_weight(const void* w, int w_fp32, int c, float (&x)[8]) {
+  if (w_fp32) load8(static_cast<const float*>(w) + c * 8, x);
+  else load8(static_cast<const uint16_t*>(w) + c * 8, x);
 }
 
 struct NormParams {
@@ -32,38 +39,65 @@ struct NormParams {
   float* sa;
   int64_t ldx, ldr, ldh, ldy, ldq, ld_sa;
   float eps;
-  int M, K;
+  int M, K, w_fp32;
 };
 
+// y / s for a scale s and r = 1 / s (rounded): one step of Markstein's division, which
+// rounds correctly where r does; three instructions where a division takes ten.
+__device__ __forceinline__ float quotient(float y, float s, float r) {
+  const float q = y * r;
+  return __builtin_fmaf(__builtin_fmaf(-q, s, y), r, q);
+}
+
 // Forward: sum of squares, then y = (h * rstd) * w in FP32, its maximum over the 16 lanes
-// of a block, and the codes by a correctly rounded division (the quantiser's).
-template <typename T, typename W, int WPR, int CH>
+// of a block, and the codes.
+template <typename T, int WPR, int CH>
 __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quantize_kernel(const NormParams p) {
   constexpr int kRows = WPR > 4 ? 1 : 4 / WPR;  // rows of a workgroup
-  __shared__ float part[WPR];
+  __shared__ float part[WPR > 4 ? WPR : 4];
   const int wave = threadIdx.x >> 6;
   const int t = WPR > 1 ? threadIdx.x : threadIdx.x & 63;
   const int row = blockIdx.x * kRows + (WPR > 1 ? 0 : wave);
   if (row >= p.M) return;  // whole rows only: no wave of a shared row leaves
   const T* X = static_cast<const T*>(p.X) + (int64_t)row * p.ldx;
   const int chunks = p.K >> 3;
-  float h[CH][8], w[CH][8];
+  Eight<T> h[CH];
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = t + i * WPR * 64;
-    if (c < chunks) {
-      load8(X + c * 8, h[i]);
-      if (p.R) {
-        float r[8];
-        load8(static_cast<const T*>(p.R) + (int64_t)row * p.ldr + c * 8, r);
+    if (c < chunks) h[i].load(X + c * 8);
+  }
+  if (p.R) {
+    const T* R = static_cast<const T*>(p.R) + (int64_t)row * p.ldr;
+    T* H = static_cast<T*>(p.H) + (int64_t)row * p.ldh;
+    Eight<T> r[CH];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] = rounded<T>(h[i][j] + r[j]);
-        store8(static_cast<T*>(p.H) + (int64_t)row * p.ldh + c * 8, h[i]);
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + i * WPR * 64;
+      if (c < chunks) r[i].load(R + c * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + i * WPR * 64;
+      if (c < chunks) {
+        float a[8], b[8];
+        h[i].get(a);
+        r[i].get(b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] += b[j];
+        h[i].set(a);  // rounded: what is normalised is what is stored
+        h[i].store(H + c * 8);
       }
-      load8(static_cast<const W*>(p.w) + c * 8, w[i]);
+    }
+  }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss += h[i][j] * h[i][j];
+  for (int i = 0; i < CH; ++i) {
+    if (t + i * WPR * 64 < chunks) {
+      float a[8];
+      h[i].get(a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += a[j] * a[j];
     }
   }
   ss = row_sum<WPR>(ss, part, wave);
@@ -73,18 +107,26 @@ __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quantize_ker
   for (int i = 0; i < CH; ++i) {
     const int c = t + i * WPR * 64;
     if (c < chunks) {
-      float y[8], amax = 0.f;
+      float y[8], w[8], amax = 0.f;
+      h[i].get(y);
+      load_weight(p.w, p.w_fp32, c, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        y[j] = h[i][j] * rstd * w[i][j];
+        y[j] = y[j] * rstd * w[j];
         amax = fmaxf(amax, fabsf(y[j]));
       }
       if (p.Y) store8(static_cast<uint16_t*>(p.Y) + (int64_t)row * p.ldy + c * 8, y);
       amax = row_max(amax);
       float s = amax / kE4m3Max;
       if (!(s > 0.f)) s = 1.0f;
+      const float r = 1.0f / s;
+      if (s > 0x1p-100f && s < 0x1p100f) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] /= s;
+        for (int j = 0; j < 8; ++j) y[j] = quotient(y[j], s, r);
+      } else {  // where r, or a product with it, could leave the normal range
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] /= s;
+      }
       *reinterpret_cast<uint2*>(p.Q + (int64_t)row * p.ldq + c * 8) = pack_e4m3(y);
       if ((c & 15) == 0) p.sa[(int64_t)(c >> 4) * p.ld_sa + row] = s;
     }
@@ -97,82 +139,115 @@ struct NormGradParams {
   void* dX;
   float* part;  // [gridDim.x][K]: each workgroup's sums for dW
   int64_t lddy, ldh, lddh, lddx;
-  int M, K;
+  int M, K, w_fp32;
 };
 
-// Backward: each workgroup takes every gridDim.x-th row (WPR == 1: group of four rows) and
-// keeps its columns' part of dW in registers over them.
-template <typename T, typename W, int WPR, int CH>
-__global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_backward_kernel(const NormGradParams p) {
-  constexpr int kRows = WPR > 4 ? 1 : 4 / WPR;
-  __shared__ float part[2][WPR];
-  __shared__ float merge[WPR == 1 ? 3 * CH * 512 : 1];
-  const int wave = threadIdx.x >> 6;
-  const int t = WPR > 1 ? threadIdx.x : threadIdx.x & 63;
+// Backward: workgroups of 16 waves, 16 / WPR rows at a time, one workgroup a CU, so that
+// few hold partial sums of dW (in registers over all rows of the workgroup; 256 parts of
+// 28 KB for 4096 rows of 7168 columns, against 235 MB read and written). The next rows are
+// loaded before the present ones are reduced.
+template <typename T, int WPR, int CH>
+__global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormGradParams p) {
+  constexpr int kRows = 16 / WPR;
+  __shared__ float part[2][16];
+  extern __shared__ float merge[];  // kRows > 1: [kRows - 1][K]
+  const int wave = threadIdx.x >> 6, sub = wave / WPR;  // sub: which of the rows
+  const int t = threadIdx.x & (WPR * 64 - 1);
   const int chunks = p.K >> 3;
+  const int stride = gridDim.x * kRows;
   float w[CH][8], dw[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = t + i * WPR * 64;
-    if (c < chunks) load8(static_cast<const W*>(p.w) + c * 8, w[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f, w[i][j] = 0.f;
+    if (c < chunks) load_weight(p.w, p.w_fp32, c, w[i]);
   }
-  int turn = 0;
-  for (int row = blockIdx.x * kRows + (WPR > 1 ? 0 : wave); row < p.M; row += gridDim.x * kRows, turn ^= 1) {
-    const float rstd = p.rstd[row];
-    float dy[CH][8], xh[CH][8];
-    float dot = 0.f;
+  Eight<T> dy[CH], h[CH], dh[CH];
+  float rstd = 0.f;
+  auto fetch = [&](int row) {
+    if (row >= p.M) return;
+    rstd = p.rstd[row];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = t + i * WPR * 64;
       if (c < chunks) {
-        load8(static_cast<const T*>(p.dY) + (int64_t)row * p.lddy + c * 8, dy[i]);
-        load8(static_cast<const T*>(p.H) + (int64_t)row * p.ldh + c * 8, xh[i]);
+        dy[i].load(static_cast<const T*>(p.dY) + (int64_t)row * p.lddy + c * 8);
+        h[i].load(static_cast<const T*>(p.H) + (int64_t)row * p.ldh + c * 8);
+        if (p.dH) dh[i].load(static_cast<const T*>(p.dH) + (int64_t)row * p.lddh + c * 8);
+      }
+    }
+  };
+  int turn = 0;
+  fetch(blockIdx.x * kRows + sub);
+  // all rows of the workgroup take part in each turn's barrier, also where one is past M
+  for (int first = blockIdx.x * kRows; first < p.M; first += stride, turn ^= 1) {
+    const int row = first + sub;
+    const bool live = row < p.M;
+    Eight<T> dy0[CH], h0[CH], dh0[CH];
+    const float r0 = rstd;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          xh[i][j] *= rstd;
-          dw[i][j] += dy[i][j] * xh[i][j];
-          dy[i][j] *= w[i][j];
-          dot += dy[i][j] * xh[i][j];
+    for (int i = 0; i < CH; ++i) dy0[i] = dy[i], h0[i] = h[i], dh0[i] = dh[i];
+    fetch(row + stride);
+    float dot = 0.f;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        if (t + i * WPR * 64 < chunks) {
+          float g[8], x[8];
+          dy0[i].get(g);
+          h0[i].get(x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[j] *= r0;
+            dw[i][j] += g[j] * x[j];
+            dot += g[j] * w[i][j] * x[j];
+          }
         }
       }
     }
-    // the parts of successive rows alternate, so that one barrier a row is enough
+    // the parts of successive turns alternate, so that one barrier a turn is enough
     dot = row_sum<WPR>(dot, part[turn], wave);
     const float mean = dot / (float)p.K;
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = t + i * WPR * 64;
-      if (c < chunks) {
-        float dx[8];
+      for (int i = 0; i < CH; ++i) {
+        const int c = t + i * WPR * 64;
+        if (c < chunks) {
+          float g[8], x[8];
+          dy0[i].get(g);
+          h0[i].get(x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dx[j] = rstd * (dy[i][j] - xh[i][j] * mean);
-        if (p.dH) {
-          float dh[8];
-          load8(static_cast<const T*>(p.dH) + (int64_t)row * p.lddh + c * 8, dh);
+          for (int j = 0; j < 8; ++j) g[j] = r0 * (g[j] * w[i][j] - x[j] * r0 * mean);
+          if (p.dH) {
+            dh0[i].get(x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dx[j] += dh[j];
+            for (int j = 0; j < 8; ++j) g[j] += x[j];
+          }
+          store8(static_cast<T*>(p.dX) + (int64_t)row * p.lddx + c * 8, g);
         }
-        store8(static_cast<T*>(p.dX) + (int64_t)row * p.lddx + c * 8, dx);
       }
     }
   }
-  if constexpr (WPR == 1) {  // the four waves hold the same columns: add them up in wave 0
-    if (wave > 0) {
+  if constexpr (kRows > 1) {  // the rows' sums, added in their order
 #pragma unroll
-      for (int i = 0; i < CH; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) merge[((wave - 1) * CH * 8 + i * 8 + j) * 64 + t] = dw[i][j];
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + i * WPR * 64;
+      if (sub > 0 && c < chunks) store8(merge + (sub - 1) * p.K + c * 8, dw[i]);
     }
     __syncthreads();
-    if (wave > 0) return;
+    if (sub > 0) return;
+    for (int k = 0; k < kRows - 1; ++k)
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+      for (int i = 0; i < CH; ++i) {
+        const int c = t + i * WPR * 64;
+        if (c < chunks) {
+          float x[8];
+          load8(merge + k * p.K + c * 8, x);
 #pragma unroll
-      for (int i = 0; i < CH; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[i][j] += merge[(k * CH * 8 + i * 8 + j) * 64 + t];
+          for (int j = 0; j < 8; ++j) dw[i][j] += x[j];
+        }
+      }
   }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
@@ -181,28 +256,27 @@ __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_backward_ker
   }
 }
 
-// dW[k] = sum of the workgroups' parts, in a fixed order: 16 column quads by 16 slices of
+// dW[k] = sum of the workgroups' parts, in a fixed order: four column quads by 64 slices of
 // the parts a workgroup.
 __global__ void __launch_bounds__(256) rmsnorm_weight_grad_kernel(const float* __restrict__ part, int parts, int K,
                                                                   float* __restrict__ dW) {
-  __shared__ float4 slice[16][16];
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-  const int k = (blockIdx.x * 16 + x) * 4;
+  __shared__ float4 slice[64][4];
+  const int x = threadIdx.x & 3, y = threadIdx.x >> 2;
+  const int k = (blockIdx.x * 4 + x) * 4;  // K is a multiple of 16
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (k < K) {
-    for (int g = y; g < parts; g += 16) {
-      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)g * K + k);
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-    }
+#pragma unroll 4
+  for (int g = y; g < parts; g += 64) {
+    const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)g * K + k);
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
   }
   slice[y][x] = s;
   __syncthreads();
-  if (y == 0 && k < K) {
-    for (int i = 1; i < 16; ++i) {
-      const float4 v = slice[i][x];
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-    }
-    dW[k] = s.x, dW[k + 1] = s.y, dW[k + 2] = s.z, dW[k + 3] = s.w;
+  if (threadIdx.x < 16) {  // one column each
+    const float* column = reinterpret_cast<const float*>(slice) + threadIdx.x;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) sum += column[i * 16];
+    dW[blockIdx.x * 16 + threadIdx.x] = sum;
   }
 }
 
