@@ -242,10 +242,12 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
   // page on either side for each sequence that has any.
   const int64_t pages = std::min<int64_t>(T, ceil_div(T, P) + 2 * (int64_t)std::min(B, T));
   const int64_t units = pages * Hkv * 2;
-  // A wave for each unit where units hold a token or two (decoding); four waves otherwise.
-  const bool small = T <= 2 * (int64_t)B;
+  // A wave for each unit where a unit is a token or two (decoding) or a small page; four
+  // otherwise.
+  const bool small = T <= 2 * (int64_t)B || P * D <= 2048;
   const int64_t unit_groups = small ? ceil_div(units, 4) : units;
-  const int64_t q_groups = q ? ceil_div((int64_t)T * Hq * (D / 16), 256) : 0;
+  const int group_tokens = (int)std::max<int64_t>(1, T / ((int64_t)cus * 8));
+  const int64_t q_groups = q ? ceil_div(T, group_tokens) : 0;
   if (unit_groups + q_groups > INT32_MAX) return FP8GEMM_ERR_SHAPE;
   const fp8layer::AppendParams p{static_cast<const uint16_t*>(q),
                                  static_cast<const uint16_t*>(k),
@@ -276,7 +278,8 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
                                  T,
                                  Hq,
                                  Hkv,
-                                 (int)unit_groups};
+                                 (int)unit_groups,
+                                 group_tokens};
   const dim3 grid((unsigned)(unit_groups + q_groups));
   auto go = [&](auto d) {
     constexpr int kD = decltype(d)::value;

@@ -1,11 +1,12 @@
 // Device code of the append to the paged 8-bit cache, with the rotation on the way.
 //
-// Work is divided by what shares a scale: one unit is one page, one head, keys or values.
-// A unit reads its new tokens twice (from L2 the second time): once for their largest
-// magnitude, which settles the page's scale, and once to encode them. So a page's scale
-// and codes have one writer, and the result does not depend on any order. WAVES waves
-// share a unit. The queries' rotation, which no unit waits for, fills further workgroups
-// of the same launch.
+// Work is divided by what shares a scale: one unit is one page, one head, keys or values,
+// shared by WAVES waves. The largest magnitude of its new tokens settles the page's scale,
+// then they are encoded: a thread holds its first kHeld groups of columns in between (a
+// whole page up to 8192 columns over four waves, or 2048 over one) and reads further ones
+// again. So a page's scale and codes have one writer, and the result does not depend on
+// any order. The queries' rotation, which no unit waits for, fills further workgroups of
+// the same launch.
 //
 // A thread handles two groups of eight columns at a time: of a rotated head, the first
 // and second members of eight pairs; of other columns, 16 in a row.
@@ -25,8 +26,11 @@ struct AppendParams {
   int64_t ldq, ldk, ldv, ld_cs, ld_bt, ldqo;
   int max_pos, rot_dim, interleaved, max_pages, num_pages, log_p;
   int B, T, Hq, Hkv;
-  int unit_groups;  // workgroups that hold units; the later ones rotate queries
+  int unit_groups;   // workgroups that hold units; the later ones rotate queries,
+  int group_tokens;  // of so many tokens each
 };
+
+constexpr int kHeld = 2;
 
 // Bits of the smallest power of two, 2^-126 at least, by which amax fits 448 = 1.75 * 2^8.
 __device__ __forceinline__ uint32_t fit_scale_bits(float amax) {
@@ -93,30 +97,32 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
   const int P = 1 << p.log_p;
   const int max_len = p.max_pages << p.log_p;
 
-  if ((int)blockIdx.x >= p.unit_groups) {  // queries
-    const int64_t n = (int64_t)(blockIdx.x - p.unit_groups) * 256 + threadIdx.x;
-    const int i = (int)(n % kItems);
-    const int64_t th = n / kItems;
-    const int h = (int)(th % p.Hq);
-    if (th / p.Hq >= p.T) return;
-    const int t = (int)(th / p.Hq);
-    // the token's sequence: the last with cu_q[b] <= t
-    int b = 0, end = p.B;
-    while (end - b > 1) {
-      const int mid = (b + end) >> 1;
-      if (p.cu_q[mid] <= t) b = mid;
-      else end = mid;
+  if ((int)blockIdx.x >= p.unit_groups) {  // queries: a thread has item n % kItems of every so many heads
+    const int t0 = ((int)blockIdx.x - p.unit_groups) * p.group_tokens, t1 = min(p.T, t0 + p.group_tokens);
+    Sequence sq{};
+    for (int t = t0; t < t1; ++t) {
+      if (t == t0 || t >= sq.row0 + sq.rows) {  // the token's sequence: the last with cu_q[b] <= t
+        int b = -1;
+        for (int base = 0; base < p.B; base += 64) {
+          const int n = __popcll(__ballot(base + lane < p.B && p.cu_q[min(base + lane, p.B - 1)] <= t));
+          b += n;
+          if (n < 64) break;
+        }
+        sq = sequence(p.cu_q, p.seq_lens, max(b, 0), p.T, max_len);
+        if (t >= sq.row0 + sq.rows) return;  // past the last sequence
+      }
+      const int at = p.positions ? p.positions[t] : sq.len - (sq.row0 + sq.rows - t);
+      const float* cs = p.cos_sin + min(max(at, 0), p.max_pos - 1) * p.ld_cs;
+      for (int n = threadIdx.x; n < p.Hq * kItems; n += 256) {
+        const int i = n % kItems, h = n / kItems;
+        const Item it = item_of(i, p.rot_dim, p.interleaved);
+        float a[8], c[8];
+        load_item(p.q + t * p.ldq + h * D, cs, it, i, p.rot_dim, p.interleaved, a, c);
+        uint16_t* dst = p.q_out + t * p.ldqo + h * D;
+        store8(dst + it.lo, a);
+        store8(dst + it.hi, c);
+      }
     }
-    const Sequence sq = sequence(p.cu_q, p.seq_lens, b, p.T, max_len);
-    if (t >= sq.row0 + sq.rows) return;  // past the last sequence
-    const int at = p.positions ? p.positions[t] : sq.len - (sq.row0 + sq.rows - t);
-    const int pos = min(max(at, 0), p.max_pos - 1);
-    const Item it = item_of(i, p.rot_dim, p.interleaved);
-    float a[8], c[8];
-    load_item(p.q + t * p.ldq + h * D, p.cos_sin + pos * p.ld_cs, it, i, p.rot_dim, p.interleaved, a, c);
-    uint16_t* dst = p.q_out + t * p.ldqo + h * D;
-    store8(dst + it.lo, a);
-    store8(dst + it.hi, c);
     return;
   }
 
@@ -176,16 +182,27 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
     load_item(src + row * ld + h * D, p.cos_sin + pos * p.ld_cs, it, i, rot, p.interleaved, a, b);
   };
 
+  float held_a[kHeld][8], held_b[kHeld][8];
   float amax = 0.f;
-  for (int s = from + t / kItems; s < to; s += kTokens) {
-    float a[8], b[8];
-    fetch(s, a, b);
+  auto measure = [&](const float(&a)[8], const float(&b)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = fabsf(a[j]), y = fabsf(b[j]);
       amax = fmaxf(amax, x < INFINITY ? x : 0.f);
       amax = fmaxf(amax, y < INFINITY ? y : 0.f);
     }
+  };
+  const int s0 = from + t / kItems;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (s0 + k * kTokens < to) {
+      fetch(s0 + k * kTokens, held_a[k], held_b[k]);
+      measure(held_a[k], held_b[k]);
+    }
+  for (int s = s0 + kHeld * kTokens; s < to; s += kTokens) {
+    float a[8], b[8];
+    fetch(s, a, b);
+    measure(a, b);
   }
   amax = wave_max(amax);
   if constexpr (WAVES == 4) {
@@ -218,13 +235,19 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
       *at = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
   }
-  for (int s = from + t / kItems; s < to; s += kTokens) {
-    float a[8], b[8];
-    fetch(s, a, b);
+  auto put = [&](int s, float(&a)[8], float(&b)[8]) {
     encode(a, inv);
     encode(b, inv);
     *reinterpret_cast<uint2*>(codes + s * D + it.lo) = pack_e4m3(a);
     *reinterpret_cast<uint2*>(codes + s * D + it.hi) = pack_e4m3(b);
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (s0 + k * kTokens < to) put(s0 + k * kTokens, held_a[k], held_b[k]);
+  for (int s = s0 + kHeld * kTokens; s < to; s += kTokens) {
+    float a[8], b[8];
+    fetch(s, a, b);
+    put(s, a, b);
   }
 }
 
