@@ -215,12 +215,6 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t off, u
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
-__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
-  const uint64_t v = (uint64_t)(uintptr_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return (const uint8_t*)(uintptr_t)((uint64_t)hi << 32 | lo);
-}
-
 // One stage of a wave's ring: 32 keys in the order their lanes feed them ([16-key group]
 // [64-byte piece][lane][16 bytes]), then 32 values, row after row.
 template <int D, bool STREAM>
@@ -505,34 +499,39 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) o[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
   }
-  int e0 = -1, e1 = -1;  // the groups' value scales (exponent fields) that these belong to
 
   const int steps = (u.k1 - u.k0 + 31) >> 5, share = (steps + 3) >> 2;
   const int step0 = min(steps, wave * share), step1 = min(steps, step0 + share);
   for (int seg = step0; seg < step1; seg += 32) {
-    // lane i holds what group i (16 keys) of the next 64 needs: its page and scales
-    int page = -1;
-    float ks = 0.f, vs = 0.f;
+    // lane i holds what group i (16 keys) of the next 64 needs: where its rows start in the
+    // caches, the factor of its logits, and the base 2 logarithm of its value scale
+    uint32_t at_lo = 0, at_hi = 0;
+    float c_lane = 0.f, v_lane = 0.f;
+    bool there = false;
     {
       const int key = u.k0 + seg * 32 + lane * 16;
       if (key < u.k1) {
-        page = p.block_table[u.b * p.ld_bt + (key >> p.log_p)];
-        if (page >= 0 && page < p.num_pages) {
-          ks = __uint_as_float(__float_as_uint(p.k_scale[(int64_t)page * p.Hkv + u.h]) & 0x7F800000u) * p.scale_log2;
-          vs = p.v_scale[(int64_t)page * p.Hkv + u.h];
-        } else {
-          page = -1;
+        const int page = p.block_table[u.b * p.ld_bt + (key >> p.log_p)];
+        there = page >= 0 && page < p.num_pages;
+        if (there) {  // page 0 stands in for none
+          const int64_t head = (int64_t)page * p.Hkv + u.h;
+          const uint64_t at = (uint64_t)((head << p.log_p) + (key & ((1 << p.log_p) - 1))) * D;
+          at_lo = (uint32_t)at, at_hi = (uint32_t)(at >> 32);
+          c_lane = __uint_as_float(__float_as_uint(p.k_scale[head]) & 0x7F800000u) * p.scale_log2;
+          v_lane = (float)(exponent(__float_as_uint(p.v_scale[head])) - 127);
         }
       }
     }
+    const uint64_t holes = ~__ballot(there);  // groups without a page
+    const float v_before = __shfl(v_lane, max(lane - 2, 0), 64);
+    const uint64_t changes = __ballot(lane < 2 || v_lane != v_before);  // another value scale than two groups before
     const int count = min(32, step1 - seg);
     const uint8_t* ring = shared + wave * 2 * Ring::kBytes;
     const uint32_t ring_lds = __builtin_amdgcn_readfirstlane(lds_address(ring));
-    // first byte of the rows of 16-key group g of this segment (page 0 stands in for none)
+    auto of_lane = [&](float v, int g) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), g)); };
     auto rows_of = [&](const uint8_t* cache, int g) {
-      const int at = (u.k0 + seg * 32 + 16 * g) & ((1 << p.log_p) - 1);
-      const int pg = max(__builtin_amdgcn_readlane(page, g), 0);
-      return uniform(cache + (((((int64_t)pg * p.Hkv + u.h) << p.log_p) + at) * D));
+      const uint32_t lo = __builtin_amdgcn_readlane(at_lo, g), hi = __builtin_amdgcn_readlane(at_hi, g);
+      return cache + ((uint64_t)hi << 32 | lo);
     };
     auto fetch_keys = [&](int s) {
       Ring::load_keys(rows_of(p.k_cache, 2 * s), rows_of(p.k_cache, 2 * s + 1), ring_lds + (s & 1) * Ring::kBytes, lane);
@@ -551,11 +550,9 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
       const int left = count - 1 - s;  // steps after this one
       const uint8_t* stage = ring + (s & 1) * Ring::kBytes;
       const int key = u.k0 + (seg + s) * 32;
-      const int pg0 = __builtin_amdgcn_readlane(page, 2 * s), pg1 = __builtin_amdgcn_readlane(page, 2 * s + 1);
-      float c0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 2 * s));
-      float c1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 2 * s + 1));
-      const int now0 = exponent(__builtin_amdgcn_readlane(__float_as_uint(vs), 2 * s));
-      const int now1 = exponent(__builtin_amdgcn_readlane(__float_as_uint(vs), 2 * s + 1));
+      float c0 = of_lane(c_lane, 2 * s), c1 = of_lane(c_lane, 2 * s + 1);
+      const float v0 = of_lane(v_lane, 2 * s), v1 = of_lane(v_lane, 2 * s + 1);
+      const uint32_t hole = (uint32_t)(holes >> (2 * s)) & 3;
 
       v4f s0[R], s1[R];
 #pragma unroll
@@ -595,11 +592,11 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
       uint32_t nan_keys = 0;
       bool any_nan = false;
       // some row does not see all of the step
-      if (rarely(key < all_lo || key + 32 > all_hi || pg0 < 0 || pg1 < 0)) {
+      if (rarely(key < all_lo || key + 32 > all_hi || hole != 0)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int at = key + (j >> 2) * 16 + kg * 4 + (j & 3);
-          const bool there = (j < 4 ? pg0 : pg1) >= 0;
+          const bool there = (hole >> (j >> 2) & 1) == 0;
           // values that no row sees may be anything: they count as 0. Where a row sees a
           // NaN code and another does not, the product gets 0 and the rows that see it NaN
           // by their probability.
@@ -627,13 +624,12 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int at = key + (j >> 2) * 16 + kg * 4 + (j & 3);
-            const bool seen = (j < 4 ? pg0 : pg1) >= 0 && at >= key_lo[i] && at < key_hi[i];
+            const bool seen = (hole >> (j >> 2) & 1) == 0 && at >= key_lo[i] && at < key_hi[i];
             if (j < 4) s0[i][j] = seen ? s0[i][j] * c0 : -INFINITY;  // factors may be 0: they come before the mask
             else s1[i][j - 4] = seen ? s1[i][j - 4] * c1 : -INFINITY;
           }
         c0 = c1 = 1.f;
       }
-      const float v0 = (float)(now0 - 127), v1 = (float)(now1 - 127);
       float top[R], top_o[R];
       bool move = false;
 #pragma unroll
@@ -655,8 +651,7 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
           for (int t2 = 0; t2 < kTiles; ++t2) o[i][t2] *= b;
         }
       }
-      if (rarely(moved || now0 != e0 || now1 != e1)) {
-        e0 = now0, e1 = now1;
+      if (rarely(moved || (changes >> (2 * s) & 3) != 0)) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           a0[i] = fmaxf(v0 + (15 - kLag) - mo[i], kFar - m[i]), k0[i] = exp2_of(-(a0[i] + m[i]));
