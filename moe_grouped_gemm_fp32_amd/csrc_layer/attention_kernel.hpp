@@ -279,7 +279,8 @@ __device__ __forceinline__ float pow2(int e) {
 }
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
-__device__ __forceinline__ bool any_nan_code(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
+// Not 0 if one of the four codes is NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 // Partial results travel between workgroups (of any XCD) as device-coherent accesses.
 constexpr int kDeviceScope = 16;        // buffer cache policy sc1
@@ -434,11 +435,11 @@ __device__ __forceinline__ v8h weights(const v4f& s0, const v4f& s1, float c0, f
   for (int j = 0; j < 8; ++j) out[j] = (_Float16)w[j];
   return out;
 }
-// Maxima as chains: the compiler makes maxima of three of them, and of a chain only the first
-// two operands cost an instruction to quiet. (Not as inline assembly: the waits between a
-// matrix instruction and a reader of its result are the compiler's to insert, and it does
-// not for assembly.)
-__device__ __forceinline__ float max4(const v4f& s) { return fmaxf(fmaxf(fmaxf(s[0], s[1]), s[2]), s[3]); }
+// A maximum as a chain from a constant: the compiler makes it of maxima of three, and of a
+// chain only its first operands, if they could be signalling NaN, cost an instruction to
+// quiet. (Not as inline assembly: the waits between a matrix instruction and a reader of
+// its result are the compiler's to insert, and it does not for assembly.)
+__device__ __forceinline__ float max4(const v4f& s) { return fmaxf(fmaxf(fmaxf(fmaxf(kNone, s[0]), s[1]), s[2]), s[3]); }
 __device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); }
 
 // Workgroups that registers leave room for on a CU.
@@ -600,19 +601,14 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
           // values that no row sees may be anything: they count as 0. Where a row sees a
           // NaN code and another does not, the product gets 0 and the rows that see it NaN
           // by their probability.
-          if (!there || at < u.lo || at >= u.hi) {
+          const bool some_see = there && at >= u.lo && at < u.hi;
+          uint32_t bad = 0;
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) v[j][w] = 0;
-          } else {
-            bool bad = false;
+          for (int w = 0; w < kWords; ++w) bad |= nan_codes(v[j][w]);
+          nan_keys |= some_see && bad != 0 ? 1u << j : 0u;
+          const uint32_t keep = some_see && bad == 0 ? ~0u : 0u;  // without branches: in place
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) bad |= any_nan_code(v[j][w]);
-            if (bad) {
-              nan_keys |= 1u << j;
-#pragma unroll
-              for (int w = 0; w < kWords; ++w) v[j][w] = 0;
-            }
-          }
+          for (int w = 0; w < kWords; ++w) v[j][w] &= keep;
         }
         any_nan = __any(nan_keys != 0);
         if (rarely(any_nan)) {  // over the 16 lanes that feed the same keys
@@ -663,9 +659,11 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
       for (int i = 0; i < R; ++i) {
         pf[i] = weights(s0[i], s1[i], c0, c1, a0[i], a1[i], k0[i], k1[i], l[i]);
         if (rarely(any_nan)) {
+          uint32_t bits = nan_keys;
+          asm("" : "+v"(bits));  // keeps the tests of its bits on this side of the branch
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if ((nan_keys >> j & 1) && (j < 4 ? s0[i][j] : s1[i][j - 4]) > -INFINITY) pf[i][j] = (_Float16)__builtin_nanf("");
+            if ((bits >> j & 1) && (j < 4 ? s0[i][j] : s1[i][j - 4]) > -INFINITY) pf[i][j] = (_Float16)__builtin_nanf("");
         }
       }
 #pragma unroll
