@@ -443,7 +443,7 @@ __device__ __forceinline__ float max4(const v4f& s) { return fmaxf(fmaxf(fmaxf(f
 __device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); }
 
 // Workgroups that registers leave room for on a CU.
-constexpr int attention_residents(int D, int R) { return D == 64 ? (R == 1 ? 4 : 3) : D == 128 ? 2 : 1; }
+constexpr int attention_residents(int D, int R) { return D == 64 ? (R == 1 ? 4 : R == 2 ? 3 : 2) : D == 128 ? 2 : 1; }
 
 // STREAM: no other unit reads this one's keys and values. The hint is worth 11% then (64
 // users of 8192 keys: 202 us without, 180 with, 5.99 TB/s) and costs 4% where many tiles
@@ -454,12 +454,12 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
   constexpr int kWords = D / 64;       // 32-bit words of one value a lane feeds
   constexpr int kTiles = D / 16;       // 16-column tiles of V
   constexpr int kStride = D + 4;       // of a row of O in LDS
-  // the ring, and after the loop the waves' results
-  constexpr int kRingBytes = 4 * 2 * Ring::kBytes, kResultBytes = 4 * 16 * R * kStride * 4;
+  // the ring, and after the loop the waves' results, 16 rows at a time
+  constexpr int kRingBytes = 4 * 2 * Ring::kBytes, kResultBytes = 4 * 16 * kStride * 4;
   __shared__ __align__(16) uint8_t shared[kRingBytes > kResultBytes ? kRingBytes : kResultBytes];
-  __shared__ float m_sh[4][16 * R], mo_sh[4][16 * R], l_sh[4][16 * R];
+  __shared__ float m_sh[4][16], mo_sh[4][16], l_sh[4][16];
   __shared__ int flag;
-  auto o_sh = reinterpret_cast<float(*)[16 * R][kStride]>(shared);
+  auto o_sh = reinterpret_cast<float(*)[16][kStride]>(shared);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, kg = lane >> 4;
   Plan<16 * R, 32> plan;
@@ -685,27 +685,23 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
     }
   }
 
-  __syncthreads();  // the ring becomes the waves' results
-  // join the four waves: row n + 16 i's column (4 kg + j) (D / 16) + t is o[i][t][j]
+  // join the four waves: row n + 16 i's column (4 kg + j) (D / 16) + t is o[i][t][j]; then
+  // thread (r, x) has rows r + 16 i, columns x D / 16 .. + D / 16
+  RowPart<kTiles> part[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     l[i] += __shfl_xor(l[i], 16, 64);
     l[i] += __shfl_xor(l[i], 32, 64);
+    __syncthreads();  // the ring, or the rows before, have been read
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int t = 0; t < kTiles; t += 4)
-        *reinterpret_cast<float4*>(&o_sh[wave][n + 16 * i][(4 * kg + j) * kTiles + t]) =
+        *reinterpret_cast<float4*>(&o_sh[wave][n][(4 * kg + j) * kTiles + t]) =
             make_float4(o[i][t][j], o[i][t + 1][j], o[i][t + 2][j], o[i][t + 3][j]);
-    if (kg == 0) m_sh[wave][n + 16 * i] = m[i], mo_sh[wave][n + 16 * i] = mo[i], l_sh[wave][n + 16 * i] = l[i];
-  }
-  __syncthreads();
-
-  // thread (r, x): rows r + 16 i, columns x D / 16 .. + D / 16
-  RowPart<kTiles> part[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int r = (threadIdx.x >> 4) + 16 * i, x = threadIdx.x & 15;
+    if (kg == 0) m_sh[wave][n] = m[i], mo_sh[wave][n] = mo[i], l_sh[wave][n] = l[i];
+    __syncthreads();
+    const int r = threadIdx.x >> 4, x = threadIdx.x & 15;
     float top = kNone, top_o = kNone, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) top = fmaxf(top, m_sh[w][r]), top_o = fmaxf(top_o, mo_sh[w][r]);

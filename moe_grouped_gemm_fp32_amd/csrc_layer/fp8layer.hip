@@ -136,6 +136,19 @@ int log2_of(int P) {
   return n;
 }
 
+// Blocks of 16 rows in a tile. One or two where that holds a sequence's rows; otherwise two,
+// or the most that registers allow if that takes less time by the padded rows (a row of a
+// larger tile costs kLargeTile of one of two blocks: 2048 prompt tokens over 8192 keys,
+// 8 key heads: D = 64 606 and 657 TFLOP/s, 128 763 and 851, 256 646 and 711) and if the
+// tiles are enough to give every CU one (2 x 95 tokens by 16 heads of 64: 13.5 and 18.4 us).
+constexpr int most_row_blocks(int D) { return D == 64 ? 4 : 3; }
+constexpr double kLargeTile = 0.9;
+int attention_row_blocks(int64_t rows, int64_t heads, int D, int cus) {
+  if (rows <= 32) return rows <= 16 ? 1 : 2;
+  const int64_t most = 16 * most_row_blocks(D), tiles = ceil_div(rows, most);
+  return tiles * most * kLargeTile < ceil_div(rows, 32) * 32 && tiles * heads >= cus ? most_row_blocks(D) : 2;
+}
+
 constexpr size_t kAttentionCounterBytes = fp8layer::kCounters * sizeof(int32_t);
 constexpr size_t kAttentionPartBytes = (size_t)64 << 20;
 
@@ -342,19 +355,17 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
   p.num_pages = num_pages;
   p.log_p = log2_of(P);
   p.max_pages = max_pages;
-  // Rows that share a key head, on average over the sequences: sixteen a tile if there are
-  // no more, 32 otherwise (registers allow 16 where heads are 256 wide). Up to one tile, the
-  // tile is the only reader of its keys and values.
-  const int64_t rows = ceil_div((int64_t)T * p.group, B);
-  const int tile = rows <= 16 || D == 256 ? 16 : 32;
-  const bool stream_kv = rows <= tile;
+  const int64_t rows = ceil_div((int64_t)T * p.group, B);  // that share a key head, on average
+  const int blocks = attention_row_blocks(rows, (int64_t)B * Hkv, D, cus);
+  const int tile = 16 * blocks;
+  const bool stream_kv = rows <= tile;  // the tile is the only reader of its keys and values
   // Most row tiles, times heads. Splitting adds units up to a number that gives every CU
   // a few: that many are wanted, and the workspace has a slot for each unit.
   const int64_t tiles = (std::min(B, T) + (int64_t)T * p.group / tile) * Hkv;
   const size_t slot = (size_t)tile * (D + 1) * sizeof(float);
   const size_t bytes = std::min<size_t>(workspace ? workspace_bytes : 0, (size_t)1 << 30);
   const int64_t slots = bytes > kAttentionCounterBytes ? (int64_t)((bytes - kAttentionCounterBytes) / slot) : 0;
-  p.residents = cus * fp8layer::attention_residents(D, tile / 16);
+  p.residents = cus * fp8layer::attention_residents(D, blocks);
   // Units that splitting may add: as many as are resident where the longest sequences that
   // the table allows make one round of work, four times that otherwise (workgroups
   // without a unit end at once, but they cost a microsecond a round).
@@ -372,14 +383,11 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
   auto go = [&](auto d) {
     constexpr int kD = decltype(d)::value;
     const dim3 groups((unsigned)grid);
-    if constexpr (kD == 256) {
-      if (stream_kv) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true>), groups, dim3(256), 0, stream, p);
-      else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, false>), groups, dim3(256), 0, stream, p);
-    } else {
-      if (tile == 16) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true>), groups, dim3(256), 0, stream, p);
-      else if (stream_kv) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, true>), groups, dim3(256), 0, stream, p);
-      else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, false>), groups, dim3(256), 0, stream, p);
-    }
+    constexpr int kMost = most_row_blocks(kD);
+    if (blocks == 1) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true>), groups, dim3(256), 0, stream, p);
+    else if (stream_kv) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, true>), groups, dim3(256), 0, stream, p);
+    else if (blocks == 2) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, false>), groups, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, kMost, false>), groups, dim3(256), 0, stream, p);
   };
   if (D == 64) go(Int<64>{});
   else if (D == 128) go(Int<128>{});
