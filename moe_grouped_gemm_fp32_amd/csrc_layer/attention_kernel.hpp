@@ -307,49 +307,63 @@ struct RowPart {
   float lse2;
 };
 
-// Joins n parts of a row, `stride` bytes apart from `at` (columns) and `lse_at` (log sum).
-template <int C>
-__device__ __forceinline__ void join_parts(RowPart<C>& r, __amdgpu_buffer_rsrc_t rs, int at, int lse_at, int stride, int n) {
-  float top = -INFINITY, sum = 0.f;
+// Joins n parts of R rows, `stride` bytes apart from at[i] (columns) and lse_at[i] (log
+// sum): the loads of as many parts as registers hold are in flight together.
+template <int R, int C>
+__device__ __forceinline__ void join_parts(RowPart<C> (&r)[R], __amdgpu_buffer_rsrc_t rs, const int (&at)[R], const int (&lse_at)[R],
+                                           int stride, int n) {
+  constexpr int kBatch = R * C <= 16 ? kJoin : kJoin / 2;
+  float top[R], sum[R];
 #pragma unroll
-  for (int t = 0; t < C; ++t) r.out[t] = 0.f;
-  for (int base = 0; base < n; base += kJoin) {
-    float w[kJoin];
-    v4f y[kJoin][C / 4];
+  for (int i = 0; i < R; ++i) {
+    top[i] = -INFINITY, sum[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < kJoin; ++c) {
+    for (int t = 0; t < C; ++t) r[i].out[t] = 0.f;
+  }
+  for (int base = 0; base < n; base += kBatch) {
+    float w[R][kBatch];
+    v4f y[R][kBatch][C / 4];
+#pragma unroll
+    for (int c = 0; c < kBatch; ++c) {
       const int off = min(base + c, n - 1) * stride;
-      w[c] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, off + lse_at, 0, kDeviceScope));
 #pragma unroll
-      for (int t = 0; t < C / 4; ++t)
-        y[c][t] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off + at + t * 16, 0, kDeviceScope));
-    }
-    float most = top;
+      for (int i = 0; i < R; ++i) {
+        w[i][c] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, off + lse_at[i], 0, kDeviceScope));
 #pragma unroll
-    for (int c = 0; c < kJoin; ++c) {
-      if (base + c >= n) w[c] = -INFINITY;
-      most = fmaxf(most, w[c]);
-    }
-    const float ref = most > -INFINITY ? most : 0.f;  // rows that have seen nothing stay at weight 0
-    const float a = exp2_of(top - ref);
-    sum *= a;
-#pragma unroll
-    for (int t = 0; t < C; ++t) r.out[t] *= a;
-#pragma unroll
-    for (int c = 0; c < kJoin; ++c) {
-      const float b = exp2_of(w[c] - ref);
-      if (base + c < n) {
-        sum += b;
-#pragma unroll
-        for (int t = 0; t < C; ++t) r.out[t] += b * y[c][t / 4][t % 4];
+        for (int t = 0; t < C / 4; ++t)
+          y[i][c][t] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, off + at[i] + t * 16, 0, kDeviceScope));
       }
     }
-    top = most;
-  }
-  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
-  for (int t = 0; t < C; ++t) r.out[t] *= inv;
-  r.lse2 = sum == 0.f ? -INFINITY : top + __log2f(sum);
+    for (int i = 0; i < R; ++i) {
+      float most = top[i];
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        if (base + c >= n) w[i][c] = -INFINITY;
+        most = fmaxf(most, w[i][c]);
+      }
+      const float ref = most > -INFINITY ? most : 0.f;  // rows that have seen nothing stay at weight 0
+      const float a = exp2_of(top[i] - ref);
+      sum[i] *= a;
+#pragma unroll
+      for (int t = 0; t < C; ++t) r[i].out[t] *= a;
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        const float b = base + c < n ? exp2_of(w[i][c] - ref) : 0.f;
+        sum[i] += b;
+#pragma unroll
+        for (int t = 0; t < C; ++t) r[i].out[t] += base + c < n ? b * y[i][c][t / 4][t % 4] : 0.f;
+      }
+      top[i] = most;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const float inv = sum[i] == 0.f ? 0.f : 1.0f / sum[i];
+#pragma unroll
+    for (int t = 0; t < C; ++t) r[i].out[t] *= inv;
+    r[i].lse2 = sum[i] == 0.f ? -INFINITY : top[i] + __log2f(sum[i]);
+  }
 }
 
 // Publishes a unit's rows, joins the tile's parts if it is the last to arrive, and writes
@@ -380,11 +394,13 @@ __device__ __forceinline__ void finish_unit(const AttentionParams& p, const Unit
       }
     };
     auto join = [&](int off, int gap, int n) {
+      int at[R], lse_at[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int row = r + 16 * i;
-        if (row < u.rows) join_parts<C>(part[i], rs, off + (row * D + x * C) * 4, off + (16 * R * D + row) * 4, gap, n);
+        const int row = min(r + 16 * i, u.rows - 1);  // rows past the tile: as its last, and not written
+        at[i] = off + (row * D + x * C) * 4, lse_at[i] = off + (16 * R * D + row) * 4;
       }
+      join_parts<R, C>(part, rs, at, lse_at, gap, n);
     };
     const int group = u.chunk / kJoin, groups = (u.chunks + kJoin - 1) / kJoin;
     const int in_group = min(kJoin, u.chunks - group * kJoin);
@@ -467,9 +483,70 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
   Unit u;
   if (!find_unit(p, plan, blockIdx.x, u)) return;
 
+  const int steps = (u.k1 - u.k0 + 31) >> 5, share = (steps + 3) >> 2;
+  const int step0 = min(steps, wave * share), step1 = min(steps, step0 + share);
+
+  // A segment is up to 32 steps, of whose 64 groups of 16 keys lane i holds what group i
+  // needs: where its rows start in the caches, the factor of its logits, and the base 2
+  // logarithm of its value scale. The loads of a unit's start depend on each other in
+  // three rounds: the sequences, the pages, and then at once the scales, the queries and
+  // the first two stages.
+  auto page_of_lane = [&](int seg) {
+    const int key = u.k0 + seg * 32 + lane * 16;
+    return seg < step1 && key < u.k1 ? p.block_table[u.b * p.ld_bt + (key >> p.log_p)] : -1;
+  };
+  struct Segment {
+    uint32_t at_lo, at_hi;
+    float c, v;
+    uint64_t holes, changes;  // groups without a page; with another value scale than two groups before
+    int count;
+  };
+  const uint8_t* ring = shared + wave * 2 * Ring::kBytes;
+  const uint32_t ring_lds = __builtin_amdgcn_readfirstlane(lds_address(ring));
+  Segment g;
+  auto rows_of = [&](const uint8_t* cache, int i) {
+    const uint32_t lo = __builtin_amdgcn_readlane(g.at_lo, i), hi = __builtin_amdgcn_readlane(g.at_hi, i);
+    return cache + ((uint64_t)hi << 32 | lo);
+  };
+  auto fetch_keys = [&](int s) {
+    Ring::load_keys(rows_of(p.k_cache, 2 * s), rows_of(p.k_cache, 2 * s + 1), ring_lds + (s & 1) * Ring::kBytes, lane);
+  };
+  auto fetch_values = [&](int s) {
+    Ring::load_values(rows_of(p.v_cache, 2 * s), rows_of(p.v_cache, 2 * s + 1), ring_lds + (s & 1) * Ring::kBytes, lane);
+  };
+  float ks = 0.f, vs = 0.f;
+  auto open = [&](int seg, int page) {  // starts a segment's loads
+    const int key = u.k0 + seg * 32 + lane * 16;
+    const bool there = page >= 0 && page < p.num_pages;
+    const int64_t head = (int64_t)page * p.Hkv + u.h;
+    const uint64_t at = there ? (uint64_t)((head << p.log_p) + (key & ((1 << p.log_p) - 1))) * D : 0;  // page 0 stands in for none
+    g.at_lo = (uint32_t)at, g.at_hi = (uint32_t)(at >> 32);
+    g.holes = ~__ballot(there);
+    g.count = min(32, step1 - seg);
+    ks = vs = 0.f;
+    if (there) ks = p.k_scale[head], vs = p.v_scale[head];
+    if (g.count > 0) {
+      fetch_keys(0);
+      fetch_values(0);
+      if (g.count > 1) {
+        fetch_keys(1);
+        fetch_values(1);
+      }
+    }
+    fence_schedule();
+  };
+  auto settle = [&]() {  // once the scales are there
+    g.c = __uint_as_float(__float_as_uint(ks) & 0x7F800000u) * p.scale_log2;
+    g.v = (float)(exponent(__float_as_uint(vs)) - 127);
+    const float before = __shfl(g.v, max(lane - 2, 0), 64);
+    g.changes = __ballot(lane < 2 || g.v != before);
+  };
+  auto of_lane = [&](float v, int i) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i)); };
+  const int first_page = page_of_lane(step0);
+
   // this lane's rows: query fragments, and the keys that each sees, [key_lo, key_hi)
   int key_lo[R], key_hi[R];
-  v8bf qf[R][D / 32];
+  uint4 q_raw[R][D / 32];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const bool live = n + 16 * i < u.rows;
@@ -481,13 +558,20 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
     const uint16_t* src = p.q + (int64_t)(u.seq.row0 + token) * p.ldq + head * D;
 #pragma unroll
     for (int s = 0; s < D / 32; ++s) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (live) x = *reinterpret_cast<const uint4*>(src + (s >> 1) * 64 + kg * 16 + (s & 1) * 8);
-      // the scale's sign is taken here, so that the factors of logits are not negative
-      x.x ^= p.q_sign, x.y ^= p.q_sign, x.z ^= p.q_sign, x.w ^= p.q_sign;
-      qf[i][s] = __builtin_bit_cast(v8bf, x);
+      q_raw[i][s] = make_uint4(0, 0, 0, 0);
+      if (live) q_raw[i][s] = *reinterpret_cast<const uint4*>(src + (s >> 1) * 64 + kg * 16 + (s & 1) * 8);
     }
   }
+  fence_schedule();
+  open(step0, first_page);
+  v8bf qf[R][D / 32];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {  // the scale's sign is taken here, so that the factors of logits are not negative
+      const uint4 x = q_raw[i][s];
+      qf[i][s] = __builtin_bit_cast(v8bf, make_uint4(x.x ^ p.q_sign, x.y ^ p.q_sign, x.z ^ p.q_sign, x.w ^ p.q_sign));
+    }
   // keys that every row of the tile sees
   const int all_hi = min(u.seq.len, u.pos0 + 1), all_lo = p.window ? u.pos1 - p.window + 1 : 0;
 
@@ -501,59 +585,17 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
     for (int t = 0; t < kTiles; ++t) o[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  const int steps = (u.k1 - u.k0 + 31) >> 5, share = (steps + 3) >> 2;
-  const int step0 = min(steps, wave * share), step1 = min(steps, step0 + share);
   for (int seg = step0; seg < step1; seg += 32) {
-    // lane i holds what group i (16 keys) of the next 64 needs: where its rows start in the
-    // caches, the factor of its logits, and the base 2 logarithm of its value scale
-    uint32_t at_lo = 0, at_hi = 0;
-    float c_lane = 0.f, v_lane = 0.f;
-    bool there = false;
-    {
-      const int key = u.k0 + seg * 32 + lane * 16;
-      if (key < u.k1) {
-        const int page = p.block_table[u.b * p.ld_bt + (key >> p.log_p)];
-        there = page >= 0 && page < p.num_pages;
-        if (there) {  // page 0 stands in for none
-          const int64_t head = (int64_t)page * p.Hkv + u.h;
-          const uint64_t at = (uint64_t)((head << p.log_p) + (key & ((1 << p.log_p) - 1))) * D;
-          at_lo = (uint32_t)at, at_hi = (uint32_t)(at >> 32);
-          c_lane = __uint_as_float(__float_as_uint(p.k_scale[head]) & 0x7F800000u) * p.scale_log2;
-          v_lane = (float)(exponent(__float_as_uint(p.v_scale[head])) - 127);
-        }
-      }
-    }
-    const uint64_t holes = ~__ballot(there);  // groups without a page
-    const float v_before = __shfl(v_lane, max(lane - 2, 0), 64);
-    const uint64_t changes = __ballot(lane < 2 || v_lane != v_before);  // another value scale than two groups before
-    const int count = min(32, step1 - seg);
-    const uint8_t* ring = shared + wave * 2 * Ring::kBytes;
-    const uint32_t ring_lds = __builtin_amdgcn_readfirstlane(lds_address(ring));
-    auto of_lane = [&](float v, int g) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), g)); };
-    auto rows_of = [&](const uint8_t* cache, int g) {
-      const uint32_t lo = __builtin_amdgcn_readlane(at_lo, g), hi = __builtin_amdgcn_readlane(at_hi, g);
-      return cache + ((uint64_t)hi << 32 | lo);
-    };
-    auto fetch_keys = [&](int s) {
-      Ring::load_keys(rows_of(p.k_cache, 2 * s), rows_of(p.k_cache, 2 * s + 1), ring_lds + (s & 1) * Ring::kBytes, lane);
-    };
-    auto fetch_values = [&](int s) {
-      Ring::load_values(rows_of(p.v_cache, 2 * s), rows_of(p.v_cache, 2 * s + 1), ring_lds + (s & 1) * Ring::kBytes, lane);
-    };
-    wait_loads<0>();  // the pages and scales
-    fetch_keys(0);
-    fetch_values(0);
-    if (count > 1) {
-      fetch_keys(1);
-      fetch_values(1);
-    }
+    if (seg > step0) open(seg, page_of_lane(seg));
+    settle();
+    const int count = g.count;
     for (int s = 0; s < count; ++s) {
       const int left = count - 1 - s;  // steps after this one
       const uint8_t* stage = ring + (s & 1) * Ring::kBytes;
       const int key = u.k0 + (seg + s) * 32;
-      float c0 = of_lane(c_lane, 2 * s), c1 = of_lane(c_lane, 2 * s + 1);
-      const float v0 = of_lane(v_lane, 2 * s), v1 = of_lane(v_lane, 2 * s + 1);
-      const uint32_t hole = (uint32_t)(holes >> (2 * s)) & 3;
+      float c0 = of_lane(g.c, 2 * s), c1 = of_lane(g.c, 2 * s + 1);
+      const float v0 = of_lane(g.v, 2 * s), v1 = of_lane(g.v, 2 * s + 1);
+      const uint32_t hole = (uint32_t)(g.holes >> (2 * s)) & 3;
 
       v4f s0[R], s1[R];
 #pragma unroll
@@ -647,7 +689,7 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
           for (int t2 = 0; t2 < kTiles; ++t2) o[i][t2] *= b;
         }
       }
-      if (rarely(moved || (changes >> (2 * s) & 3) != 0)) {
+      if (rarely(moved || (g.changes >> (2 * s) & 3) != 0)) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           a0[i] = fmaxf(v0 + (15 - kLag) - mo[i], kFar - m[i]), k0[i] = exp2_of(-(a0[i] + m[i]));
