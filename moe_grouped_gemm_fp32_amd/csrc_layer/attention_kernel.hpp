@@ -54,6 +54,13 @@ constexpr int kJoin = 8;                // parts joined at a time, all loads in 
 // what o holds, w keeps this much below the likeliest key's 2^0 instead, for l's sake.
 constexpr float kFar = -60.f;
 
+// Division of numbers below 2^31 by a divisor known on the host: n m / 2^s with m the
+// quotient 2^s / d rounded up, s = 31 + ceil(log2 d), so that n times m's error is below 2^s.
+struct Divisor {
+  uint32_t d, m, s;
+  __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> s); }
+};
+
 struct AttentionParams {
   const uint16_t* q;
   const uint8_t *k_cache, *v_cache;
@@ -67,6 +74,7 @@ struct AttentionParams {
   float scale_log2;  // |softmax_scale| log2(e)
   uint32_t q_sign;   // the scale's sign, as the sign bits of two BF16 values
   int window, B, T, Hq, Hkv, group, num_pages, log_p, max_pages;
+  Divisor by_group, by_heads;  // group, Hkv
   int residents;   // workgroups that the GPU holds at a time
   int most_units;  // units that splitting may add; 0: no splitting
 };
@@ -96,6 +104,9 @@ struct Plan {
   Demand want;
   int chunk_len;
 
+  __device__ __forceinline__ int chunks_of(int keys) const {
+    return (int)(((uint32_t)keys + (uint32_t)chunk_len - 1) / (uint32_t)chunk_len);
+  }
   __device__ __forceinline__ void look(const AttentionParams& p, int base) {
     const int b = base + (threadIdx.x & 63);
     seq = {}, want = {};
@@ -141,13 +152,13 @@ struct Unit {
 template <int TILE, int STEP>
 __device__ __forceinline__ bool find_unit(const AttentionParams& p, Plan<TILE, STEP>& plan, int number, Unit& u) {
   u.slot = number;
-  u.h = number % p.Hkv;
-  const int want = number / p.Hkv;
+  const int want = p.by_heads.of(number);
+  u.h = number - want * p.Hkv;
   int before = 0, tiles_before = 0;
   for (int base = 0; base < p.B; base += 64) {
     if (p.B > 64 || p.most_units == 0) plan.look(p, base);
     const Demand d = plan.want;
-    const int count = d.tiles * max(1, (int)(((int64_t)d.keys + plan.chunk_len - 1) / plan.chunk_len));
+    const int count = d.tiles * max(1, plan.chunks_of(d.keys));
     const int incl = wave_scan(count);
     const uint64_t hit = __ballot(want < before + incl);
     if (hit) {
@@ -158,25 +169,25 @@ __device__ __forceinline__ bool find_unit(const AttentionParams& p, Plan<TILE, S
       u.seq = {pick(plan.seq.row0), pick(plan.seq.rows), pick(plan.seq.len)};
       u.tiles = pick(d.tiles);
       const int within = want - (before + pick(incl - count));
-      u.chunk = within / u.tiles;
-      u.tile = u.tiles - 1 - within % u.tiles;  // the tiles with the most keys first
+      u.chunk = (uint32_t)within / (uint32_t)u.tiles;
+      u.tile = u.tiles - 1 - (within - u.chunk * u.tiles);  // the tiles with the most keys first
       u.tile_id = (tiles_before + pick(tiles_incl - d.tiles) + u.tile) * p.Hkv + u.h;
       const int total = u.seq.rows * p.group;
       u.row0 = u.tile * TILE;
       u.rows = min(TILE, total - u.row0);
       const int first = u.seq.len - u.seq.rows;
-      u.pos0 = first + u.row0 / p.group;
-      u.pos1 = first + (u.row0 + u.rows - 1) / p.group;
+      u.pos0 = first + p.by_group.of(u.row0);
+      u.pos1 = first + p.by_group.of(u.row0 + u.rows - 1);
       u.lo = p.window ? max(0, u.pos0 - p.window + 1) / STEP * STEP : 0;
       u.hi = max(u.lo, min(u.seq.len, u.pos1 + 1));
       // as many chunks as the length asks for, of equal length
       const int keys = u.hi - u.lo;
-      const int wanted = max(1, (int)(((int64_t)keys + plan.chunk_len - 1) / plan.chunk_len));
-      const int len = max(128, ((keys + wanted - 1) / wanted + 127) / 128 * 128);
-      u.chunks = max(1, (keys + len - 1) / len);
+      const uint32_t wanted = max(1, plan.chunks_of(keys));
+      const uint32_t len = max(128u, (((uint32_t)keys + wanted - 1) / wanted + 127) / 128 * 128);
+      u.chunks = max(1, (int)(((uint32_t)keys + len - 1) / len));
       if (u.chunk >= u.chunks) return false;  // a tile that sees fewer keys than the sequence's last
-      u.k0 = min(u.hi, u.lo + u.chunk * len);
-      u.k1 = min(u.hi, u.k0 + len);
+      u.k0 = (int)min((uint32_t)u.hi, u.lo + u.chunk * len);
+      u.k1 = (int)min((uint32_t)u.hi, u.k0 + len);
       return true;
     }
     before += last_lane(incl);
@@ -402,19 +413,22 @@ __device__ __forceinline__ void finish_unit(const AttentionParams& p, const Unit
       }
       join_parts<R, C>(part, rs, at, lse_at, gap, n);
     };
+    // first the group of kJoin neighbours that this unit is one of, then the groups, whose
+    // results stand in their first member's place: one code for both, since a short call
+    // pays for every line of it that is fetched
     const int group = u.chunk / kJoin, groups = (u.chunks + kJoin - 1) / kJoin;
-    const int in_group = min(kJoin, u.chunks - group * kJoin);
-    const int group_off = group * kJoin * stride;
-    if (in_group > 1) {
-      publish(u.chunk * stride);
-      if (!arrive_last(&p.counters[kTileCounters + first + group * kJoin * step], in_group, flag)) return;
-      join(group_off, stride, in_group);
-    }
-    if (groups > 1) {
-      __syncthreads();  // the flag is used again
-      publish(group_off);
-      if (!arrive_last(&p.counters[u.tile_id], groups, flag)) return;
-      join(0, kJoin * stride, groups);
+    int own = u.chunk * stride, from = group * kJoin * stride, gap = stride, n = min(kJoin, u.chunks - group * kJoin);
+    int32_t* counter = p.counters + kTileCounters + first + group * kJoin * step;
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+      if (n > 1) {
+        publish(own);
+        if (!arrive_last(counter, n, flag)) return;
+        join(from, gap, n);
+        __syncthreads();  // the flag is used again
+      }
+      own = from, from = 0, gap = kJoin * stride, n = groups;
+      counter = p.counters + u.tile_id;
     }
   }
 #pragma unroll
@@ -422,8 +436,9 @@ __device__ __forceinline__ void finish_unit(const AttentionParams& p, const Unit
     const int row = r + 16 * i;
     if (row < u.rows) {
       const int rr = u.row0 + row;
-      const int64_t token = u.seq.row0 + rr / p.group;
-      const int head = u.h * p.group + rr % p.group;
+      const int in_seq = p.by_group.of(rr);
+      const int64_t token = u.seq.row0 + in_seq;
+      const int head = u.h * p.group + rr - in_seq * p.group;
       uint16_t* dst = p.O + token * p.ldo + head * D + x * C;
 #pragma unroll
       for (int t = 0; t < C; t += 4)
@@ -551,7 +566,7 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
   for (int i = 0; i < R; ++i) {
     const bool live = n + 16 * i < u.rows;
     const int row = u.row0 + (live ? n + 16 * i : 0);
-    const int token = row / p.group, head = u.h * p.group + row % p.group;
+    const int token = p.by_group.of(row), head = u.h * p.group + row - token * p.group;
     const int pos = u.seq.len - u.seq.rows + token;
     key_hi[i] = min(u.seq.len, pos + 1);
     key_lo[i] = p.window ? max(0, pos - p.window + 1) : 0;

@@ -149,6 +149,11 @@ int attention_row_blocks(int64_t rows, int64_t heads, int D, int cus) {
   return tiles * most * kLargeTile < ceil_div(rows, 32) * 32 && tiles * heads >= cus ? most_row_blocks(D) : 2;
 }
 
+fp8layer::Divisor divisor(int d) {
+  const int log = d > 1 ? 32 - __builtin_clz(d - 1) : 0;  // ceil(log2 d)
+  return {(uint32_t)d, (uint32_t)((((uint64_t)1 << (31 + log)) + d - 1) / d), (uint32_t)(31 + log)};
+}
+
 constexpr size_t kAttentionCounterBytes = fp8layer::kCounters * sizeof(int32_t);
 constexpr size_t kAttentionPartBytes = (size_t)64 << 20;
 
@@ -352,6 +357,8 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.group = Hq / Hkv;
+  p.by_group = divisor(p.group);
+  p.by_heads = divisor(Hkv);
   p.num_pages = num_pages;
   p.log_p = log2_of(P);
   p.max_pages = max_pages;
