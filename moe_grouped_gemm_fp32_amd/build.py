@@ -1,4 +1,5 @@
-"""Ahead-of-time build of libfp8gemm.so for gfx950 (hipcc, in-tree).
+"""Ahead-of-time build of libfp8gemm.so for gfx950 (hipcc, in-tree), and of the native half
+of the layer operators' Python binding (_layer_call.so, host code).
 
 Every kernel variant is a template instance compiled once here; the host code
 picks one per call. Packed-FP32 VALU instructions are disabled for all device code.
@@ -10,11 +11,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", "fp8gemm.hip"), os.path.join(PKG, "csrc_layer", "fp8layer.hip")]
 LIB = os.path.join(PKG, "libfp8gemm.so")
+CALL_SRC = os.path.join(PKG, "csrc_layer", "binding.cpp")
+CALL = os.path.join(PKG, "_layer_call.so")
 ARCH = "gfx950"
 
 
@@ -38,11 +42,25 @@ def sources() -> list:
         sorted(glob.glob(os.path.join(ROOT, "include", "*.h"))) + [os.path.abspath(__file__)]
 
 
-def _compile(out: str, extra: list, verbose: bool) -> str:
-    """One object per source, compiled side by side, linked into `out`."""
+def _call_command() -> list:
+    """Compiles the layer operators' Python calls: host code against the interpreter's, torch's
+    and the HIP runtime's headers. The library itself is bound when it is loaded."""
+    from torch.utils.cpp_extension import include_paths, library_paths
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    headers = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(rocm, "include")]
+    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__",
+            "-I", os.path.join(ROOT, "include"), *(x for h in headers for x in ("-isystem", h)), CALL_SRC,
+            *("-L" + d for d in library_paths()), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+
+
+def _compile(out: str, extra: list, verbose: bool, beside: dict = {}) -> str:
+    """One object per source, compiled side by side, linked into `out`; `beside`: further
+    files and the commands, up to -o, that make them."""
     tmp = out + ".tmp%d" % os.getpid()
     objs = ["%s.%d.o" % (tmp, i) for i in range(len(SRCS))]
+    more = {path: path + ".tmp%d" % os.getpid() for path in beside}
     steps = [[hipcc(), *FLAGS, *extra, "-c", src, "-o", obj] for src, obj in zip(SRCS, objs)]
+    steps += [[*cmd, "-o", more[path]] for path, cmd in beside.items()]
     link = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *extra, *objs, "-o", tmp]
     try:
         if verbose:
@@ -56,18 +74,21 @@ def _compile(out: str, extra: list, verbose: bool) -> str:
             done.append(res.returncode)
         if any(done):
             sys.stderr.write("".join(said))
-            raise RuntimeError("hipcc failed building " + os.path.basename(out))
+            raise RuntimeError("the compiler failed building " + os.path.basename(out))
         os.replace(tmp, out)
+        for path, made in more.items():
+            os.replace(made, path)
     finally:
-        for f in (*objs, tmp):
+        for f in (*objs, tmp, *more.values()):
             if os.path.exists(f):
                 os.remove(f)
     return out
 
 
 def build(verbose: bool = True) -> str:
-    """Compile libfp8gemm.so next to this file (always rebuilds). Returns its path."""
-    return _compile(LIB, [], verbose)
+    """Compile libfp8gemm.so and _layer_call.so next to this file (always rebuilds). Returns the
+    library's path."""
+    return _compile(LIB, [], verbose, {CALL: _call_command()})
 
 
 # Host-sanitizer build: the same library with its host code (argument checks, planner,

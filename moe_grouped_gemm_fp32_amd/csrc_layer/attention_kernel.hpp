@@ -414,21 +414,20 @@ __device__ __forceinline__ void finish_unit(const AttentionParams& p, const Unit
       join_parts<R, C>(part, rs, at, lse_at, gap, n);
     };
     // first the group of kJoin neighbours that this unit is one of, then the groups, whose
-    // results stand in their first member's place: one code for both, since a short call
-    // pays for every line of it that is fetched
+    // results stand in their first member's place
     const int group = u.chunk / kJoin, groups = (u.chunks + kJoin - 1) / kJoin;
-    int own = u.chunk * stride, from = group * kJoin * stride, gap = stride, n = min(kJoin, u.chunks - group * kJoin);
-    int32_t* counter = p.counters + kTileCounters + first + group * kJoin * step;
-#pragma unroll 1
-    for (int level = 0; level < 2; ++level) {
-      if (n > 1) {
-        publish(own);
-        if (!arrive_last(counter, n, flag)) return;
-        join(from, gap, n);
-        __syncthreads();  // the flag is used again
-      }
-      own = from, from = 0, gap = kJoin * stride, n = groups;
-      counter = p.counters + u.tile_id;
+    const int in_group = min(kJoin, u.chunks - group * kJoin);
+    const int group_off = group * kJoin * stride;
+    if (in_group > 1) {
+      publish(u.chunk * stride);
+      if (!arrive_last(&p.counters[kTileCounters + first + group * kJoin * step], in_group, flag)) return;
+      join(group_off, stride, in_group);
+    }
+    if (groups > 1) {
+      __syncthreads();  // the flag is used again
+      publish(group_off);
+      if (!arrive_last(&p.counters[u.tile_id], groups, flag)) return;
+      join(0, kJoin * stride, groups);
     }
   }
 #pragma unroll
