@@ -17,9 +17,14 @@ constexpr float kE4m3Max = 448.0f;
 template <typename T>
 struct Eight {
   uint4 v[sizeof(T) / 2];
+  // STREAM: with the hint that the lines are read once.
+  template <bool STREAM = false>
   __device__ __forceinline__ void load(const T* src) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(src)[i];
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      if constexpr (STREAM) v[i] = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const v4u*>(src) + i));
+      else v[i] = reinterpret_cast<const uint4*>(src)[i];
+    }
   }
   __device__ __forceinline__ void store(T* dst) const {
 #pragma unroll
@@ -41,10 +46,10 @@ struct Eight {
   __device__ __forceinline__ void set(const float (&x)[8]);
 };
 
-template <typename T>
+template <bool STREAM = false, typename T>
 __device__ __forceinline__ void load8(const T* src, float (&x)[8]) {
   Eight<T> e;
-  e.load(src);
+  e.template load<STREAM>(src);
   e.get(x);
 }
 

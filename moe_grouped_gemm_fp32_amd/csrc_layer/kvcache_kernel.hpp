@@ -50,13 +50,13 @@ __device__ __forceinline__ Item item_of(int i, int rot_dim, int interleaved) {
   return {halves ? 8 * i : 16 * i, halves ? (rot_dim >> 1) + 8 * i : 16 * i + 8, turns};
 }
 
-// Loads the item's 16 columns and turns them, by cos/sin of pairs 8 i .. 8 i + 7 of the
-// row `cs`. Every product and sum is rounded by itself.
-__device__ __forceinline__ void load_item(const uint16_t* src, const float* cs, const Item& it, int i, int rot_dim,
-                                          int interleaved, float (&a)[8], float (&b)[8]) {
+// Turns the item's 16 columns by cos/sin of pairs 8 i .. 8 i + 7 of the row `cs`. Every
+// product and sum is rounded by itself.
+__device__ __forceinline__ void turn_item(const Eight<uint16_t>& lo, const Eight<uint16_t>& hi, const float* cs, const Item& it, int i,
+                                          int rot_dim, int interleaved, float (&a)[8], float (&b)[8]) {
 #pragma clang fp contract(off)
-  load8(src + it.lo, a);
-  load8(src + it.hi, b);
+  lo.get(a);
+  hi.get(b);
   if (it.turns) {
     float c[8], s[8];
     load8(cs + 8 * i, c);
@@ -87,7 +87,7 @@ __device__ __forceinline__ void encode(float (&x)[8], float inv) {
   for (int j = 0; j < 8; ++j) x[j] = fabsf(x[j]) < INFINITY ? x[j] * inv : __builtin_nanf("");
 }
 
-template <int D, int WAVES>
+template <int D, int WAVES, bool STREAM>
 __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) {
   constexpr int kItems = D / 16;               // items of one head
   constexpr int kThreads = WAVES * 64;         // threads of a unit
@@ -99,28 +99,41 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
 
   if ((int)blockIdx.x >= p.unit_groups) {  // queries: a thread has item n % kItems of every so many heads
     const int t0 = ((int)blockIdx.x - p.unit_groups) * p.group_tokens, t1 = min(p.T, t0 + p.group_tokens);
-    Sequence sq{};
-    for (int t = t0; t < t1; ++t) {
-      if (t == t0 || t >= sq.row0 + sq.rows) {  // the token's sequence: the last with cu_q[b] <= t
-        int b = -1;
-        for (int base = 0; base < p.B; base += 64) {
-          const int n = __popcll(__ballot(base + lane < p.B && p.cu_q[min(base + lane, p.B - 1)] <= t));
-          b += n;
-          if (n < 64) break;
+    for (int n0 = 0; n0 < p.Hq * kItems; n0 += 256) {
+      const int n = n0 + threadIdx.x, i = n % kItems, h = n / kItems;
+      const bool live = n < p.Hq * kItems;
+      const Item it = item_of(i, p.rot_dim, p.interleaved);
+      Eight<uint16_t> lo, hi;  // of the next token
+      auto fetch = [&](int t) {
+        if (live && t < t1) {
+          const uint16_t* src = p.q + t * p.ldq + h * D;
+          lo.template load<STREAM>(src + it.lo), hi.template load<STREAM>(src + it.hi);
         }
-        sq = sequence(p.cu_q, p.seq_lens, max(b, 0), p.T, max_len);
-        if (t >= sq.row0 + sq.rows) return;  // past the last sequence
-      }
-      const int at = p.positions ? p.positions[t] : sq.len - (sq.row0 + sq.rows - t);
-      const float* cs = p.cos_sin + min(max(at, 0), p.max_pos - 1) * p.ld_cs;
-      for (int n = threadIdx.x; n < p.Hq * kItems; n += 256) {
-        const int i = n % kItems, h = n / kItems;
-        const Item it = item_of(i, p.rot_dim, p.interleaved);
-        float a[8], c[8];
-        load_item(p.q + t * p.ldq + h * D, cs, it, i, p.rot_dim, p.interleaved, a, c);
-        uint16_t* dst = p.q_out + t * p.ldqo + h * D;
-        store8(dst + it.lo, a);
-        store8(dst + it.hi, c);
+      };
+      fetch(t0);
+      Sequence sq{};
+      for (int t = t0; t < t1; ++t) {
+        if (t == t0 || t >= sq.row0 + sq.rows) {  // the token's sequence: the last with cu_q[b] <= t
+          int b = -1;
+          for (int base = 0; base < p.B; base += 64) {
+            const int before = __popcll(__ballot(base + lane < p.B && p.cu_q[min(base + lane, p.B - 1)] <= t));
+            b += before;
+            if (before < 64) break;
+          }
+          sq = sequence(p.cu_q, p.seq_lens, max(b, 0), p.T, max_len);
+          if (t >= sq.row0 + sq.rows) break;  // past the last sequence
+        }
+        const int at = p.positions ? p.positions[t] : sq.len - (sq.row0 + sq.rows - t);
+        const float* cs = p.cos_sin + min(max(at, 0), p.max_pos - 1) * p.ld_cs;
+        const Eight<uint16_t> lo0 = lo, hi0 = hi;
+        fetch(t + 1);
+        if (live) {
+          float a[8], c[8];
+          turn_item(lo0, hi0, cs, it, i, p.rot_dim, p.interleaved, a, c);
+          uint16_t* dst = p.q_out + t * p.ldqo + h * D;
+          store8(dst + it.lo, a);
+          store8(dst + it.hi, c);
+        }
       }
     }
     return;
@@ -179,7 +192,9 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
     const int row = row_at + s;
     const int at = p.positions ? p.positions[row] : slot0 + s;
     const int pos = min(max(at, 0), p.max_pos - 1);
-    load_item(src + row * ld + h * D, p.cos_sin + pos * p.ld_cs, it, i, rot, p.interleaved, a, b);
+    Eight<uint16_t> lo, hi;
+    lo.template load<STREAM>(src + row * ld + h * D + it.lo), hi.template load<STREAM>(src + row * ld + h * D + it.hi);
+    turn_item(lo, hi, p.cos_sin + pos * p.ld_cs, it, i, rot, p.interleaved, a, b);
   };
 
   float held_a[kHeld][8], held_b[kHeld][8];

@@ -51,7 +51,7 @@ __device__ __forceinline__ float quotient(float y, float s, float r) {
 
 // Forward: sum of squares, then y = (h * rstd) * w in FP32, its maximum over the 16 lanes
 // of a block, and the codes.
-template <typename T, int WPR, int CH>
+template <typename T, int WPR, int CH, bool STREAM>
 __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quantize_kernel(const NormParams p) {
   constexpr int kRows = WPR > 4 ? 1 : 4 / WPR;  // rows of a workgroup
   __shared__ float part[WPR > 4 ? WPR : 4];
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quantize_ker
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = t + i * WPR * 64;
-    if (c < chunks) h[i].load(X + c * 8);
+    if (c < chunks) h[i].template load<STREAM>(X + c * 8);
   }
   if (p.R) {
     const T* R = static_cast<const T*>(p.R) + (int64_t)row * p.ldr;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quantize_ker
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = t + i * WPR * 64;
-      if (c < chunks) r[i].load(R + c * 8);
+      if (c < chunks) r[i].template load<STREAM>(R + c * 8);
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -146,7 +146,7 @@ struct NormGradParams {
 // few hold partial sums of dW (in registers over all rows of the workgroup; 256 parts of
 // 28 KB for 4096 rows of 7168 columns, against 235 MB read and written). The next rows are
 // loaded before the present ones are reduced.
-template <typename T, int WPR, int CH>
+template <typename T, int WPR, int CH, bool STREAM>
 __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormGradParams p) {
   constexpr int kRows = 16 / WPR;
   __shared__ float part[2][16];
@@ -172,9 +172,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormGradPa
     for (int i = 0; i < CH; ++i) {
       const int c = t + i * WPR * 64;
       if (c < chunks) {
-        dy[i].load(static_cast<const T*>(p.dY) + (int64_t)row * p.lddy + c * 8);
-        h[i].load(static_cast<const T*>(p.H) + (int64_t)row * p.ldh + c * 8);
-        if (p.dH) dh[i].load(static_cast<const T*>(p.dH) + (int64_t)row * p.lddh + c * 8);
+        dy[i].template load<STREAM>(static_cast<const T*>(p.dY) + (int64_t)row * p.lddy + c * 8);
+        h[i].template load<STREAM>(static_cast<const T*>(p.H) + (int64_t)row * p.ldh + c * 8);
+        if (p.dH) dh[i].template load<STREAM>(static_cast<const T*>(p.dH) + (int64_t)row * p.lddh + c * 8);
       }
     }
   };
