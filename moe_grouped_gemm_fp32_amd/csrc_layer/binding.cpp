@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
+#include <cmath>
 
 #include "fp8gemm.h"
 #include "fp8layer.h"
@@ -316,7 +317,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// q, cache, block_table, seq_lens, cu_q, out, lse, softmax_scale, window, workspace, stream -> out
+// q, cache, block_table, seq_lens, cu_q, out, lse, softmax_scale (None: D^-1/2), window, workspace, stream -> out
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arguments(n, 11);
@@ -345,7 +346,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(t.device() == dev && t.is_contiguous(), "workspace must be contiguous on q's device");
     ws = t.data_ptr(), ws_bytes = t.nbytes();
   }
-  const float scale = to_float(a[7]);
+  const float scale = given(a[7]) ? to_float(a[7]) : (float)(1.0 / std::sqrt((double)D));
   const int window = to_int(a[8], "window"), tokens = to_int(T, "T"), q_heads = to_int(Hq, "Hq");
   const hipStream_t stream = stream_of(a[10], dev);
   call("fp8_paged_attention", [&] {

@@ -174,6 +174,4 @@ def paged_attention(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Ten
     [T, Hq], receives log sum exp of each row's scaled logits. A row that sees nothing gives
     0 and -inf. workspace: optional (make_attention_workspace), lets sequences be split over
     workgroups; calls that may overlap in time must not share one."""
-    if softmax_scale is None:
-        softmax_scale = q.shape[-1] ** -0.5
     return (_native or _calls()).attend(q, cache, block_table, seq_lens, cu_q, out, lse, softmax_scale, window, workspace, stream)
