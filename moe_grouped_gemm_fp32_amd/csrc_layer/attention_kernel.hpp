@@ -75,7 +75,7 @@ struct AttentionParams {
   uint32_t q_sign;   // the scale's sign, as the sign bits of two BF16 values
   int window, B, T, Hq, Hkv, group, num_pages, log_p, max_pages;
   Divisor by_group, by_heads;  // group, Hkv
-  int residents;   // workgroups that the GPU holds at a time
+  int cus;         // compute units
   int most_units;  // units that splitting may add; 0: no splitting
 };
 
@@ -91,13 +91,19 @@ __device__ __forceinline__ Demand demand(const Sequence& s, const AttentionParam
   return {tiles, (int)most};
 }
 
-// How the call's work is cut. With q keys (over all tiles and heads) for each resident
-// workgroup: up to kOneRound, all units at once, one for each workgroup; beyond, units of
-// about kGoodChunk keys, several rounds of them, which even out ragged batches. (Every unit
-// costs ~5 us before its keys stream: measured on 2 x 131072 keys, a chunk length of 1024,
-// 512 and 256 keys took 62, 91 and 149 us.)
-constexpr float kOneRound = 2048.f;
-constexpr float kGoodChunk = 1024.f;
+// How the call's work is cut, by an estimate of the time in keys that a CU reads in it (a CU
+// reads about 100 keys of 128 columns a microsecond). `even` keys are a CU's share.
+//   One unit for each CU, nothing but a start and an end that do not overlap: needs chunks of
+//     `even` keys or a little more, so that the tiles' last chunks fit as well.
+//   Tiles whole: the longest as often as there are rounds, or, of ragged lengths, the share
+//     and a part of the longest.
+//   Several rounds of chunks of c keys: the share, that part of c, and what each unit's start
+//     and end cost; least at c = sqrt(kUnitCost / kTail even).
+// Measured, heads of 128, 8 key heads, one unit for each CU, whole tiles, rounds of 1024 and
+// of 2048: 4 x 65536 keys 86, -, 104, 99 us; 64 x 8192 -, 166, 181, 181; 64 users of 500 to
+// 8192 keys -, 133, 115, 114; 16 x 16000 88, 106, 106, 95.
+constexpr float kUnitCost = 200.f;
+constexpr float kTail = 0.4f;
 template <int TILE, int STEP>
 struct Plan {
   Sequence seq;   // the lane's sequence and demand, of the 64 looked at last
@@ -115,22 +121,46 @@ struct Plan {
       want = demand<TILE, STEP>(seq, p);
     }
   }
-  __device__ __forceinline__ void make(const AttentionParams& p) {
+  __device__ __forceinline__ int rounded(float chunk) const {
+    return max(kMinChunk, ((int)fminf(chunk, 1e9f) + 127) / 128 * 128);
+  }
+  // unit_cost: kUnitCost for the call's head size.
+  __device__ __forceinline__ void make(const AttentionParams& p, float unit_cost) {
     chunk_len = 1 << 30;
     if (p.most_units == 0) return;
     // in FP32: every wave of the call gets the same sums
-    float keys = 0.f, tiles = 0.f;
+    float keys = 0.f, tiles = 0.f, most = 0.f;
     for (int base = 0; base < p.B; base += 64) {
       look(p, base);
       keys += wave_sum((float)want.tiles * (float)want.keys);
       tiles += wave_sum((float)want.tiles);
+      most = fmaxf(most, wave_max((float)want.keys));
     }
     keys *= (float)p.Hkv, tiles *= (float)p.Hkv;
-    const float all = (float)p.residents;
-    float chunk = keys <= kOneRound * all ? keys / fmaxf(all - 0.5f * tiles, 0.5f * all) : kGoodChunk;
+    const float cus = (float)p.cus, even = keys * __builtin_amdgcn_rcpf(cus);
+    // one each, where half of every tile's last chunk is empty
+    float chunk = keys * __builtin_amdgcn_rcpf(fmaxf(cus - 0.5f * tiles, 0.5f * cus));
+    if (chunk > kMinChunk) {
+      if (tiles < cus && p.B <= 64) {  // or exactly, if so many units are no more than the CUs: two counts in one sum
+        const int n = last_lane(wave_scan(units(even) + (units(1.125f * even) << 16))) * p.Hkv;
+        if ((n >> 16) <= p.cus) chunk = (n & 0xFFFF) <= p.cus ? even : 1.125f * even;
+      }
+      const float rounds = ceilf(tiles * __builtin_amdgcn_rcpf(cus));
+      const float whole = fminf(rounds * most, even + kTail * most) + rounds * unit_cost;
+      const float several = __builtin_amdgcn_sqrtf(unit_cost * (1.f / kTail) * even);
+      float cost = tiles < cus ? chunk + unit_cost : INFINITY;
+      if (whole < cost) chunk = most, cost = whole;
+      if (even + 2.f * kTail * several < cost) chunk = several;
+    }
+    // one level of joining where that takes chunks of two steps for each wave at most (1500
+    // keys of one user: 10.3 us by two levels, 9.1 by one; 2500 keys: 10.5 and 10.7)
+    if (most <= 2.f * kMinChunk * kJoin) chunk = fmaxf(chunk, most * (1.f / kJoin));
     // a ten-thousandth more than the sums can be off: no more units than there are slots
-    chunk = fmaxf(chunk, keys / (float)p.most_units * 1.0001f);
-    chunk_len = max(kMinChunk, ((int)fminf(chunk, 1e9f) + 128) / 128 * 128);
+    chunk_len = rounded(fmaxf(chunk, keys / (float)p.most_units * 1.0001f));
+  }
+  // The lane's sequence in about so many keys each (tiles times chunks).
+  __device__ __forceinline__ int units(float chunk) const {
+    return want.tiles * (int)ceilf((float)want.keys * __builtin_amdgcn_rcpf((float)rounded(chunk)) - 1e-3f);
   }
 };
 
@@ -493,7 +523,7 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, kg = lane >> 4;
   Plan<16 * R, 32> plan;
-  plan.make(p);
+  plan.make(p, kUnitCost * 128 / D);
   Unit u;
   if (!find_unit(p, plan, blockIdx.x, u)) return;
 

@@ -152,6 +152,7 @@ int log2_of(int P) {
 // tiles are enough to give every CU one (2 x 95 tokens by 16 heads of 64: 13.5 and 18.4 us).
 constexpr int most_row_blocks(int D) { return D == 64 ? 4 : 3; }
 constexpr double kLargeTile = 0.9;
+constexpr int kFewKeys = 2048;  // for a CU
 int attention_row_blocks(int64_t rows, int64_t heads, int D, int cus) {
   if (rows <= 32) return rows <= 16 ? 1 : 2;
   const int64_t most = 16 * most_row_blocks(D), tiles = ceil_div(rows, most);
@@ -392,13 +393,13 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
   const size_t slot = (size_t)tile * (D + 1) * sizeof(float);
   const size_t bytes = std::min<size_t>(workspace ? workspace_bytes : 0, (size_t)1 << 30);
   const int64_t slots = bytes > kAttentionCounterBytes ? (int64_t)((bytes - kAttentionCounterBytes) / slot) : 0;
-  p.residents = cus * fp8layer::attention_residents(D, blocks);
-  // Units that splitting may add: as many as are resident where the longest sequences that
-  // the table allows make one round of work, four times that otherwise (workgroups
-  // without a unit end at once, but they cost a microsecond a round).
-  const int64_t keys = tiles * max_len;
-  const int64_t rounds = keys <= fp8layer::kOneRound * p.residents ? 1 : 4;
-  const int64_t added = std::min(rounds * p.residents, std::min<int64_t>(slots, fp8layer::kPartCounters) - tiles);
+  p.cus = cus;
+  // Units that splitting may add: one for each CU where the longest sequences that the table
+  // allows are little work, four otherwise (workgroups without a unit end at once, but 512 of
+  // them cost a microsecond).
+  const int64_t most_keys = tiles * max_len;
+  const int64_t rounds = most_keys <= (int64_t)kFewKeys * cus ? 1 : 4;
+  const int64_t added = std::min(rounds * cus, std::min<int64_t>(slots, fp8layer::kPartCounters) - tiles);
   int64_t grid = tiles;
   if (tiles <= fp8layer::kTileCounters && added > 0 && max_len > fp8layer::kMinChunk) {
     p.most_units = (int)added;
