@@ -57,7 +57,7 @@ constexpr float kFar = -60.f;
 // Division of numbers below 2^31 by a divisor known on the host: n m / 2^s with m the
 // quotient 2^s / d rounded up, s = 31 + ceil(log2 d), so that n times m's error is below 2^s.
 struct Divisor {
-  uint32_t d, m, s;
+  uint32_t m, s;
   __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> s); }
 };
 
@@ -156,7 +156,7 @@ struct Plan {
     // keys of one user: 10.3 us by two levels, 9.1 by one; 2500 keys: 10.5 and 10.7)
     if (most <= 2.f * kMinChunk * kJoin) chunk = fmaxf(chunk, most * (1.f / kJoin));
     // a ten-thousandth more than the sums can be off: no more units than there are slots
-    chunk_len = rounded(fmaxf(chunk, keys / (float)p.most_units * 1.0001f));
+    chunk_len = rounded(fmaxf(chunk, keys * __builtin_amdgcn_rcpf((float)p.most_units) * 1.0001f));
   }
   // The lane's sequence in about so many keys each (tiles times chunks).
   __device__ __forceinline__ int units(float chunk) const {
@@ -314,10 +314,6 @@ __device__ __forceinline__ void columns_f16(const uint32_t (&w)[8], bool upper, 
 
 // Exponent field of a power of two.
 __device__ __forceinline__ int exponent(uint32_t bits) { return (int)((bits >> 23) & 0xFF); }
-// 2^e; 0 where that is below the normal range, infinity above.
-__device__ __forceinline__ float pow2(int e) {
-  return e < -126 ? 0.f : e > 127 ? INFINITY : __uint_as_float((uint32_t)(e + 127) << 23);
-}
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Not 0 if one of the four codes is NaN.
@@ -400,7 +396,7 @@ __device__ __forceinline__ void join_parts(RowPart<C> (&r)[R], __amdgpu_buffer_r
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const float inv = sum[i] == 0.f ? 0.f : 1.0f / sum[i];
+    const float inv = sum[i] == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum[i]);
 #pragma unroll
     for (int t = 0; t < C; ++t) r[i].out[t] *= inv;
     r[i].lse2 = sum[i] == 0.f ? -INFINITY : top[i] + __log2f(sum[i]);
@@ -676,17 +672,16 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
         wait_lds_reads();
         fetch_values(s + 2);
       }
-      uint32_t nan_keys = 0;
-      bool any_nan = false;
       // some row does not see all of the step
       if (rarely(key < all_lo || key + 32 > all_hi || hole != 0)) {
+        uint32_t nan_keys = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int at = key + (j >> 2) * 16 + kg * 4 + (j & 3);
           const bool there = (hole >> (j >> 2) & 1) == 0;
           // values that no row sees may be anything: they count as 0. Where a row sees a
-          // NaN code and another does not, the product gets 0 and the rows that see it NaN
-          // by their probability.
+          // NaN code and another does not, the product gets 0, and o of the rows that see it
+          // becomes NaN here.
           const bool some_see = there && at >= u.lo && at < u.hi;
           uint32_t bad = 0;
 #pragma unroll
@@ -695,11 +690,6 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
           const uint32_t keep = some_see && bad == 0 ? ~0u : 0u;  // without branches: in place
 #pragma unroll
           for (int w = 0; w < kWords; ++w) v[j][w] &= keep;
-        }
-        any_nan = __any(nan_keys != 0);
-        if (rarely(any_nan)) {  // over the 16 lanes that feed the same keys
-#pragma unroll
-          for (int off = 1; off < 16; off <<= 1) nan_keys |= __shfl_xor((int)nan_keys, off, 64);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i)
@@ -711,6 +701,22 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
             else s1[i][j - 4] = seen ? s1[i][j - 4] * c1 : -INFINITY;
           }
         c0 = c1 = 1.f;
+        if (rarely(__any(nan_keys != 0))) {
+#pragma unroll
+          for (int off = 1; off < 16; off <<= 1) nan_keys |= __shfl_xor((int)nan_keys, off, 64);  // over the lanes that feed the same keys
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            int bad = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bad |= (nan_keys >> j & 1) && (j < 4 ? s0[i][j] : s1[i][j - 4]) > -INFINITY;
+            bad |= __shfl_xor(bad, 16, 64);
+            bad |= __shfl_xor(bad, 32, 64);
+            if (bad) {
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) o[i][t] = v4f{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+            }
+          }
+        }
       }
       float top[R], top_o[R];
       bool move = false;
@@ -742,16 +748,7 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
       }
       v8h pf[R];
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        pf[i] = weights(s0[i], s1[i], c0, c1, a0[i], a1[i], k0[i], k1[i], l[i]);
-        if (rarely(any_nan)) {
-          uint32_t bits = nan_keys;
-          asm("" : "+v"(bits));  // keeps the tests of its bits on this side of the branch
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if ((bits >> j & 1) && (j < 4 ? s0[i][j] : s1[i][j - 4]) > -INFINITY) pf[i][j] = (_Float16)__builtin_nanf("");
-        }
-      }
+      for (int i = 0; i < R; ++i) pf[i] = weights(s0[i], s1[i], c0, c1, a0[i], a1[i], k0[i], k1[i], l[i]);
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
         uint32_t words[8];
@@ -805,7 +802,7 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
     }
     // o stands for itself times 2^(mo - m - (15 - kLag)), in two factors so that each is in
     // range; a row that saw no key gives 0, and minus infinity
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    const float inv = sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum);
     const float shift = fminf(fmaxf(0.5f * (top_o - top - (15 - kLag)), -126.f), 126.f), half = exp2_of(shift);
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) part[i].out[t] = part[i].out[t] * inv * half * half;

@@ -161,7 +161,7 @@ int attention_row_blocks(int64_t rows, int64_t heads, int D, int cus) {
 
 fp8layer::Divisor divisor(int d) {
   const int log = d > 1 ? 32 - __builtin_clz(d - 1) : 0;  // ceil(log2 d)
-  return {(uint32_t)d, (uint32_t)((((uint64_t)1 << (31 + log)) + d - 1) / d), (uint32_t)(31 + log)};
+  return {(uint32_t)((((uint64_t)1 << (31 + log)) + d - 1) / d), (uint32_t)(31 + log)};
 }
 
 constexpr size_t kAttentionCounterBytes = fp8layer::kCounters * sizeof(int32_t);
