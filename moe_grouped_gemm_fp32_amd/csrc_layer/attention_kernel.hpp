@@ -491,11 +491,24 @@ __device__ __forceinline__ v8h weights(const v4f& s0, const v4f& s1, float c0, f
   for (int j = 0; j < 8; ++j) out[j] = (_Float16)w[j];
   return out;
 }
+__device__ __forceinline__ v8h weights(const v4f& s0, const v4f& s1, float c, float a, float k, float& l) {
+  float w[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w[j] = exp2_of(__builtin_fmaf(s0[j], c, a));
+    w[4 + j] = exp2_of(__builtin_fmaf(s1[j], c, a));
+  }
+  l = __builtin_fmaf(((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7])), k, l);
+  v8h out;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) out[j] = (_Float16)w[j];
+  return out;
+}
 // A maximum as a chain from a constant: the compiler makes it of maxima of three, and of a
 // chain only its first operands, if they could be signalling NaN, cost an instruction to
 // quiet. (Not as inline assembly: the waits between a matrix instruction and a reader of
 // its result are the compiler's to insert, and it does not for assembly.)
-__device__ __forceinline__ float max4(const v4f& s) { return fmaxf(fmaxf(fmaxf(fmaxf(kNone, s[0]), s[1]), s[2]), s[3]); }
+__device__ __forceinline__ float max4(float from, const v4f& s) { return fmaxf(fmaxf(fmaxf(fmaxf(from, s[0]), s[1]), s[2]), s[3]); }
 __device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); }
 
 // Workgroups that registers leave room for on a CU.
@@ -504,7 +517,7 @@ constexpr int attention_residents(int D, int R) { return D == 64 ? (R == 1 ? 4 :
 // STREAM: no other unit reads this one's keys and values. The hint is worth 11% then (64
 // users of 8192 keys: 202 us without, 180 with, 5.99 TB/s) and costs 4% where many tiles
 // share them (2048 prompt tokens: 488 and 506 us).
-template <int D, int R, bool STREAM>
+template <int D, int R, bool STREAM, bool WIDE>
 __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kernel(const AttentionParams p) {
   using Ring = Stage<D, STREAM>;
   constexpr int kWords = D / 64;       // 32-bit words of one value a lane feeds
@@ -722,8 +735,12 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
       bool move = false;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const float t0 = max4(s0[i]) * c0, t1 = max4(s1[i]) * c1;
-        top[i] = fmaxf(t0, t1), top_o[i] = fmaxf(t0 + v0, t1 + v1);
+        if constexpr (WIDE) {
+          top[i] = max4(max4(kNone, s0[i]), s1[i]) * c0, top_o[i] = top[i] + v0;
+        } else {
+          const float t0 = max4(kNone, s0[i]) * c0, t1 = max4(kNone, s1[i]) * c1;
+          top[i] = fmaxf(t0, t1), top_o[i] = fmaxf(t0 + v0, t1 + v1);
+        }
         move |= fmaxf(top[i] - m[i], top_o[i] - mo[i]) > kLag;
       }
       const bool moved = __any(move);
@@ -743,12 +760,15 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           a0[i] = fmaxf(v0 + (15 - kLag) - mo[i], kFar - m[i]), k0[i] = exp2_of(-(a0[i] + m[i]));
-          a1[i] = fmaxf(v1 + (15 - kLag) - mo[i], kFar - m[i]), k1[i] = exp2_of(-(a1[i] + m[i]));
+          if constexpr (!WIDE) a1[i] = fmaxf(v1 + (15 - kLag) - mo[i], kFar - m[i]), k1[i] = exp2_of(-(a1[i] + m[i]));
         }
       }
       v8h pf[R];
 #pragma unroll
-      for (int i = 0; i < R; ++i) pf[i] = weights(s0[i], s1[i], c0, c1, a0[i], a1[i], k0[i], k1[i], l[i]);
+      for (int i = 0; i < R; ++i) {
+        if constexpr (WIDE) pf[i] = weights(s0[i], s1[i], c0, a0[i], k0[i], l[i]);
+        else pf[i] = weights(s0[i], s1[i], c0, c1, a0[i], a1[i], k0[i], k1[i], l[i]);
+      }
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
         uint32_t words[8];

@@ -412,10 +412,13 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
     constexpr int kD = decltype(d)::value;
     const dim3 groups((unsigned)grid);
     constexpr int kMost = most_row_blocks(kD);
-    if (blocks == 1) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true>), groups, dim3(256), 0, stream, p);
-    else if (stream_kv) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, true>), groups, dim3(256), 0, stream, p);
-    else if (blocks == 2) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, false>), groups, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, kMost, false>), groups, dim3(256), 0, stream, p);
+    with_stream(P >= 32, [&](auto w) {
+      constexpr bool kWide = decltype(w)::value;
+      if (blocks == 1) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true, kWide>), groups, dim3(256), 0, stream, p);
+      else if (stream_kv) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, true, kWide>), groups, dim3(256), 0, stream, p);
+      else if (blocks == 2) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, false, kWide>), groups, dim3(256), 0, stream, p);
+      else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, kMost, false, kWide>), groups, dim3(256), 0, stream, p);
+    });
   };
   if (D == 64) go(Int<64>{});
   else if (D == 128) go(Int<128>{});
