@@ -257,37 +257,46 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 // One stage of a wave's ring: 32 keys in the order their lanes feed them ([16-key group]
-// [64-byte piece][lane][16 bytes]), then 32 values, row after row.
+// [64-byte piece][lane][16 bytes]), then 32 values, row after row, each row's 16-byte pieces
+// permuted by an exclusive or with a number of the row, so that the rows which are read
+// together lie in different banks.
 template <int D, bool STREAM>
 struct Stage {
   static constexpr int kPieces = D / 64;            // 64-byte pieces of a row
   static constexpr int kLoads = 2 * kPieces;        // load instructions of a half
   static constexpr int kHalf = 32 * D, kBytes = 2 * kHalf;
+  static constexpr int kShared = D == 64 ? 2 : D == 128 ? 1 : 0;  // log2 of the rows in one line of the 64 banks
+  static constexpr int kLane16 = D / 16;            // 16-byte pieces of a row
+  // row 0 .. 31 of a stage; the 16 rows r & 8 apart from each other share no bank
+  static __device__ __forceinline__ constexpr uint32_t turn(int row) { return ((row & 7) >> kShared | (row >> 4) << (3 - kShared)) * 16; }
   // base0, base1: first rows of the two 16-key groups
   static __device__ __forceinline__ void load_keys(const uint8_t* base0, const uint8_t* base1, uint32_t lds, int lane) {
     const uint32_t off = (lane & 15) * D + (lane >> 4) * 16;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      load_to_lds<STREAM>(i < kPieces ? base0 : base1, off + (i % kPieces) * 64, lds + i * 1024);
+      load_to_lds<STREAM>((i < kPieces ? base0 : base1) + (i % kPieces) * 64, off, lds + i * 1024);
   }
   static __device__ __forceinline__ void load_values(const uint8_t* base0, const uint8_t* base1, uint32_t lds, int lane) {
+    constexpr int kRows = 1024 / D;  // of an instruction
+    const uint32_t off = lane * 16 ^ turn(lane / kLane16 & 7);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      load_to_lds<STREAM>(i < kPieces ? base0 : base1, (i % kPieces) * 1024 + lane * 16, lds + kHalf + i * 1024);
+      load_to_lds<STREAM>((i < kPieces ? base0 : base1) + (i % kPieces) * 1024, off ^ turn(i * kRows), lds + kHalf + i * 1024);
+  }
+  // Where the lane reads for the transposing load of value columns 16 t .. 16 t + 15, but
+  // for an exclusive or with 16 t: of 16 lanes, two hold a row's halves.
+  static __device__ __forceinline__ uint32_t value_at(int lane) {
+    const int j = (lane & 15) >> 1, row = (j >> 2) * 16 + (lane >> 4) * 4 + (j & 3);
+    return row * D + turn(row) + (lane & 1) * 8;
   }
 };
 
-template <int D>
-__device__ __forceinline__ void load_value(uint32_t (&dst)[D / 64], const uint8_t* src) {
-  if constexpr (D == 64) {
-    dst[0] = *reinterpret_cast<const uint32_t*>(src);
-  } else if constexpr (D == 128) {
-    const uint2 x = *reinterpret_cast<const uint2*>(src);
-    dst[0] = x.x, dst[1] = x.y;
-  } else {
-    const uint4 x = *reinterpret_cast<const uint4*>(src);
-    dst[0] = x.x, dst[1] = x.y, dst[2] = x.z, dst[3] = x.w;
-  }
+// Eight values of one column each: 16 lanes read 8 rows of 16 bytes, and lane n gets the rows'
+// bytes n in their order.
+typedef int v2i __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint2 load_columns(uint32_t lds) {
+  const v2i x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i*)(uintptr_t)lds);
+  return make_uint2((uint32_t)x.x, (uint32_t)x.y);
 }
 
 // Eight codes to BF16, exactly.
@@ -299,24 +308,20 @@ __device__ __forceinline__ v8bf codes_bf16(uint32_t a, uint32_t b) {
   return v8bf{x0.x, x0.y, x1.x, x1.y, x2.x, x2.y, x3.x, x3.y};
 }
 
-// Byte e (0 .. 3) of eight words to FP16, exactly, for e and e + 1 (e even).
-__device__ __forceinline__ void columns_f16(const uint32_t (&w)[8], bool upper, v8h& even, v8h& odd) {
-  const uint32_t sel = upper ? 0x07030602u : 0x05010400u;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t x = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], sel);
-    const v2h lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, false);
-    const v2h hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, true);
-    even[2 * j] = lo.x, even[2 * j + 1] = lo.y;
-    odd[2 * j] = hi.x, odd[2 * j + 1] = hi.y;
-  }
+// Eight codes to FP16, exactly.
+__device__ __forceinline__ v8h codes_f16(uint2 w) {
+  const v2h x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, 1.0f, false);
+  const v2h x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, 1.0f, true);
+  const v2h x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, 1.0f, false);
+  const v2h x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, 1.0f, true);
+  return v8h{x0.x, x0.y, x1.x, x1.y, x2.x, x2.y, x3.x, x3.y};
 }
 
 // Exponent field of a power of two.
 __device__ __forceinline__ int exponent(uint32_t bits) { return (int)((bits >> 23) & 0xFF); }
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Not 0 if one of the four codes is NaN.
+// Bit 7 of each of the four codes that is NaN.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 // Partial results travel between workgroups (of any XCD) as device-coherent accesses.
@@ -520,12 +525,11 @@ constexpr int attention_residents(int D, int R) { return D == 64 ? (R == 1 ? 4 :
 template <int D, int R, bool STREAM, bool WIDE>
 __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kernel(const AttentionParams p) {
   using Ring = Stage<D, STREAM>;
-  constexpr int kWords = D / 64;       // 32-bit words of one value a lane feeds
   constexpr int kTiles = D / 16;       // 16-column tiles of V
   constexpr int kStride = D + 4;       // of a row of O in LDS
   // the ring, and after the loop the waves' results, 16 rows at a time
   constexpr int kRingBytes = 4 * 2 * Ring::kBytes, kResultBytes = 4 * 16 * kStride * 4;
-  __shared__ __align__(16) uint8_t shared[kRingBytes > kResultBytes ? kRingBytes : kResultBytes];
+  __shared__ __align__(256) uint8_t shared[kRingBytes > kResultBytes ? kRingBytes : kResultBytes];
   __shared__ float m_sh[4][16], mo_sh[4][16], l_sh[4][16];
   __shared__ int flag;
   auto o_sh = reinterpret_cast<float(*)[16][kStride]>(shared);
@@ -556,6 +560,7 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
   };
   const uint8_t* ring = shared + wave * 2 * Ring::kBytes;
   const uint32_t ring_lds = __builtin_amdgcn_readfirstlane(lds_address(ring));
+  const uint32_t value_at = lds_address(ring) + Ring::kHalf + Ring::value_at(lane);
   Segment g;
   auto rows_of = [&](const uint8_t* cache, int i) {
     const uint32_t lo = __builtin_amdgcn_readlane(g.at_lo, i), hi = __builtin_amdgcn_readlane(g.at_hi, i);
@@ -674,62 +679,21 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
           s1[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, qf[i][d], s1[i], 0, 0, 0);
         }
       }
-      if (left >= 2) wait_loads<3 * Ring::kLoads>();
-      else if (left == 1) wait_loads<2 * Ring::kLoads>();
-      else wait_loads<0>();
-      uint32_t v[8][kWords];  // this lane's values: key + 4 kg + j, and 16 further for j >= 4
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        load_value<D>(v[j], stage + Ring::kHalf + ((j >> 2) * 16 + kg * 4 + (j & 3)) * D + n * (D / 16));
-      if (left >= 2) {
-        wait_lds_reads();
-        fetch_values(s + 2);
-      }
       // some row does not see all of the step
-      if (rarely(key < all_lo || key + 32 > all_hi || hole != 0)) {
-        uint32_t nan_keys = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int at = key + (j >> 2) * 16 + kg * 4 + (j & 3);
-          const bool there = (hole >> (j >> 2) & 1) == 0;
-          // values that no row sees may be anything: they count as 0. Where a row sees a
-          // NaN code and another does not, the product gets 0, and o of the rows that see it
-          // becomes NaN here.
-          const bool some_see = there && at >= u.lo && at < u.hi;
-          uint32_t bad = 0;
-#pragma unroll
-          for (int w = 0; w < kWords; ++w) bad |= nan_codes(v[j][w]);
-          nan_keys |= some_see && bad != 0 ? 1u << j : 0u;
-          const uint32_t keep = some_see && bad == 0 ? ~0u : 0u;  // without branches: in place
-#pragma unroll
-          for (int w = 0; w < kWords; ++w) v[j][w] &= keep;
-        }
+      auto seen = [&](int i, int j) {
+        const int at = key + (j >> 2) * 16 + kg * 4 + (j & 3);
+        return (hole >> (j >> 2) & 1) == 0 && at >= key_lo[i] && at < key_hi[i];
+      };
+      const bool partly = key < all_lo || key + 32 > all_hi || hole != 0;
+      if (rarely(partly)) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int at = key + (j >> 2) * 16 + kg * 4 + (j & 3);
-            const bool seen = (hole >> (j >> 2) & 1) == 0 && at >= key_lo[i] && at < key_hi[i];
-            if (j < 4) s0[i][j] = seen ? s0[i][j] * c0 : -INFINITY;  // factors may be 0: they come before the mask
-            else s1[i][j - 4] = seen ? s1[i][j - 4] * c1 : -INFINITY;
+            if (j < 4) s0[i][j] = seen(i, j) ? s0[i][j] * c0 : -INFINITY;  // factors may be 0: they come before the mask
+            else s1[i][j - 4] = seen(i, j) ? s1[i][j - 4] * c1 : -INFINITY;
           }
         c0 = c1 = 1.f;
-        if (rarely(__any(nan_keys != 0))) {
-#pragma unroll
-          for (int off = 1; off < 16; off <<= 1) nan_keys |= __shfl_xor((int)nan_keys, off, 64);  // over the lanes that feed the same keys
-#pragma unroll
-          for (int i = 0; i < R; ++i) {
-            int bad = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) bad |= (nan_keys >> j & 1) && (j < 4 ? s0[i][j] : s1[i][j - 4]) > -INFINITY;
-            bad |= __shfl_xor(bad, 16, 64);
-            bad |= __shfl_xor(bad, 32, 64);
-            if (bad) {
-#pragma unroll
-              for (int t = 0; t < kTiles; ++t) o[i][t] = v4f{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
-            }
-          }
-        }
       }
       float top[R], top_o[R];
       bool move = false;
@@ -769,26 +733,62 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
         if constexpr (WIDE) pf[i] = weights(s0[i], s1[i], c0, a0[i], k0[i], l[i]);
         else pf[i] = weights(s0[i], s1[i], c0, c1, a0[i], a1[i], k0[i], k1[i], l[i]);
       }
+      if (left >= 2) wait_loads<3 * Ring::kLoads>();
+      else if (left == 1) wait_loads<2 * Ring::kLoads>();
+      else wait_loads<0>();
+      uint2 v[kTiles];  // this lane's values: keys 4 kg + j, and 16 further for j >= 4, of column 16 t + n
+      const uint32_t at_values = value_at + (s & 1) * Ring::kBytes;
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        uint32_t words[8];
+      for (int t = 0; t < kTiles; ++t) v[t] = load_columns(at_values ^ t * 16);
+      if (left >= 2) {
+        wait_lds_reads();
+        fetch_values(s + 2);
+      }
+      if (rarely(partly)) {
+        // values that no row sees may be anything: they count as 0. Where a row sees a NaN
+        // code and another does not, the product gets 0, and o of the rows that see it
+        // becomes NaN here.
+        uint32_t see[2] = {0, 0}, nan[2] = {0, 0};  // a byte for each key
 #pragma unroll
-        for (int j = 0; j < 8; ++j) words[j] = v[j][w];
+        for (int j = 0; j < 8; ++j) {
+          const int at = key + (j >> 2) * 16 + kg * 4 + (j & 3);
+          see[j >> 2] |= (hole >> (j >> 2) & 1) == 0 && at >= u.lo && at < u.hi ? 0xFFu << (j & 3) * 8 : 0u;
+        }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          v8h a, b;
-          columns_f16(words, half != 0, a, b);
+        for (int t = 0; t < kTiles; ++t) {
+          v[t].x &= see[0], v[t].y &= see[1];
+          const uint32_t x = nan_codes(v[t].x), y = nan_codes(v[t].y);
+          nan[0] |= x, nan[1] |= y;
+          v[t].x &= ~((x >> 7) * 0xFF), v[t].y &= ~((y >> 7) * 0xFF);
+        }
+        if (rarely(__any((nan[0] | nan[1]) != 0))) {
+#pragma unroll
+          for (int off = 1; off < 16; off <<= 1)  // over the lanes that feed the same keys
+            nan[0] |= __shfl_xor((int)nan[0], off, 64), nan[1] |= __shfl_xor((int)nan[1], off, 64);
 #pragma unroll
           for (int i = 0; i < R; ++i) {
-            o[i][4 * w + 2 * half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[i], o[i][4 * w + 2 * half], 0, 0, 0);
-            o[i][4 * w + 2 * half + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pf[i], o[i][4 * w + 2 * half + 1], 0, 0, 0);
+            int bad = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bad |= (nan[j >> 2] >> (8 * (j & 3) + 7) & 1) && seen(i, j);
+            bad |= __shfl_xor(bad, 16, 64);
+            bad |= __shfl_xor(bad, 32, 64);
+            if (bad) {
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) o[i][t] = v4f{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+            }
           }
         }
+      }
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const v8h a = codes_f16(v[t]);
+#pragma unroll
+        for (int i = 0; i < R; ++i) o[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pf[i], o[i][t], 0, 0, 0);
       }
     }
   }
 
-  // join the four waves: row n + 16 i's column (4 kg + j) (D / 16) + t is o[i][t][j]; then
+  // join the four waves: row n + 16 i's column 16 t + 4 kg + j is o[i][t][j]; then
   // thread (r, x) has rows r + 16 i, columns x D / 16 .. + D / 16
   RowPart<kTiles> part[R];
 #pragma unroll
@@ -797,11 +797,7 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
     l[i] += __shfl_xor(l[i], 32, 64);
     __syncthreads();  // the ring, or the rows before, have been read
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int t = 0; t < kTiles; t += 4)
-        *reinterpret_cast<float4*>(&o_sh[wave][n][(4 * kg + j) * kTiles + t]) =
-            make_float4(o[i][t][j], o[i][t + 1][j], o[i][t + 2][j], o[i][t + 3][j]);
+    for (int t = 0; t < kTiles; ++t) *reinterpret_cast<v4f*>(&o_sh[wave][n][16 * t + 4 * kg]) = o[i][t];
     if (kg == 0) m_sh[wave][n] = m[i], mo_sh[wave][n] = mo[i], l_sh[wave][n] = l[i];
     __syncthreads();
     const int r = threadIdx.x >> 4, x = threadIdx.x & 15;
