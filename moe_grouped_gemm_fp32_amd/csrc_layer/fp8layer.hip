@@ -51,13 +51,14 @@ constexpr int kMaxNormCols = 65536;
 
 // Waves that share a row, and most chunks of eight columns a thread. Forward: where rows
 // are many, as few waves as keep a row within four chunks a thread (K = 7168: 8 workgroups
-// of 4 waves on a CU); where they would not fill the GPU, one chunk a thread, for latency.
+// of 4 waves on a CU); where they would not fill the GPU, one chunk a thread, for latency
+// (K = 7168, 256 rows: 6.5 us by few waves, 5.0 by many; 700: 10.9 and 10.2; 2048: 22.7 and 24.2).
 struct NormShape {
   int waves, chunks;
 };
 NormShape norm_shape(int M, int K, int cus) {
   const int chunks = K / 8;
-  if (M < 2 * cus) {
+  if (M <= 4 * cus) {
     if (chunks <= 64) return {1, 1};
     if (chunks <= 4 * 64) return {4, 1};
     if (chunks <= 16 * 64) return {16, 1};
@@ -276,9 +277,11 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
   // page on either side for each sequence that has any.
   const int64_t pages = std::min<int64_t>(T, ceil_div(T, P) + 2 * (int64_t)std::min(B, T));
   const int64_t units = pages * Hkv * 2;
-  // A wave for each unit where a unit is a token or two (decoding) or a small page; four
-  // otherwise.
-  const bool small = T <= 2 * (int64_t)B || P * D <= 2048;
+  // A wave for each unit where its registers hold a sequence's new tokens, or pages are small,
+  // and units are many; four otherwise. Heads of 128, one wave and four: 64 users' single
+  // tokens 4.5 and 5.3 us, 16 tokens each 6.8 and 8.4, 32 each 11.2 both; 8 users' 16 tokens
+  // 5.0 and 4.2; prompts in pages of 16, 32 and 64 40 and 56, 49 and 53, 50 and 47 us.
+  const bool small = units > 2 * cus && ((int64_t)T * D <= (int64_t)fp8layer::kHeld * 64 * 16 * B || P * D <= 4096);
   const int64_t unit_groups = small ? ceil_div(units, 4) : units;
   // Queries: a token a workgroup; two where that still leaves several rounds of workgroups,
   // the second's in flight while the first is turned (8636 tokens by 32 heads of 128, with

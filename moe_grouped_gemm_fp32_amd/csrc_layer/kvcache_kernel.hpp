@@ -9,10 +9,9 @@
 // the same launch.
 //
 // Bound by memory where tokens are many (8636 tokens of 6 prompts, 32 + 2 x 8 heads of 128,
-// pages of 16: 45.1 us, 4.4 TB/s; a quarter of it are rows of 256 bytes that units of 16
-// tokens read), by the chain sequences, page, scale and tokens, amax, codes where they are
-// few (64 users, one token each: 4.5 us). More waves a CU did not help (fewer registers
-// spill: 48 us became 54 to 75).
+// pages of 16: 45.1 us, 4.4 TB/s), by the chain of sequences, page, tokens, maximum and codes
+// where they are few (64 users, one token each: 4.5 us). Fewer registers a wave, for more
+// waves on a CU, spilled: 54 to 75 us instead of 48.
 //
 // A thread handles two groups of eight columns at a time: of a rotated head, the first
 // and second members of eight pairs; of other columns, 16 in a row.
