@@ -113,6 +113,18 @@ void with_shape(NormShape s, F f) {
 // where they do not fit the L2 caches (8 of 4 MB). 4096 x 7168 BF16, without and with: norm
 // 46.0 and 40.5 us, gradient 49.0 and 45.6; the gradient of 333 x 2048 FP32, which fits: 7.3 and 8.0.
 bool streams(int M, int K, size_t bytes) { return (size_t)M * K * bytes > ((size_t)32 << 20); }
+// Whether a gradient is taken in one launch, which reads the rows twice: where they fit the
+// L2 caches and a row's chunks are one a thread. In two launches and in one: 10 x 1536 FP32
+// 5.9 and 3.7 us, 333 x 2048 7.5 and 4.9, 1024 x 2048 11.4 and 10.8 (1024 x 1024, whose rows
+// crowd into few L2 channels, 7.7 and 9.8); BF16 256 x 7168 14.0 and 6.8, 1024 x 4096 13.8
+// and 10.0.
+bool norm_grad_few(int M, int K, size_t bytes, int cus) { return M <= 4 * cus && K <= 8 * 1024 && !streams(M, K, bytes); }
+// Whether rows written to dX lie among those at p: then no workgroup may read what another
+// has finished with.
+bool rows_meet(const void* dX, int64_t lddx, const void* p, int64_t ld, int M, int K, size_t size) {
+  const uintptr_t a = (uintptr_t)dX, b = (uintptr_t)p;
+  return a < b + ((size_t)(M - 1) * ld + K) * size && b < a + ((size_t)(M - 1) * lddx + K) * size;
+}
 template <typename F>
 void with_flag(bool flag, F f) {
   if (flag) f(std::true_type{});
@@ -227,11 +239,28 @@ int fp8_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int64_t ld
   const int groups = M > 0 ? norm_grad_groups(M, s, cus) : 0;
   if (groups > 0 && (!workspace || workspace_bytes < (size_t)groups * K * sizeof(float))) return FP8GEMM_ERR_WORKSPACE;
   float* part = static_cast<float*>(workspace);
+  const size_t size = dtype == FP8GEMM_QUANT_BF16 ? 2 : 4, row_bytes = size * (dH ? 3 : 2);
+  if (M > 0 && norm_grad_few(M, K, row_bytes, cus) && !rows_meet(dX, lddx, dY, lddy, M, K, size) &&
+      !rows_meet(dX, lddx, H, ldh, M, K, size)) {
+    const fp8layer::NormGradParams p{dY, H, dH, w, rstd, dX, nullptr, lddy, ldh, lddh, lddx, M, K, w_dtype == FP8GEMM_QUANT_FP32};
+    with_type(dtype, [&](auto t) {
+      auto go = [&](auto waves) {
+        constexpr int kWaves = decltype(waves)::value;
+        hipLaunchKernelGGL((fp8layer::rmsnorm_backward_few_kernel<decltype(t), kWaves>),
+                           dim3((unsigned)(K * (int)sizeof(t) / 128 + ceil_div(M, 16 / kWaves))), dim3(1024), 0, stream, p, dW);
+      };
+      const int waves = norm_shape(M, K, cus).waves;
+      if (waves == 1) go(Int<1>{});
+      else if (waves == 4) go(Int<4>{});
+      else go(Int<16>{});
+    });
+    return launched();
+  }
   if (M > 0) {
     const fp8layer::NormGradParams p{dY, H, dH, w, rstd, dX, part, lddy, ldh, lddh, lddx, M, K, w_dtype == FP8GEMM_QUANT_FP32};
     const size_t merge = (size_t)(16 / s.waves - 1) * K * sizeof(float);  // at most 30 KB
     with_type(dtype, [&](auto t) {
-      with_flag(streams(M, K, sizeof(t) * (dH ? 3 : 2)), [&](auto nt) {
+      with_flag(streams(M, K, row_bytes), [&](auto nt) {
         with_grad_shape(s, [&](auto waves, auto chunks) {
           hipLaunchKernelGGL(
               (fp8layer::rmsnorm_backward_kernel<decltype(t), decltype(waves)::value, decltype(chunks)::value, decltype(nt)::value>),

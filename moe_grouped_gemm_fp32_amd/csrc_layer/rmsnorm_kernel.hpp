@@ -148,8 +148,7 @@ struct NormGradParams {
 // few hold partial sums of dW (in registers over all rows of the workgroup; 256 parts of
 // 28 KB for 4096 rows of 7168 columns, against 235 MB read and written). The next rows are
 // loaded before the present ones are reduced. Bound by memory: 4096 x 7168 BF16 with the
-// residual stream's gradient 45.6 us with the sums' reduction, 5.1 TB/s; 333 x 2048 FP32
-// 7.3 us, two launches of which the second waits for the first.
+// residual stream's gradient 45.6 us with the sums' reduction, 5.1 TB/s.
 template <typename T, int WPR, int CH, bool STREAM>
 __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormGradParams p) {
   constexpr int kRows = 16 / WPR;
@@ -258,6 +257,79 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormGradPa
     const int c = t + i * WPR * 64;
     if (c < chunks) store8(p.part + (int64_t)blockIdx.x * p.K + c * 8, dw[i]);
   }
+}
+
+// Backward of few rows, in one launch, for a dX that is not in dY's place (both are read by
+// other workgroups while it is written): neither result needs the other, as rstd is given. The
+// first workgroups sum dW of 128 bytes of columns each, a thread eight columns over every
+// 128th (FP32: 256th) row; the others take 16 / WPR rows each for dX. The rows are read twice, the
+// second time from L2. 333 x 2048 FP32 4.9 us, 64 x 7168 BF16 3.7, where the kernels above
+// take 7.4 and 7.6 and cost the host two launches.
+template <typename T, int WPR>
+__global__ void __launch_bounds__(1024) rmsnorm_backward_few_kernel(const NormGradParams p, float* dW) {
+  constexpr int kWaves = 16, kRows = kWaves / WPR;
+  constexpr int kLanes = 16 / sizeof(T), kCols = 8 * kLanes;  // of a slice: 128 bytes of a row
+  __shared__ float part[kWaves];
+  __shared__ __align__(16) float sums[kWaves][kCols];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int slices = p.K / kCols;
+  if ((int)blockIdx.x < slices) {
+    const int at = lane % kLanes * 8, c = blockIdx.x * kCols + at;
+    float dw[8] = {};
+#pragma unroll 4
+    for (int row = threadIdx.x / kLanes; row < p.M; row += kWaves * 64 / kLanes) {
+      float g[8], x[8];
+      load8(static_cast<const T*>(p.dY) + row * p.lddy + c, g);
+      load8(static_cast<const T*>(p.H) + row * p.ldh + c, x);
+      const float r = p.rstd[row];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dw[j] += g[j] * (x[j] * r);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)  // over the wave's rows
+#pragma unroll
+      for (int off = kLanes; off < 64; off <<= 1) dw[j] += __shfl_xor(dw[j], off, 64);
+    if (lane < kLanes) store8(&sums[wave][at], dw);
+    __syncthreads();
+    if (threadIdx.x < kCols) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) sum += sums[w][threadIdx.x];
+      dW[blockIdx.x * kCols + threadIdx.x] = sum;
+    }
+    return;
+  }
+  const int row = ((int)blockIdx.x - slices) * kRows + wave / WPR;
+  const int c = threadIdx.x & (WPR * 64 - 1);
+  const bool live = row < p.M && c < p.K >> 3;  // the barrier below is for whole rows
+  Eight<T> dy, h, dh;
+  float w[8], r = 0.f, dot = 0.f;
+  if (live) {
+    r = p.rstd[row];
+    dy.load(static_cast<const T*>(p.dY) + row * p.lddy + c * 8);
+    h.load(static_cast<const T*>(p.H) + row * p.ldh + c * 8);
+    if (p.dH) dh.load(static_cast<const T*>(p.dH) + row * p.lddh + c * 8);
+    load_weight(p.w, p.w_fp32, c, w);
+    float g[8], x[8];
+    dy.get(g);
+    h.get(x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dot += g[j] * w[j] * (x[j] * r);
+  }
+  dot = row_sum<WPR>(dot, part, wave);
+  if (!live) return;
+  const float mean = dot / (float)p.K;
+  float g[8], x[8];
+  dy.get(g);
+  h.get(x);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] = r * (g[j] * w[j] - x[j] * r * mean);
+  if (p.dH) {
+    dh.get(x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] += x[j];
+  }
+  store8(static_cast<T*>(p.dX) + row * p.lddx + c * 8, g);
 }
 
 // dW[k] = sum of the workgroups' parts, in a fixed order: four column quads by 64 slices of

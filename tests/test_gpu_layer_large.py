@@ -60,3 +60,24 @@ def test_append_of_many_tokens(cuda_device, D, P, interleaved):
         assert torch.equal(run(parts, at, table[b:b + 1], lens[b:b + 1], one), q[at])
     for a, b in zip(whole, parts):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,K", [(1, 256), (37, 2048), (700, 1152), (1024, 4096)])
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_gradient_of_few_rows_in_the_place_of_an_input(cuda_device, dtype, M, K):
+    """dX may be dY or dH itself: the weight's gradient, summed beside it, is of dY as it was."""
+    g = synth.make_generator(4, cuda_device)
+    dy, h, dh = (torch.randn(M, K, generator=g, device=cuda_device).to(dtype) for _ in range(3))
+    w = torch.randn(K, generator=g, device=cuda_device)
+    _, _, _, rstd = fg.rmsnorm_quantize_1x128(h, w)
+    dX, dW = fg.rmsnorm_backward(dy, h, rstd, w, dH=dh)
+    terms = (dy.double() * h.double() * rstd.double()[:, None])
+    bound = (M + 44) * 2.0 ** -24 * terms.abs().sum(dim=0)
+    assert bool(((dW.double() - terms.sum(dim=0)).abs() <= bound).all())
+    both = torch.cat([dy, dh], dim=1)  # views whose rows alternate, too
+    for place in (dy.clone(), dh.clone(), both[:, :K], both[:, K:]):
+        a = place if torch.equal(place, dy) else dy
+        b = place if torch.equal(place, dh) else dh
+        x, s = fg.rmsnorm_backward(a, h, rstd, w, dH=b, dX=place)
+        assert torch.equal(x, dX)
+        assert bool(((s.double() - terms.sum(dim=0)).abs() <= bound).all())
