@@ -23,15 +23,18 @@
  *           stands for c * scales[p][h].
  * Which pages hold a sequence is its row of the block table:
  *   block_table  int32 [B][ld_bt]: entry j < max_pages is the page of token slots
- *           j P .. j P + P - 1. Entries past a sequence's length are not read.
+ *           j P .. j P + P - 1. Entries past a sequence's length are not read. Slots from
+ *           max_pages P on have no page: a token there keeps its position, and is not
+ *           stored and not seen.
  *   seq_lens     int32 [B]: the sequence's length in the cache, the call's new tokens
  *           included.
  *   cu_q         int32 [B + 1]: rows cu_q[b] .. cu_q[b + 1] - 1 of the call's tokens belong to
  *           sequence b and are the last of its seq_lens[b] tokens; cu_q[0] = 0,
  *           non-decreasing. A sequence may have none.
- * These arrays are device data and are not trusted with addresses: lengths are clamped to
- * [0, max_pages P], row numbers to [0, T], and a page number outside [0, num_pages) is
- * never followed (the append writes nothing there, attention leaves its keys out).
+ * These arrays are device data and are not trusted with addresses: a length below 0 counts
+ * as 0, row numbers are clamped to [0, T], slots past the table are never looked up, and a
+ * page number outside [0, num_pages) is never followed (the append writes nothing there,
+ * attention leaves its keys out).
  * A call without rows (M, T or B is 0) does nothing and looks at no pointer to rows or to
  * these arrays.
  */
@@ -114,7 +117,8 @@ size_t fp8_rmsnorm_backward_workspace_size(int M, int K);
  * whatever it held. Values are rounded to the nearest code, ties to even; NaN and
  * infinities are stored as the NaN code and do not move the scale.
  * A page that the call appends to must belong to one sequence. Slots below 0 (more new
- * tokens than seq_lens) and past the table are dropped. Rows past cu_q[B] are untouched.
+ * tokens than seq_lens) and past the table (max_pages P and on) are dropped; their queries
+ * are rotated like all others. Rows past cu_q[B] are untouched.
  * D, P as above; rot_dim a multiple of 16, 0 .. D. q, k, v, q_out, cos_sin 16-byte
  * aligned, their strides multiples of 8 (BF16) and 4 (cos_sin) elements. T * Hq and
  * max_pages * P below 2^31.

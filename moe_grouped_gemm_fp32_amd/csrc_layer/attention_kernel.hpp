@@ -85,6 +85,10 @@ struct AttentionParams {
   Divisor by_group, by_heads;  // group, Hkv
   int cus;         // compute units
   int most_units;  // units that splitting may add; 0: no splitting
+
+  // The first key that a row at position `pos` sees. (A window may be 2^31 - 1 wide, and rows
+  // below position 0, which see none, far below it.)
+  __device__ __forceinline__ int first_key(int pos) const { return window ? max(0, max(pos, -1) - window + 1) : 0; }
 };
 
 // What a sequence asks for: its row tiles, and the most keys that one of them reads.
@@ -204,7 +208,7 @@ __device__ __forceinline__ bool find_unit(const AttentionParams& p, Plan<TILE, S
       auto pick = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
       const int tiles_incl = wave_scan(d.tiles);
       u.b = base + src;
-      u.seq = {pick(plan.seq.row0), pick(plan.seq.rows), pick(plan.seq.len)};
+      u.seq = {pick(plan.seq.row0), pick(plan.seq.rows), pick(plan.seq.start), pick(plan.seq.len)};
       u.tiles = pick(d.tiles);
       const int within = want - (before + pick(incl - count));
       u.chunk = (uint32_t)within / (uint32_t)u.tiles;
@@ -213,10 +217,9 @@ __device__ __forceinline__ bool find_unit(const AttentionParams& p, Plan<TILE, S
       const int total = u.seq.rows * p.group;
       u.row0 = u.tile * TILE;
       u.rows = min(TILE, total - u.row0);
-      const int first = u.seq.len - u.seq.rows;
-      u.pos0 = first + p.by_group.of(u.row0);
-      u.pos1 = first + p.by_group.of(u.row0 + u.rows - 1);
-      u.lo = p.window ? max(0, u.pos0 - p.window + 1) / STEP * STEP : 0;
+      u.pos0 = u.seq.start + p.by_group.of(u.row0);
+      u.pos1 = u.seq.start + p.by_group.of(u.row0 + u.rows - 1);
+      u.lo = min(p.first_key(u.pos0), u.seq.len) / STEP * STEP;
       u.hi = max(u.lo, min(u.seq.len, u.pos1 + 1));
       // as many chunks as the length asks for, of equal length
       const int keys = u.hi - u.lo;
@@ -621,9 +624,9 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
     const bool live = n + 16 * i < u.rows;
     const int row = u.row0 + (live ? n + 16 * i : 0);
     const int token = p.by_group.of(row), head = u.h * p.group + row - token * p.group;
-    const int pos = u.seq.len - u.seq.rows + token;
+    const int pos = u.seq.start + token;
     key_hi[i] = min(u.seq.len, pos + 1);
-    key_lo[i] = p.window ? max(0, pos - p.window + 1) : 0;
+    key_lo[i] = p.first_key(pos);
     const uint16_t* src = p.q + (int64_t)(u.seq.row0 + token) * p.ldq + head * D;
 #pragma unroll
     for (int s = 0; s < D / 32; ++s) {
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
       qf[i][s] = __builtin_bit_cast(v8bf, make_uint4(x.x ^ p.q_sign, x.y ^ p.q_sign, x.z ^ p.q_sign, x.w ^ p.q_sign));
     }
   // keys that every row of the tile sees
-  const int all_hi = min(u.seq.len, u.pos0 + 1), all_lo = p.window ? u.pos1 - p.window + 1 : 0;
+  const int all_hi = min(u.seq.len, u.pos0 + 1), all_lo = p.first_key(u.pos1);
 
   v4f o[R][kTiles];
   float m[R], mo[R], l[R];

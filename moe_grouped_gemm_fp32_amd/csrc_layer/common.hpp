@@ -136,16 +136,19 @@ __device__ __forceinline__ float wave_max(float v) {
 
 // The part of a sequence that a call concerns, from its device arrays, clamped to what
 // the call's host arguments allow (nothing read from these arrays becomes an address
-// unchecked).
+// unchecked). Only what is held is clamped to the table, not where the rows stand: a row
+// past the table's slots has its own position and no slot.
 struct Sequence {
-  int row0;  // its first row among the call's tokens
-  int rows;  // its number of rows
-  int len;   // its length in the cache
+  int row0;   // its first row among the call's tokens
+  int rows;   // its number of rows
+  int start;  // position of the first row: below 0 for more rows than the sequence is long
+  int len;    // its slots that the table can hold
 };
 __device__ __forceinline__ Sequence sequence(const int32_t* cu_q, const int32_t* seq_lens, int b, int T, int max_len) {
   const int q0 = min(max(cu_q[b], 0), T);
   const int q1 = min(max(cu_q[b + 1], q0), T);
-  return {q0, q1 - q0, min(max(seq_lens[b], 0), max_len)};
+  const int len = max(seq_lens[b], 0);
+  return {q0, q1 - q0, len - (q1 - q0), min(len, max_len)};
 }
 
 }  // namespace fp8layer

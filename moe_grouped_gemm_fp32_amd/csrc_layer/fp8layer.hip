@@ -405,7 +405,7 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
   p.ld_bt = ld_bt;
   p.scale_log2 = std::fabs(softmax_scale) * 1.4426950408889634f;
   p.q_sign = softmax_scale < 0.f ? 0x80008000u : 0u;
-  p.window = window >= max_len ? 0 : window;  // no key is that far back
+  p.window = window;
   p.B = B;
   p.T = T;
   p.Hq = Hq;

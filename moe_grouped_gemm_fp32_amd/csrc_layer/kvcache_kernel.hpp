@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
           sq = sequence(p.cu_q, p.seq_lens, max(b, 0), p.T, max_len);
           if (t >= sq.row0 + sq.rows) break;  // past the last sequence
         }
-        const int at = p.positions ? p.positions[t] : sq.len - (sq.row0 + sq.rows - t);
+        const int at = p.positions ? p.positions[t] : sq.start + (t - sq.row0);
         const float* cs = p.cos_sin + min(max(at, 0), p.max_pos - 1) * p.ld_cs;
         const Eight<uint16_t> lo0 = lo, hi0 = hi;
         fetch(t + 1);
@@ -158,15 +158,15 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
     int count = 0, page0 = 0;
     if (base + lane < p.B) {
       mine = sequence(p.cu_q, p.seq_lens, base + lane, p.T, max_len);
-      page0 = max(mine.len - mine.rows, 0) >> p.log_p;
-      if (mine.rows > 0 && mine.len > 0) count = ((mine.len - 1) >> p.log_p) - page0 + 1;
+      page0 = max(mine.start, 0) >> p.log_p;
+      if (mine.rows > 0 && mine.start < mine.len) count = ((mine.len - 1) >> p.log_p) - page0 + 1;
     }
     const int incl = wave_scan(count);
     const uint64_t hit = __ballot(want < done + incl);
     if (hit) {
       const int src = __ffsll((unsigned long long)hit) - 1;
       auto pick = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
-      sq = {pick(mine.row0), pick(mine.rows), pick(mine.len)};
+      sq = {pick(mine.row0), pick(mine.rows), pick(mine.start), pick(mine.len)};
       first_page = pick(page0) + want - (done + pick(incl - count));
       done = base + src;  // the sequence, from here on
       found = true;
@@ -177,11 +177,10 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
   if (!found) return;  // the grid covers the most units that there can be (all waves of a shared unit agree)
   const int page = p.block_table[done * p.ld_bt + first_page];
   if (page < 0 || page >= p.num_pages) return;
-  const int start = sq.len - sq.rows;  // slot of the sequence's first new token
   const int slot0 = first_page << p.log_p;
-  const int from = max(start - slot0, 0);           // earlier tokens of this page: [0, from)
+  const int from = max(sq.start - slot0, 0);        // earlier tokens of this page: [0, from)
   const int to = min(sq.len - slot0, P);            // new ones: [from, to)
-  const int row_at = sq.row0 - start + slot0;       // row of slot 0 of the page
+  const int row_at = sq.row0 - sq.start + slot0;       // row of slot 0 of the page
   const uint16_t* src = keys ? p.k : p.v;
   const int64_t ld = keys ? p.ldk : p.ldv;
   const int64_t head = (int64_t)page * p.Hkv + h;

@@ -147,7 +147,8 @@ def rope_append_paged_kv(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Te
     slots in their sequences, clamped to the table). q_out may be q itself.
     A page's scale is the smallest power of two by which what was appended fits e4m3; when
     it has to grow, the page's earlier codes are re-encoded. block_table, seq_lens, cu_q:
-    see the module's text; seq_lens counts the new tokens."""
+    see the module's text; seq_lens counts the new tokens. Tokens past the table's slots are
+    not stored."""
     return (_native or _calls()).rope_append(q, k, v, cos_sin, cache, block_table, seq_lens, cu_q, positions, interleaved,
                                              q_out, stream)
 
