@@ -149,8 +149,8 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
  *        size may be given; fp8_paged_attention_workspace_size() suffices for every call.
  *        Calls that may run at the same time must not share it.
  * NaN codes in slots that no row sees change nothing; a row that sees one gives NaN.
- * Hkv divides Hq. q, O 16-byte aligned with strides multiples of 8; T * Hq and
- * max_pages * P below 2^31; window >= 0; num_pages >= 1.
+ * Hkv divides Hq. q, O 16-byte aligned with strides multiples of 8; T * Hq below 2^31,
+ * max_pages * P at most 2^30; window >= 0; num_pages >= 1.
  */
 int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const float* k_scale, const void* v_cache,
                         const float* v_scale, int num_pages, int P, const int32_t* block_table, int64_t ld_bt,

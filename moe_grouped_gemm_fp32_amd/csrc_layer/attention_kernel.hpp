@@ -57,6 +57,8 @@ constexpr int kTileCounters = 8192;     // arrival counters at the workspace's s
 constexpr int kPartCounters = 8192;     // and of groups of parts
 constexpr int kCounters = kTileCounters + kPartCounters;
 constexpr int kMinChunk = 128;          // least keys of a unit: one step for each wave
+constexpr int kMostKeys = 1 << 30;      // most keys of a sequence: key numbers a segment further fit 32 bits,
+constexpr int kWhole = kMostKeys;       // and a chunk of so many leaves every tile whole
 constexpr int kJoin = 8;                // parts joined at a time, all loads in flight together
 // Where a page's values are so small that even the likeliest key adds less than 2^-60 of
 // what o holds, w keeps this much below the likeliest key's 2^0 instead, for l's sake.
@@ -91,6 +93,13 @@ struct AttentionParams {
   __device__ __forceinline__ int first_key(int pos) const { return window ? max(0, max(pos, -1) - window + 1) : 0; }
 };
 
+// Chunks of `len` keys that `keys` keys make, and keys rounded up to whole steps of four waves.
+// A tile that may not be cut is one chunk at every length that a call can have.
+constexpr __host__ __device__ int pieces(int keys, int len) { return (int)(((uint32_t)keys + (uint32_t)len - 1) / (uint32_t)len); }
+constexpr __host__ __device__ int up128(int keys) { return (int)(((uint32_t)keys + 127) / 128 * 128); }
+static_assert(pieces(kMostKeys, kWhole) == 1 && pieces(kMostKeys, up128((int)(float)kWhole)) == 1 && up128(kMostKeys) == kMostKeys);
+static_assert((int64_t)kMostKeys + 64 * 32 <= INT32_MAX);
+
 // What a sequence asks for: its row tiles, and the most keys that one of them reads.
 struct Demand {
   int tiles, keys;
@@ -122,9 +131,7 @@ struct Plan {
   Demand want;
   int chunk_len;
 
-  __device__ __forceinline__ int chunks_of(int keys) const {
-    return (int)(((uint32_t)keys + (uint32_t)chunk_len - 1) / (uint32_t)chunk_len);
-  }
+  __device__ __forceinline__ int chunks_of(int keys) const { return pieces(keys, chunk_len); }
   __device__ __forceinline__ void look(const AttentionParams& p, int base) {
     const int b = base + (threadIdx.x & 63);
     seq = {}, want = {};
@@ -134,11 +141,11 @@ struct Plan {
     }
   }
   __device__ __forceinline__ int rounded(float chunk) const {
-    return max(kMinChunk, ((int)fminf(chunk, 1e9f) + 127) / 128 * 128);
+    return max(kMinChunk, up128((int)fminf(chunk, (float)kWhole)));
   }
   // unit_cost: kUnitCost for the call's head size.
   __device__ __forceinline__ void make(const AttentionParams& p, float unit_cost) {
-    chunk_len = 1 << 30;
+    chunk_len = kWhole;
     if (p.most_units == 0) return;
     // in FP32: every wave of the call gets the same sums
     float keys = 0.f, tiles = 0.f, most = 0.f;
@@ -223,12 +230,11 @@ __device__ __forceinline__ bool find_unit(const AttentionParams& p, Plan<TILE, S
       u.hi = max(u.lo, min(u.seq.len, u.pos1 + 1));
       // as many chunks as the length asks for, of equal length
       const int keys = u.hi - u.lo;
-      const uint32_t wanted = max(1, plan.chunks_of(keys));
-      const uint32_t len = max(128u, (((uint32_t)keys + wanted - 1) / wanted + 127) / 128 * 128);
-      u.chunks = max(1, (int)(((uint32_t)keys + len - 1) / len));
+      const int len = max(kMinChunk, up128(pieces(keys, max(1, plan.chunks_of(keys)))));
+      u.chunks = max(1, pieces(keys, len));
       if (u.chunk >= u.chunks) return false;  // a tile that sees fewer keys than the sequence's last
-      u.k0 = (int)min((uint32_t)u.hi, u.lo + u.chunk * len);
-      u.k1 = (int)min((uint32_t)u.hi, u.k0 + len);
+      u.k0 = min(u.hi, u.lo + u.chunk * len);
+      u.k1 = (int)min((uint32_t)u.hi, (uint32_t)u.k0 + len);
       return true;
     }
     before += last_lane(incl);

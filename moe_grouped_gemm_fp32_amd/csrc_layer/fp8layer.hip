@@ -377,7 +377,7 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
       (T != 0 && B != 0 && (!q || !block_table || !seq_lens || !cu_q || !O)))
     return FP8GEMM_ERR_NULL;
   if (!cache_shape(num_pages, P, Hkv, D) || B < 0 || T < 0 || Hq < 1 || Hq % Hkv != 0 || max_pages < 0 || window < 0 ||
-      !std::isfinite(softmax_scale) || (int64_t)T * Hq >= INT32_MAX - 256 || (int64_t)max_pages * P > INT32_MAX)
+      !std::isfinite(softmax_scale) || (int64_t)T * Hq >= INT32_MAX - 256 || (int64_t)max_pages * P > fp8layer::kMostKeys)
     return FP8GEMM_ERR_SHAPE;
   if (B == 0 || T == 0) return FP8GEMM_OK;
   if (ldq < (int64_t)Hq * D || ldq % 8 || ldo < (int64_t)Hq * D || ldo % 8 || ld_bt < max_pages) return FP8GEMM_ERR_LAYOUT;
