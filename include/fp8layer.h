@@ -34,7 +34,8 @@
  * These arrays are device data and are not trusted with addresses: a length below 0 counts
  * as 0, row numbers are clamped to [0, T], slots past the table are never looked up, and a
  * page number outside [0, num_pages) is never followed (the append writes nothing there,
- * attention leaves its keys out).
+ * attention leaves its keys out). Offsets in cu_q that overlap give rows of no meaning, and
+ * no access outside the arrays.
  * A call without rows (M, T or B is 0) does nothing and looks at no pointer to rows or to
  * these arrays.
  */

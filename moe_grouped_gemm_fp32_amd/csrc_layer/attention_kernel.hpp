@@ -218,6 +218,7 @@ __device__ __forceinline__ bool find_unit(const AttentionParams& p, Plan<TILE, S
       u.seq = {pick(plan.seq.row0), pick(plan.seq.rows), pick(plan.seq.start), pick(plan.seq.len)};
       u.tiles = pick(d.tiles);
       const int within = want - (before + pick(incl - count));
+      if ((uint32_t)within >= (uint32_t)pick(count)) return false;  // only where overlapping rows overflow the sums
       u.chunk = (uint32_t)within / (uint32_t)u.tiles;
       u.tile = u.tiles - 1 - (within - u.chunk * u.tiles);  // the tiles with the most keys first
       u.tile_id = (tiles_before + pick(tiles_incl - d.tiles) + u.tile) * p.Hkv + u.h;
@@ -232,9 +233,15 @@ __device__ __forceinline__ bool find_unit(const AttentionParams& p, Plan<TILE, S
       const int keys = u.hi - u.lo;
       const int len = max(kMinChunk, up128(pieces(keys, max(1, plan.chunks_of(keys)))));
       u.chunks = max(1, pieces(keys, len));
-      if (u.chunk >= u.chunks) return false;  // a tile that sees fewer keys than the sequence's last
+      // Where rows overlap (cu_q is not trusted), more units can be asked for than there are: a
+      // tile whose chunks do not all have a workgroup and a slot, or whose counter would not be
+      // a tile's, stays whole, so that everyone whom a counter waits for arrives.
+      const int64_t last_slot = number + (int64_t)(u.chunks - 1 - u.chunk) * u.tiles * p.Hkv;
+      const bool whole = u.chunks > 1 && (last_slot >= (int64_t)gridDim.x || u.tile_id >= kTileCounters);
+      if (whole) u.chunks = 1;
+      if (u.chunk >= u.chunks) return false;  // also a tile that sees fewer keys than the sequence's last
       u.k0 = min(u.hi, u.lo + u.chunk * len);
-      u.k1 = (int)min((uint32_t)u.hi, (uint32_t)u.k0 + len);
+      u.k1 = whole ? u.hi : (int)min((uint32_t)u.hi, (uint32_t)u.k0 + len);
       return true;
     }
     before += last_lane(incl);

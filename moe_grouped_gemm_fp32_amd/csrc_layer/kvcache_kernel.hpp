@@ -167,7 +167,9 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
       const int src = __ffsll((unsigned long long)hit) - 1;
       auto pick = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
       sq = {pick(mine.row0), pick(mine.rows), pick(mine.start), pick(mine.len)};
-      first_page = pick(page0) + want - (done + pick(incl - count));
+      const int within = want - (done + pick(incl - count));
+      if ((uint32_t)within >= (uint32_t)pick(count)) return;  // only where overlapping rows overflow the sums
+      first_page = pick(page0) + within;
       done = base + src;  // the sequence, from here on
       found = true;
     } else {
