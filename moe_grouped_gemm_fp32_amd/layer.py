@@ -104,7 +104,7 @@ def rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, weig
     workspace: optional uint8 buffer, fp8_rmsnorm_backward_workspace_size(M, K) bytes;
     allocated if not given."""
     calls = _native or _calls()
-    if workspace is None and stream is not None:
+    if workspace is None and stream is not None and isinstance(dY, torch.Tensor) and dY.is_cuda and dY.dim() == 2:
         with torch.cuda.device(dY.device):
             size = _fn("fp8_rmsnorm_backward_workspace_size")(*dY.shape)
         workspace = torch.empty(size, dtype=torch.uint8, device=dY.device)

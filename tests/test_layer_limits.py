@@ -1,6 +1,8 @@
 """Limits and promises of the layer operators that need no GPU to be checked."""
+import pytest
 import torch
 
+import moe_grouped_gemm_fp32_amd as fg
 from test_layer_abi import ATTEND, DEVICE, SHAPE, call
 
 
@@ -10,3 +12,10 @@ def test_attention_takes_tables_of_2_to_the_30_slots():
         assert call("fp8_paged_attention", ATTEND, P=P, max_pages=pages + 1, ld_bt=pages + 1) == SHAPE
         if not torch.cuda.is_available():  # the arguments are good and their addresses are not
             assert call("fp8_paged_attention", ATTEND, P=P, max_pages=pages, ld_bt=pages) == DEVICE
+
+
+def test_what_is_no_gpu_tensor_is_refused_on_another_stream_as_well():
+    x = torch.zeros(4, 256)
+    for bad, error in ((7, TypeError), ([1.0], TypeError), (None, TypeError), (x, ValueError), (x[0], ValueError)):
+        with pytest.raises(error):
+            fg.rmsnorm_backward(bad, x, x[:, 0], x[0], stream=object())
