@@ -10,8 +10,12 @@
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/StreamGuard.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/Stream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <climits>
 #include <cmath>
@@ -32,8 +36,9 @@ struct Library {
   decltype(&fp8_rope_append_paged_kv) append;
   decltype(&fp8_paged_attention) attend;
   decltype(&fp8_gemm_scale_ld) scale_ld;
-  PyObject* check;           // check(status, name) raises
-  PyObject* current_stream;  // current_stream(device index): its raw handle
+  PyObject* check;            // check(status, name) raises
+  PyObject* current_stream;   // current_stream(device index): its raw handle
+  PyObject* external_stream;  // external_stream(raw handle, device index): a torch stream
 } library;
 
 // ----------------------------------------------------------------------------- arguments
@@ -94,26 +99,52 @@ void* vector(const Tensor& t, const char* name, int64_t n, ScalarType type, Devi
 void* weight(const Tensor& t, int64_t K, Device dev) {
   return vector(t, "weight", K, t.scalar_type() == at::kBFloat16 ? at::kBFloat16 : at::kFloat, dev);
 }
-// The tensor that was given, or a new one.
-Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, ScalarType type, Device dev) {
-  return given(o) ? tensor(o, name) : at::empty(shape, at::TensorOptions().dtype(type).device(dev));
-}
 
-hipStream_t stream_of(PyObject* stream, Device dev) {
-  PyObject* raw;
-  if (given(stream)) {
-    raw = PyObject_GetAttrString(stream, "cuda_stream");
-  } else {
-    PyObject* index = PyLong_FromLong(dev.index());
-    raw = index ? PyObject_CallFunctionObjArgs(library.current_stream, index, nullptr) : nullptr;
-    Py_XDECREF(index);
+// The stream that a call runs on. While this lives it is the current one, so that what the call
+// allocates is not memory on which earlier work of the caller's stream is still queued.
+class Launch {
+ public:
+  Launch(PyObject* stream, Device dev) : dev_(dev) {
+    THPObjectPtr index(PyLong_FromLong(dev.index()));
+    if (!index) throw python_error();
+    THPObjectPtr raw(given(stream) ? PyObject_GetAttrString(stream, "cuda_stream")
+                                   : PyObject_CallFunctionObjArgs(library.current_stream, index.get(), nullptr));
+    if (!raw) throw python_error();
+    void* const p = PyLong_AsVoidPtr(raw);
+    if (!p && PyErr_Occurred()) throw python_error();
+    handle_ = static_cast<hipStream_t>(p);
+    if (!given(stream)) return;
+    THPObjectPtr made;  // of an object that has only the handle
+    if (!THPStream_Check(stream)) {
+      made = PyObject_CallFunctionObjArgs(library.external_stream, raw.get(), index.get(), nullptr);
+      if (!made) throw python_error();
+      stream = made;
+    }
+    const auto* const s = reinterpret_cast<const THPStream*>(stream);
+    const auto to =
+        c10::Stream::unpack3(s->stream_id, (c10::DeviceIndex)s->device_index, static_cast<c10::DeviceType>(s->device_type));
+    TORCH_CHECK_VALUE(to.device() == dev, "stream must be one of ", dev);
+    if (to != c10::impl::VirtualGuardImpl(dev.type()).getStream(dev)) guard_.reset_stream(to);
   }
-  if (!raw) throw python_error();
-  void* p = PyLong_AsVoidPtr(raw);
-  Py_DECREF(raw);
-  if (!p && PyErr_Occurred()) throw python_error();
-  return static_cast<hipStream_t>(p);
-}
+
+  hipStream_t handle() const { return handle_; }
+
+  Tensor scratch(at::IntArrayRef shape, ScalarType type) const {
+    return at::empty(shape, at::TensorOptions().dtype(type).device(dev_));
+  }
+  // The tensor that was given, or a new one. The caller will use it on its own stream.
+  Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, ScalarType type) const {
+    if (given(o)) return tensor(o, name);
+    Tensor t = scratch(shape, type);
+    if (const auto caller = guard_.original_stream()) t.record_stream(*caller);
+    return t;
+  }
+
+ private:
+  Device dev_;
+  hipStream_t handle_;
+  c10::OptionalStreamGuard guard_;
+};
 
 // Calls the library without Python's lock (a full queue makes a launch wait).
 template <typename F>
@@ -190,6 +221,7 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   norm_rows(X, "X");
   const Device dev = X.device();
   const c10::DeviceGuard guard(dev);
+  const Launch launch(a[9], dev);
   const int64_t M = X.size(0), K = X.size(1);
   const Tensor& w = tensor(a[1], "weight");
   void* const wp = weight(w, K, dev);
@@ -200,14 +232,14 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (given(a[2])) {
     const Tensor& R = tensor(a[2], "residual");
     ldr = matrix(R, "residual", M, K, X.scalar_type(), dev), r = R.data_ptr();
-    H = output(a[6], "H", {M, K}, X.scalar_type(), dev);
+    H = launch.output(a[6], "H", {M, K}, X.scalar_type());
     ldh = matrix(H, "H", M, K, X.scalar_type(), dev), h = H.data_ptr();
   } else {
     TORCH_CHECK_VALUE(!given(a[6]) || a[6] == a[0], "H is written only with a residual");
   }
-  const Tensor Q = output(a[4], "Q", {M, K}, at::kByte, dev);
-  const Tensor sa = output(a[5], "sa", {K / 128, given(a[5]) ? 0 : library.scale_ld(to_int(M, "M"))}, at::kFloat, dev);
-  const Tensor rstd = output(a[7], "rstd", {M}, at::kFloat, dev);
+  const Tensor Q = launch.output(a[4], "Q", {M, K}, at::kByte);
+  const Tensor sa = launch.output(a[5], "sa", {K / 128, given(a[5]) ? 0 : library.scale_ld(to_int(M, "M"))}, at::kFloat);
+  const Tensor rstd = launch.output(a[7], "rstd", {M}, at::kFloat);
   const int64_t ldq = matrix(Q, "Q", M, K, codes_type(Q) ? Q.scalar_type() : at::kByte, dev);
   TORCH_CHECK_VALUE(sa.scalar_type() == at::kFloat && sa.dim() == 2 && sa.size(0) == K / 128 && sa.size(1) >= M && sa.stride(1) == 1 &&
                         sa.device() == dev,
@@ -219,10 +251,9 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float eps = to_float(a[3]);
   const int rows = to_int(M, "M"), cols = to_int(K, "K");
   auto* const rstd_p = static_cast<float*>(vector(rstd, "rstd", M, at::kFloat, dev));
-  const hipStream_t stream = stream_of(a[9], dev);
   call("fp8_rmsnorm_quantize_1x128", [&] {
     return library.norm(X.data_ptr(), row_stride(X), r, ldr, type_code(X), wp, type_code(w), eps, h, ldh, y, ldy, rstd_p, Q.data_ptr(), ldq,
-                        static_cast<float*>(sa.data_ptr()), row_stride(sa), rows, cols, stream);
+                        static_cast<float*>(sa.data_ptr()), row_stride(sa), rows, cols, launch.handle());
   });
   return Py_BuildValue("NNNN", THPVariable_Wrap(Q), THPVariable_Wrap(sa), THPVariable_Wrap(H), THPVariable_Wrap(rstd));
   END_HANDLE_TH_ERRORS
@@ -236,6 +267,7 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   norm_rows(dY, "dY");
   const Device dev = dY.device();
   const c10::DeviceGuard guard(dev);
+  const Launch launch(a[8], dev);
   const int64_t M = dY.size(0), K = dY.size(1);
   const ScalarType type = dY.scalar_type();
   const Tensor &H = tensor(a[1], "H"), &rstd = tensor(a[2], "rstd"), &w = tensor(a[3], "weight");
@@ -248,17 +280,17 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& dH = tensor(a[4], "dH");
     lddh = matrix(dH, "dH", M, K, type, dev), dh = dH.data_ptr();
   }
-  const Tensor dX = output(a[5], "dX", {M, K}, type, dev);
+  const Tensor dX = launch.output(a[5], "dX", {M, K}, type);
   const int64_t lddx = matrix(dX, "dX", M, K, type, dev);
-  const Tensor dW = output(a[6], "dW", {K}, at::kFloat, dev);
+  const Tensor dW = launch.output(a[6], "dW", {K}, at::kFloat);
   auto* const dw = static_cast<float*>(vector(dW, "dW", K, at::kFloat, dev));
   const int rows = to_int(M, "M"), cols = to_int(K, "K");
-  const Tensor ws = output(a[7], "workspace", {given(a[7]) ? 0 : (int64_t)library.norm_grad_workspace(rows, cols)}, at::kByte, dev);
+  const Tensor ws =
+      given(a[7]) ? tensor(a[7], "workspace") : launch.scratch({(int64_t)library.norm_grad_workspace(rows, cols)}, at::kByte);
   TORCH_CHECK_VALUE(ws.device() == dev && ws.is_contiguous(), "workspace must be contiguous on dY's device");
-  const hipStream_t stream = stream_of(a[8], dev);
   call("fp8_rmsnorm_backward", [&] {
     return library.norm_grad(dY.data_ptr(), row_stride(dY), H.data_ptr(), ldh, dh, lddh, type_code(dY), rstd_p, wp, type_code(w),
-                             dX.data_ptr(), lddx, dw, rows, cols, ws.data_ptr(), ws.nbytes(), stream);
+                             dX.data_ptr(), lddx, dw, rows, cols, ws.data_ptr(), ws.nbytes(), launch.handle());
   });
   return Py_BuildValue("NN", THPVariable_Wrap(dX), THPVariable_Wrap(dW));
   END_HANDLE_TH_ERRORS
@@ -271,6 +303,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& k = gpu_tensor(a[1], "k", 3);
   const Device dev = k.device();
   const c10::DeviceGuard guard(dev);
+  const Launch launch(a[11], dev);
   const int64_t T = k.size(0), Hkv = k.size(1), D = k.size(2);
   const Cache c = cache_of(a[4], dev);
   TORCH_CHECK_VALUE(c.heads == Hkv && c.dim == D, "the cache has other heads than k");
@@ -284,7 +317,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& Q = gpu_tensor(a[0], "q", 3);
     Hq = Q.size(1);
     ldq = heads(Q, "q", T, Hq, D, dev), q = Q.data_ptr();
-    q_out = output(a[10], "q_out", {T, Hq, D}, at::kBFloat16, dev);
+    q_out = launch.output(a[10], "q_out", {T, Hq, D}, at::kBFloat16);
     ldqo = heads(q_out, "q_out", T, Hq, D, dev), qo = q_out.data_ptr();
   } else {
     TORCH_CHECK_VALUE(!given(a[10]), "q_out without q");
@@ -305,12 +338,11 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int interleaved = PyObject_IsTrue(a[9]);
   if (interleaved < 0) throw python_error();
   const int tokens = to_int(T, "T"), q_heads = to_int(Hq, "Hq");
-  const hipStream_t stream = stream_of(a[11], dev);
   call("fp8_rope_append_paged_kv", [&] {
     return library.append(q, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, table, ld_cs, max_pos, rot_dim, interleaved, positions, s.table,
                           s.stride, s.pages, s.lens, s.cu, qo, ldqo, c.k.data_ptr(), static_cast<float*>(c.k_scale.data_ptr()),
                           c.v.data_ptr(), static_cast<float*>(c.v_scale.data_ptr()), c.num_pages, c.page, s.count, tokens, q_heads,
-                          c.heads, c.dim, stream);
+                          c.heads, c.dim, launch.handle());
   });
   if (!q_out.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(q_out);
@@ -324,11 +356,12 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& q = gpu_tensor(a[0], "q", 3);
   const Device dev = q.device();
   const c10::DeviceGuard guard(dev);
+  const Launch launch(a[10], dev);
   const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2);
   const Cache c = cache_of(a[1], dev);
   TORCH_CHECK_VALUE(c.dim == D && c.heads != 0 && Hq % c.heads == 0, "q's heads do not match the cache's");
   const int64_t ldq = heads(q, "q", T, Hq, D, dev);
-  const Tensor out = output(a[5], "out", {T, Hq, D}, at::kBFloat16, dev);
+  const Tensor out = launch.output(a[5], "out", {T, Hq, D}, at::kBFloat16);
   const int64_t ldo = heads(out, "out", T, Hq, D, dev);
   float* lse = nullptr;
   if (given(a[6])) {
@@ -348,20 +381,20 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const float scale = given(a[7]) ? to_float(a[7]) : (float)(1.0 / std::sqrt((double)D));
   const int window = to_int(a[8], "window"), tokens = to_int(T, "T"), q_heads = to_int(Hq, "Hq");
-  const hipStream_t stream = stream_of(a[10], dev);
   call("fp8_paged_attention", [&] {
     return library.attend(q.data_ptr(), ldq, c.k.data_ptr(), static_cast<const float*>(c.k_scale.data_ptr()), c.v.data_ptr(),
                           static_cast<const float*>(c.v_scale.data_ptr()), c.num_pages, c.page, s.table, s.stride, s.pages, s.lens, s.cu,
-                          out.data_ptr(), ldo, lse, scale, window, s.count, tokens, q_heads, c.heads, c.dim, ws, ws_bytes, stream);
+                          out.data_ptr(), ldo, lse, scale, window, s.count, tokens, q_heads, c.heads, c.dim, ws, ws_bytes,
+                          launch.handle());
   });
   return THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }
 
-// The library's functions as a dict of addresses by name, check, current_stream
+// The library's functions as a dict of addresses by name, check, current_stream, external_stream
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 3);
+  arguments(n, 4);
   TORCH_CHECK_TYPE(PyDict_Check(a[0]), "expected a dict of addresses");
   auto set = [&](auto& f, const char* name) {
     PyObject* at = PyDict_GetItemString(a[0], name);
@@ -375,8 +408,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   set(library.append, "fp8_rope_append_paged_kv");
   set(library.attend, "fp8_paged_attention");
   set(library.scale_ld, "fp8_gemm_scale_ld");
-  Py_INCREF(a[1]), Py_INCREF(a[2]);
-  library.check = a[1], library.current_stream = a[2];
+  Py_INCREF(a[1]), Py_INCREF(a[2]), Py_INCREF(a[3]);
+  library.check = a[1], library.current_stream = a[2], library.external_stream = a[3];
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

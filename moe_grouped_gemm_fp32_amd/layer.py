@@ -14,6 +14,10 @@ sequence, and which rows of a call are its new tokens, is given by three int32 t
 block_table [B, max_pages], seq_lens [B] (new tokens included) and cu_q [B + 1] (row
 offsets of the sequences' new tokens). They are read on the device only, so every call may
 be captured into a graph.
+
+Calls take a `stream`, the current one by default. What a call allocates belongs to the stream
+it runs on, as under torch.cuda.stream(), and stays allocated until the work that the current
+stream had when it was let go of is done.
 """
 from __future__ import annotations
 
@@ -73,7 +77,7 @@ def _calls():
         loader.exec_module(module)
         names = [*_SIGS, "fp8_gemm_scale_ld"]
         address = {n: ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names}
-        module.bind(address, _check, torch._C._cuda_getCurrentRawStream)
+        module.bind(address, _check, torch._C._cuda_getCurrentRawStream, torch.cuda.ExternalStream)
         _native = module
     return _native
 
@@ -103,13 +107,7 @@ def rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, weig
     gradient of X and of the residual alike, and may be dY or dH itself; dW is float32 [K].
     workspace: optional uint8 buffer, fp8_rmsnorm_backward_workspace_size(M, K) bytes;
     allocated if not given."""
-    calls = _native or _calls()
-    if workspace is None and stream is not None and isinstance(dY, torch.Tensor) and dY.is_cuda and dY.dim() == 2:
-        with torch.cuda.device(dY.device):
-            size = _fn("fp8_rmsnorm_backward_workspace_size")(*dY.shape)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dY.device)
-        workspace.record_stream(stream)  # used there after this function has let go of it
-    return calls.rmsnorm_backward(dY, H, rstd, weight, dH, dX, dW, workspace, stream)
+    return (_native or _calls()).rmsnorm_backward(dY, H, rstd, weight, dH, dX, dW, workspace, stream)
 
 
 class PagedKVCache(NamedTuple):
