@@ -253,7 +253,8 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   auto* const rstd_p = static_cast<float*>(vector(rstd, "rstd", M, at::kFloat, dev));
   call("fp8_rmsnorm_quantize_1x128", [&] {
     return library.norm(X.data_ptr(), row_stride(X), r, ldr, type_code(X), wp, type_code(w), eps, h, ldh, y, ldy, rstd_p, Q.data_ptr(), ldq,
-                        static_cast<float*>(sa.data_ptr()), row_stride(sa), rows, cols, launch.handle());
+                        static_cast<float*>(sa.data_ptr()), sa.size(0) > 1 ? sa.stride(0) : library.scale_ld(sa.size(1)), rows, cols,
+                        launch.handle());
   });
   return Py_BuildValue("NNNN", THPVariable_Wrap(Q), THPVariable_Wrap(sa), THPVariable_Wrap(H), THPVariable_Wrap(rstd));
   END_HANDLE_TH_ERRORS
