@@ -37,7 +37,7 @@
  * attention leaves its keys out). Offsets in cu_q that overlap give rows of no meaning, and
  * no access outside the arrays.
  * A call without rows (M, T or B is 0) does nothing and looks at no pointer to rows or to
- * these arrays.
+ * these arrays. A table without pages (max_pages 0) may be NULL: nothing is stored or seen.
  */
 #ifndef FP8LAYER_H_
 #define FP8LAYER_H_

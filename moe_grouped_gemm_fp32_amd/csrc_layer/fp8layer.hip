@@ -283,7 +283,7 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
                              float* k_scale, void* v_cache, float* v_scale, int num_pages, int P, int B, int T, int Hq,
                              int Hkv, int D, hipStream_t stream) {
   if (!k_cache || !k_scale || !v_cache || !v_scale ||
-      (T != 0 && B != 0 && (!k || !v || !block_table || !seq_lens || !cu_q || (q == nullptr) != (q_out == nullptr) ||
+      (T != 0 && B != 0 && (!k || !v || (max_pages > 0 && !block_table) || !seq_lens || !cu_q || (q == nullptr) != (q_out == nullptr) ||
                             (rot_dim > 0 && !cos_sin))))
     return FP8GEMM_ERR_NULL;
   if (!cache_shape(num_pages, P, Hkv, D) || B < 0 || T < 0 || Hq < 1 || max_pages < 0 || rot_dim < 0 || rot_dim > D ||
@@ -374,7 +374,7 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
                         float softmax_scale, int window, int B, int T, int Hq, int Hkv, int D, void* workspace,
                         size_t workspace_bytes, hipStream_t stream) {
   if (!k_cache || !k_scale || !v_cache || !v_scale ||
-      (T != 0 && B != 0 && (!q || !block_table || !seq_lens || !cu_q || !O)))
+      (T != 0 && B != 0 && (!q || (max_pages > 0 && !block_table) || !seq_lens || !cu_q || !O)))
     return FP8GEMM_ERR_NULL;
   if (!cache_shape(num_pages, P, Hkv, D) || B < 0 || T < 0 || Hq < 1 || Hq % Hkv != 0 || max_pages < 0 || window < 0 ||
       !std::isfinite(softmax_scale) || (int64_t)T * Hq >= INT32_MAX - 256 || (int64_t)max_pages * P > fp8layer::kMostKeys)

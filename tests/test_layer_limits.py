@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import moe_grouped_gemm_fp32_amd as fg
-from test_layer_abi import ATTEND, DEVICE, SHAPE, call
+from test_layer_abi import APPEND, ATTEND, DEVICE, NULL, SHAPE, call
 
 
 def test_attention_takes_tables_of_2_to_the_30_slots():
@@ -19,3 +19,10 @@ def test_what_is_no_gpu_tensor_is_refused_on_another_stream_as_well():
     for bad, error in ((7, TypeError), ([1.0], TypeError), (None, TypeError), (x, ValueError), (x[0], ValueError)):
         with pytest.raises(error):
             fg.rmsnorm_backward(bad, x, x[:, 0], x[0], stream=object())
+
+
+def test_a_table_without_pages_may_have_no_address():
+    for name, defaults in (("fp8_rope_append_paged_kv", APPEND), ("fp8_paged_attention", ATTEND)):
+        assert call(name, defaults, block_table=None, max_pages=1, ld_bt=1) == NULL
+        if not torch.cuda.is_available():
+            assert call(name, defaults, block_table=None, max_pages=0, ld_bt=0) == DEVICE
