@@ -87,6 +87,7 @@ struct AttentionParams {
   Divisor by_group, by_heads;  // group, Hkv
   int cus;         // compute units
   int most_units;  // units that splitting may add; 0: no splitting
+  int first_unit;  // the launch's first unit (0 with splitting)
 
   // The first key that a row at position `pos` sees. (A window may be 2^31 - 1 wide, and rows
   // below position 0, which see none, far below it.)
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kern
   Plan<16 * R, 32> plan;
   plan.make(p, kUnitCost * 128 / D);
   Unit u;
-  if (!find_unit(p, plan, blockIdx.x, u)) return;
+  if (!find_unit(p, plan, p.first_unit + (int)blockIdx.x, u)) return;
 
   const int steps = (u.k1 - u.k0 + 31) >> 5, share = (steps + 3) >> 2;
   const int step0 = min(steps, wave * share), step1 = min(steps, step0 + share);

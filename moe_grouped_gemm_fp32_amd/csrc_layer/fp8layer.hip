@@ -43,6 +43,13 @@ int device(int* cus) {
   return d.status;
 }
 
+// Launches so many workgroups in slices: a launch takes less than 2^32 threads, and those past
+// that are left out without an error. f(first, groups) launches one slice.
+template <typename F>
+void in_slices(int64_t groups, int threads, F f) {
+  const int64_t most = UINT32_MAX / threads;
+  for (int64_t first = 0; first < groups; first += most) f((int)first, dim3((unsigned)std::min(most, groups - first)));
+}
 int launched() { return hipGetLastError() == hipSuccess ? FP8GEMM_OK : FP8GEMM_ERR_LAUNCH; }
 
 // ---------------------------------------------------------------------------- RMS norm
@@ -200,15 +207,18 @@ int fp8_rmsnorm_quantize_1x128(const void* X, int64_t ldx, const void* R, int64_
   int cus;
   const int st = device(&cus);
   if (st != FP8GEMM_OK) return st;
-  const fp8layer::NormParams p{X,   R,   w,   H,   Y,   rstd,  static_cast<uint8_t*>(Q), sa, ldx,
-                               ldr, ldh, ldy, ldq, ld_sa, eps, M, K, w_dtype == FP8GEMM_QUANT_FP32};
+  fp8layer::NormParams p{X,   R,   w,   H,   Y,   rstd,  static_cast<uint8_t*>(Q), sa, ldx,
+                         ldr, ldh, ldy, ldq, ld_sa, eps, M, K, w_dtype == FP8GEMM_QUANT_FP32, 0};
   with_type(x_dtype, [&](auto t) {
     with_flag(streams(M, K, sizeof(t) * (R ? 2 : 1)), [&](auto nt) {
       with_shape(norm_shape(M, K, cus), [&](auto waves, auto chunks) {
         constexpr int kWaves = decltype(waves)::value;
-        constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves;
-        hipLaunchKernelGGL((fp8layer::rmsnorm_quantize_kernel<decltype(t), kWaves, decltype(chunks)::value, decltype(nt)::value>),
-                           dim3((unsigned)ceil_div(M, kRows)), dim3(kWaves > 4 ? kWaves * 64 : 256), 0, stream, p);
+        constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves, kThreads = kWaves > 4 ? kWaves * 64 : 256;
+        in_slices(ceil_div(M, kRows), kThreads, [&](int first, dim3 groups) {
+          p.first_group = first;
+          hipLaunchKernelGGL((fp8layer::rmsnorm_quantize_kernel<decltype(t), kWaves, decltype(chunks)::value, decltype(nt)::value>),
+                             groups, dim3(kThreads), 0, stream, p);
+        });
       });
     });
   });
@@ -318,46 +328,49 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
   const int group_tokens = T >= 8 * cus ? 2 : 1;
   const int64_t q_groups = q ? ceil_div(T, group_tokens) : 0;
   if (unit_groups + q_groups > INT32_MAX) return FP8GEMM_ERR_SHAPE;
-  const fp8layer::AppendParams p{static_cast<const uint16_t*>(q),
-                                 static_cast<const uint16_t*>(k),
-                                 static_cast<const uint16_t*>(v),
-                                 cos_sin,
-                                 positions,
-                                 block_table,
-                                 seq_lens,
-                                 cu_q,
-                                 static_cast<uint16_t*>(q_out),
-                                 static_cast<uint8_t*>(k_cache),
-                                 static_cast<uint8_t*>(v_cache),
-                                 k_scale,
-                                 v_scale,
-                                 ldq,
-                                 ldk,
-                                 ldv,
-                                 ld_cs,
-                                 ld_bt,
-                                 ldqo,
-                                 max_pos,
-                                 rot_dim,
-                                 interleaved ? 1 : 0,
-                                 max_pages,
-                                 num_pages,
-                                 log2_of(P),
-                                 B,
-                                 T,
-                                 Hq,
-                                 Hkv,
-                                 (int)unit_groups,
-                                 group_tokens};
-  const dim3 grid((unsigned)(unit_groups + q_groups));
+  fp8layer::AppendParams p{static_cast<const uint16_t*>(q),
+                           static_cast<const uint16_t*>(k),
+                           static_cast<const uint16_t*>(v),
+                           cos_sin,
+                           positions,
+                           block_table,
+                           seq_lens,
+                           cu_q,
+                           static_cast<uint16_t*>(q_out),
+                           static_cast<uint8_t*>(k_cache),
+                           static_cast<uint8_t*>(v_cache),
+                           k_scale,
+                           v_scale,
+                           ldq,
+                           ldk,
+                           ldv,
+                           ld_cs,
+                           ld_bt,
+                           ldqo,
+                           max_pos,
+                           rot_dim,
+                           interleaved ? 1 : 0,
+                           max_pages,
+                           num_pages,
+                           log2_of(P),
+                           B,
+                           T,
+                           Hq,
+                           Hkv,
+                           (int)unit_groups,
+                           group_tokens,
+                           0};
   auto go = [&](auto d) {
     constexpr int kD = decltype(d)::value;
     with_flag(streams(T, ((q ? Hq : 0) + 2 * Hkv) * D, sizeof(uint16_t)), [&](auto nt) {
       constexpr bool kStream = decltype(nt)::value;
-      if (small)
-        hipLaunchKernelGGL((fp8layer::rope_append_kernel<kD, 1, kStream>), grid, dim3(256), 0, stream, p);
-      else
-        hipLaunchKernelGGL((fp8layer::rope_append_kernel<kD, 4, kStream>), grid, dim3(256), 0, stream, p);
+      in_slices(unit_groups + q_groups, 256, [&](int first, dim3 groups) {
+        p.first_group = first;
+        if (small)
+          hipLaunchKernelGGL((fp8layer::rope_append_kernel<kD, 1, kStream>), groups, dim3(256), 0, stream, p);
+        else
+          hipLaunchKernelGGL((fp8layer::rope_append_kernel<kD, 4, kStream>), groups, dim3(256), 0, stream, p);
+      });
     });
   };
   if (D == 64) go(Int<64>{});
@@ -443,19 +456,21 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
   if (grid > INT32_MAX) return FP8GEMM_ERR_SHAPE;
   auto go = [&](auto d) {
     constexpr int kD = decltype(d)::value;
-    const dim3 groups((unsigned)grid);
     constexpr int kMost = most_row_blocks(kD);
-    if (blocks == 1) {
-      hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true, false>), groups, dim3(256), 0, stream, p);
-    } else if (stream_kv) {
-      hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, true, false>), groups, dim3(256), 0, stream, p);
-    } else {
-      with_flag(P >= 32, [&](auto w) {
-        constexpr bool kWide = decltype(w)::value;
-        if (blocks == 2) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, false, kWide>), groups, dim3(256), 0, stream, p);
-        else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, kMost, false, kWide>), groups, dim3(256), 0, stream, p);
-      });
-    }
+    in_slices(grid, 256, [&](int first, dim3 groups) {
+      p.first_unit = first;
+      if (blocks == 1) {
+        hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 1, true, false>), groups, dim3(256), 0, stream, p);
+      } else if (stream_kv) {
+        hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, true, false>), groups, dim3(256), 0, stream, p);
+      } else {
+        with_flag(P >= 32, [&](auto w) {
+          constexpr bool kWide = decltype(w)::value;
+          if (blocks == 2) hipLaunchKernelGGL((fp8layer::attention_kernel<kD, 2, false, kWide>), groups, dim3(256), 0, stream, p);
+          else hipLaunchKernelGGL((fp8layer::attention_kernel<kD, kMost, false, kWide>), groups, dim3(256), 0, stream, p);
+        });
+      }
+    });
   };
   if (D == 64) go(Int<64>{});
   else if (D == 128) go(Int<128>{});

@@ -33,6 +33,7 @@ struct AppendParams {
   int B, T, Hq, Hkv;
   int unit_groups;   // workgroups that hold units; the later ones rotate queries,
   int group_tokens;  // of so many tokens each
+  int first_group;   // the launch's first workgroup of the call's
 };
 
 constexpr int kHeld = 2;
@@ -101,9 +102,10 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int P = 1 << p.log_p;
   const int max_len = p.max_pages << p.log_p;
+  const int group = p.first_group + (int)blockIdx.x;
 
-  if ((int)blockIdx.x >= p.unit_groups) {  // queries: a thread has item n % kItems of every so many heads
-    const int t0 = ((int)blockIdx.x - p.unit_groups) * p.group_tokens, t1 = min(p.T, t0 + p.group_tokens);
+  if (group >= p.unit_groups) {  // queries: a thread has item n % kItems of every so many heads
+    const int t0 = (group - p.unit_groups) * p.group_tokens, t1 = min(p.T, t0 + p.group_tokens);
     for (int n0 = 0; n0 < p.Hq * kItems; n0 += 256) {
       const int n = n0 + threadIdx.x, i = n % kItems, h = n / kItems;
       const bool live = n < p.Hq * kItems;
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const AppendParams p) 
 
   // the unit: a page of a sequence (found by scanning the sequences' page counts), a head,
   // keys or values
-  const int unit = WAVES == 4 ? (int)blockIdx.x : (int)blockIdx.x * 4 + wave;
+  const int unit = WAVES == 4 ? group : group * 4 + wave;
   const bool keys = (unit & 1) == 0;
   const int h = (unit >> 1) % p.Hkv;
   const int want = (unit >> 1) / p.Hkv;

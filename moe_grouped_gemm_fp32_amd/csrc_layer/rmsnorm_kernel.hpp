@@ -40,6 +40,7 @@ struct NormParams {
   int64_t ldx, ldr, ldh, ldy, ldq, ld_sa;
   float eps;
   int M, K, w_fp32;
+  int first_group;  // the launch's first workgroup of the call's
 };
 
 // y / s for a scale s and r = 1 / s (rounded): one step of Markstein's division, which
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quantize_ker
   __shared__ float part[WPR > 4 ? WPR : 4];
   const int wave = threadIdx.x >> 6;
   const int t = WPR > 1 ? threadIdx.x : threadIdx.x & 63;
-  const int row = blockIdx.x * kRows + (WPR > 1 ? 0 : wave);
+  const int row = (p.first_group + (int)blockIdx.x) * kRows + (WPR > 1 ? 0 : wave);
   if (row >= p.M) return;  // whole rows only: no wave of a shared row leaves
   const T* X = static_cast<const T*>(p.X) + (int64_t)row * p.ldx;
   const int chunks = p.K >> 3;
