@@ -55,29 +55,45 @@ def _call_command() -> list:
 
 def _compile(out: str, extra: list, verbose: bool, beside: dict = {}) -> str:
     """One object per source, compiled side by side, linked into `out`; `beside`: further
-    files and the commands, up to -o, that make them."""
+    files and the commands, up to -o, that make them. What could be made is there when another
+    file's failure is raised."""
     tmp = out + ".tmp%d" % os.getpid()
     objs = ["%s.%d.o" % (tmp, i) for i in range(len(SRCS))]
     more = {path: path + ".tmp%d" % os.getpid() for path in beside}
     steps = [[hipcc(), *FLAGS, *extra, "-c", src, "-o", obj] for src, obj in zip(SRCS, objs)]
     steps += [[*cmd, "-o", more[path]] for path, cmd in beside.items()]
     link = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *extra, *objs, "-o", tmp]
+
+    def start(cmd):
+        try:
+            return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+        except OSError as e:  # no such compiler
+            return e
+
+    def finish(p):
+        """A command's output if it failed, else None."""
+        if isinstance(p, OSError):
+            return f"{p}\n"
+        said = p.communicate()[0]
+        return said if p.returncode != 0 else None
+
     try:
         if verbose:
             print("\n".join("[build] " + " ".join(c) for c in [*steps, link]), flush=True)
-        running = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in steps]
-        said = [p.communicate()[0] for p in running]
-        done = [p.returncode for p in running]
-        if not any(done):
-            res = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-            said.append(res.stdout)
-            done.append(res.returncode)
-        if any(done):
-            sys.stderr.write("".join(said))
-            raise RuntimeError("the compiler failed building " + os.path.basename(out))
-        os.replace(tmp, out)
-        for path, made in more.items():
-            os.replace(made, path)
+        failed = [finish(p) for p in [start(c) for c in steps]]
+        parts = failed[:len(objs)]
+        if not any(f is not None for f in parts):
+            parts.append(finish(start(link)))
+        results = [(out, tmp, parts)] + [(path, made, [f]) for (path, made), f in zip(more.items(), failed[len(objs):])]
+        missing = []
+        for path, made, errors in results:
+            if all(f is None for f in errors):
+                os.replace(made, path)
+            else:
+                sys.stderr.write("".join(f for f in errors if f))
+                missing.append(os.path.basename(path))
+        if missing:
+            raise RuntimeError("the compiler failed building " + ", ".join(missing))
     finally:
         for f in (*objs, tmp, *more.values()):
             if os.path.exists(f):
@@ -85,10 +101,22 @@ def _compile(out: str, extra: list, verbose: bool, beside: dict = {}) -> str:
     return out
 
 
+def build_library(verbose: bool = True) -> str:
+    """Compile libfp8gemm.so next to this file (always rebuilds). Returns its path. The C
+    interface alone: hipcc is all that it needs."""
+    return _compile(LIB, [], verbose)
+
+
 def build(verbose: bool = True) -> str:
     """Compile libfp8gemm.so and _layer_call.so next to this file (always rebuilds). Returns the
-    library's path."""
-    return _compile(LIB, [], verbose, {CALL: _call_command()})
+    library's path. Where the binding cannot be built (no torch or Python headers, no host
+    compiler), the library is built all the same before that is raised."""
+    try:
+        beside = {CALL: _call_command()}
+    except Exception as e:
+        build_library(verbose)
+        raise RuntimeError(f"{os.path.basename(CALL)} cannot be built: {e}") from e
+    return _compile(LIB, [], verbose, beside)
 
 
 # Host-sanitizer build: the same library with its host code (argument checks, planner,
@@ -126,5 +154,7 @@ def build_host_sanitized(verbose: bool = True, force: bool = False) -> str:
 if __name__ == "__main__":
     if "--host-sanitizers" in sys.argv[1:]:
         build_host_sanitized(force=True)
+    elif "--library" in sys.argv[1:]:
+        build_library()
     else:
         build()
