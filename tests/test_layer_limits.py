@@ -1,4 +1,8 @@
 """Limits and promises of the layer operators that need no GPU to be checked."""
+import glob
+import os
+import re
+
 import pytest
 import torch
 
@@ -26,3 +30,14 @@ def test_a_table_without_pages_may_have_no_address():
         assert call(name, defaults, block_table=None, max_pages=1, ld_bt=1) == NULL
         if not torch.cuda.is_available():
             assert call(name, defaults, block_table=None, max_pages=0, ld_bt=0) == DEVICE
+
+
+def test_assembly_says_which_registers_it_writes():
+    """m0 is the compiler's to use as well: a statement that sets it has to name it."""
+    found = 0
+    for path in glob.glob(os.path.join(os.path.dirname(fg.__file__), "csrc_layer", "*")):
+        for statement in re.findall(r"\basm\b[^;]*?\((.*?)\);", open(path).read(), re.S):
+            if re.search(r"s_mov_b32 m0,", statement):
+                found += 1
+                assert '"m0"' in statement.rsplit(":", 1)[1], (path, statement)
+    assert found == 2
