@@ -120,12 +120,17 @@ void with_shape(NormShape s, F f) {
 // where they do not fit the L2 caches (8 of 4 MB). 4096 x 7168 BF16, without and with: norm
 // 46.0 and 40.5 us, gradient 49.0 and 45.6; the gradient of 333 x 2048 FP32, which fits: 7.3 and 8.0.
 bool streams(int M, int K, size_t bytes) { return (size_t)M * K * bytes > ((size_t)32 << 20); }
-// Whether a gradient is taken in one launch, which reads the rows twice: where they fit the
-// L2 caches and a row's chunks are one a thread. In two launches and in one: 10 x 1536 FP32
-// 5.9 and 3.7 us, 333 x 2048 7.5 and 4.9, 1024 x 2048 11.4 and 10.8 (1024 x 1024, whose rows
-// crowd into few L2 channels, 7.7 and 9.8); BF16 256 x 7168 14.0 and 6.8, 1024 x 4096 13.8
-// and 10.0.
-bool norm_grad_few(int M, int K, size_t bytes, int cus) { return M <= 4 * cus && K <= 8 * 1024 && !streams(M, K, bytes); }
+// Whether a gradient is taken in one launch, which reads the rows twice: where they are 32 MB
+// at most and a row's chunks are one a thread. In two launches and in one, in a graph: FP32
+// 16 x 1536 5.7 and 3.5 us, 512 x 2048 8.4 and 6.1, 1024 x 512 6.3 and 4.8, 1024 x 2048 10.5 and
+// 10.7, 1024 x 4096 15.4 and 14.6; BF16 256 x 8192 11.5 and 6.7, 1024 x 1024 6.7 and 4.8,
+// 1024 x 8192 15.9 and 15.2. But for more than three FP32 rows a CU between those widths the
+// second reading costs more than a launch: 1024 x 768 7.2 and 9.2, x 1024 7.8 and 9.7, x 1280
+// 8.7 and 11.2, x 1536 9.3 and 10.7 (768 x 1024: 7.1 and 6.8).
+bool norm_grad_few(int M, int K, size_t bytes, bool fp32, int cus) {
+  if (fp32 && M > 3 * cus && K > 512 && K < 2048) return false;
+  return M <= 4 * cus && K <= 8 * 1024 && !streams(M, K, bytes);
+}
 // Whether rows written to dX lie among those at p: then no workgroup may read what another
 // has finished with.
 bool rows_meet(const void* dX, int64_t lddx, const void* p, int64_t ld, int M, int K, size_t size) {
@@ -250,7 +255,7 @@ int fp8_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int64_t ld
   if (groups > 0 && (!workspace || workspace_bytes < (size_t)groups * K * sizeof(float))) return FP8GEMM_ERR_WORKSPACE;
   float* part = static_cast<float*>(workspace);
   const size_t size = dtype == FP8GEMM_QUANT_BF16 ? 2 : 4, row_bytes = size * (dH ? 3 : 2);
-  if (M > 0 && norm_grad_few(M, K, row_bytes, cus) && !rows_meet(dX, lddx, dY, lddy, M, K, size) &&
+  if (M > 0 && norm_grad_few(M, K, row_bytes, dtype == FP8GEMM_QUANT_FP32, cus) && !rows_meet(dX, lddx, dY, lddy, M, K, size) &&
       !rows_meet(dX, lddx, H, ldh, M, K, size)) {
     const fp8layer::NormGradParams p{dY, H, dH, w, rstd, dX, nullptr, lddy, ldh, lddh, lddx, M, K, w_dtype == FP8GEMM_QUANT_FP32};
     with_type(dtype, [&](auto t) {
