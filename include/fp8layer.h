@@ -87,8 +87,10 @@ int fp8_rmsnorm_quantize_1x128(const void* X, int64_t ldx, const void* R, int64_
  * residual stream, is optional.
  *   dY, H, dH, dX  [M, K] of one type (dtype), row strides ld*; dX may be dY or dH itself.
  *   rstd  fp32 [M], as written by the forward call. w [K] (w_dtype).
- *   dW    fp32 [K], overwritten. The rows are summed in a fixed order: equal inputs give
- *         equal bits.
+ *   dW    fp32 [K], overwritten. The rows are summed in an order that is fixed by M, K, dtype,
+ *         whether dH is given, the number of compute units (fp8_gemm_set_num_cus), and
+ *         whether the memory that dX's rows span meets that of dY's or H's rows: equal
+ *         inputs give equal bits in any such call.
  *   workspace  fp8_rmsnorm_backward_workspace_size(M, K) bytes, 16-byte aligned; its
  *         contents need no initial value. FP8GEMM_ERR_WORKSPACE if smaller or NULL.
  * K, alignment and strides as above. M == 0 zeroes dW.
