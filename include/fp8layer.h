@@ -123,8 +123,8 @@ size_t fp8_rmsnorm_backward_workspace_size(int M, int K);
  * tokens than seq_lens) and past the table (max_pages P and on) are dropped; their queries
  * are rotated like all others. Rows past cu_q[B] are untouched.
  * D, P as above; rot_dim a multiple of 16, 0 .. D. q, k, v, q_out, cos_sin 16-byte
- * aligned, their strides multiples of 8 (BF16) and 4 (cos_sin) elements. T * Hq and
- * max_pages * P below 2^31.
+ * aligned, their strides multiples of 8 (BF16) and 4 (cos_sin) elements. T * Hq, T * Hkv,
+ * Hq * D, Hkv * D and max_pages * P below 2^31.
  */
 int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
                              const float* cos_sin, int64_t ld_cs, int max_pos, int rot_dim, int interleaved,
@@ -152,8 +152,8 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
  *        size may be given; fp8_paged_attention_workspace_size() suffices for every call.
  *        Calls that may run at the same time must not share it.
  * NaN codes in slots that no row sees change nothing; a row that sees one gives NaN.
- * Hkv divides Hq. q, O 16-byte aligned with strides multiples of 8; T * Hq below 2^31,
- * max_pages * P at most 2^30; window >= 0; num_pages >= 1.
+ * Hkv divides Hq. q, O 16-byte aligned with strides multiples of 8; T * Hq and Hq * D
+ * below 2^31, max_pages * P at most 2^30; window >= 0; num_pages >= 1.
  */
 int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const float* k_scale, const void* v_cache,
                         const float* v_scale, int num_pages, int P, const int32_t* block_table, int64_t ld_bt,

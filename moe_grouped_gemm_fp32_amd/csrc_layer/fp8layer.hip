@@ -119,7 +119,7 @@ void with_shape(NormShape s, F f) {
 // Whether M rows of K columns, `bytes` each, are read with the hint that they are read once:
 // where they do not fit the L2 caches (8 of 4 MB). 4096 x 7168 BF16, without and with: norm
 // 46.0 and 40.5 us, gradient 49.0 and 45.6; the gradient of 333 x 2048 FP32, which fits: 7.3 and 8.0.
-bool streams(int M, int K, size_t bytes) { return (size_t)M * K * bytes > ((size_t)32 << 20); }
+bool streams(int M, int64_t K, size_t bytes) { return (size_t)M * K * bytes > ((size_t)32 << 20); }
 // Whether a gradient is taken in one launch, which reads the rows twice: where they are 32 MB
 // at most and a row's chunks are one a thread. In two launches and in one, in a graph: FP32
 // 16 x 1536 5.7 and 3.5 us, 512 x 2048 8.4 and 6.1, 1024 x 512 6.3 and 4.8, 1024 x 2048 10.5 and
@@ -303,7 +303,7 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
     return FP8GEMM_ERR_NULL;
   if (!cache_shape(num_pages, P, Hkv, D) || B < 0 || T < 0 || Hq < 1 || max_pages < 0 || rot_dim < 0 || rot_dim > D ||
       rot_dim % 16 != 0 || (rot_dim > 0 && max_pos < 1) || (int64_t)T * std::max(Hq, Hkv) >= INT32_MAX - 256 ||
-      (int64_t)max_pages * P > INT32_MAX)
+      (int64_t)std::max(Hq, Hkv) * D > INT32_MAX || (int64_t)max_pages * P > INT32_MAX)
     return FP8GEMM_ERR_SHAPE;
   if (B == 0 || T == 0) return FP8GEMM_OK;
   if (ldk < (int64_t)Hkv * D || ldk % 8 || ldv < (int64_t)Hkv * D || ldv % 8 || ld_bt < max_pages ||
@@ -367,7 +367,7 @@ int fp8_rope_append_paged_kv(const void* q, int64_t ldq, const void* k, int64_t 
                            0};
   auto go = [&](auto d) {
     constexpr int kD = decltype(d)::value;
-    with_flag(streams(T, ((q ? Hq : 0) + 2 * Hkv) * D, sizeof(uint16_t)), [&](auto nt) {
+    with_flag(streams(T, ((q ? Hq : 0) + 2 * (int64_t)Hkv) * D, sizeof(uint16_t)), [&](auto nt) {
       constexpr bool kStream = decltype(nt)::value;
       in_slices(unit_groups + q_groups, 256, [&](int first, dim3 groups) {
         p.first_group = first;
@@ -395,7 +395,8 @@ int fp8_paged_attention(const void* q, int64_t ldq, const void* k_cache, const f
       (T != 0 && B != 0 && (!q || (max_pages > 0 && !block_table) || !seq_lens || !cu_q || !O)))
     return FP8GEMM_ERR_NULL;
   if (!cache_shape(num_pages, P, Hkv, D) || B < 0 || T < 0 || Hq < 1 || Hq % Hkv != 0 || max_pages < 0 || window < 0 ||
-      !std::isfinite(softmax_scale) || (int64_t)T * Hq >= INT32_MAX - 256 || (int64_t)max_pages * P > fp8layer::kMostKeys)
+      !std::isfinite(softmax_scale) || (int64_t)T * Hq >= INT32_MAX - 256 || (int64_t)Hq * D > INT32_MAX ||
+      (int64_t)max_pages * P > fp8layer::kMostKeys)
     return FP8GEMM_ERR_SHAPE;
   if (B == 0 || T == 0) return FP8GEMM_OK;
   if (ldq < (int64_t)Hq * D || ldq % 8 || ldo < (int64_t)Hq * D || ldo % 8 || ld_bt < max_pages) return FP8GEMM_ERR_LAYOUT;

@@ -41,3 +41,15 @@ def test_assembly_says_which_registers_it_writes():
                 found += 1
                 assert '"m0"' in statement.rsplit(":", 1)[1], (path, statement)
     assert found == 2
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_of_heads_are_less_than_2_to_the_31_columns(D):
+    """A head's first column is a 32-bit number in the kernels."""
+    for name, defaults, rows in (("fp8_rope_append_paged_kv", {**APPEND, "rot_dim": 0}, ("ldq", "ldqo")),
+                                 ("fp8_paged_attention", ATTEND, ("ldq", "ldo"))):
+        wide = dict.fromkeys(rows, 1 << 40)
+        assert call(name, defaults, T=1, B=1, Hq=(1 << 31) // D, Hkv=2, D=D, **wide) == SHAPE
+        if not torch.cuda.is_available():
+            assert call(name, defaults, T=1, B=1, Hq=(1 << 31) // D - 2, Hkv=2, D=D, **{**wide, **({"ldk": 512, "ldv": 512} if "ldk" in defaults else {})}) == DEVICE
+    assert call("fp8_rope_append_paged_kv", {**APPEND, "rot_dim": 0}, T=1, B=1, Hkv=(1 << 31) // D, D=D, ldk=1 << 40, ldv=1 << 40) == SHAPE
