@@ -40,7 +40,8 @@ def append(dev, seed):
     g = torch.Generator(dev).manual_seed(seed)
     q, k, v = (torch.randn(2048, h, 128, generator=g, device=dev).to(BF16) for h in (8, 1, 1))
     cache, rot = fg.make_paged_kv_cache(64, 1, 32, 128, device=dev), torch.rand(2048, 128, generator=g, device=dev)
-    return lambda **kw: (fg.rope_append_paged_kv(q, k, v, rot, cache, *sequences(dev), **kw),)
+    seqs = sequences(dev)
+    return lambda **kw: (fg.rope_append_paged_kv(q, k, v, rot, cache, *seqs, **kw),)
 
 
 def attend(dev, seed):
@@ -141,3 +142,26 @@ def test_any_stream_object_and_a_stream_of_its_own_handle(cuda_device):
         torch.cuda.synchronize()
         assert torch.cuda.current_stream() == torch.cuda.default_stream()
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+
+
+@CALLS
+def test_on_a_side_stream_of_a_captured_graph(cuda_device, make):
+    """Outputs allocated on a stream that a capture forks to belong to the graph: replays write them."""
+    call, side = make(cuda_device, 6), torch.cuda.Stream()
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        copies = [t.clone() for t in got]
+    for _ in range(3):
+        for t in (*got, *copies):
+            t.view(torch.uint8).fill_(0x5A)
+        other = call()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c, d in zip(got, copies, want, other):
+            assert torch.equal(a.view(torch.uint8), c.view(torch.uint8)) and torch.equal(b.view(torch.uint8), c.view(torch.uint8))
+            assert torch.equal(d.view(torch.uint8), c.view(torch.uint8))
