@@ -34,10 +34,11 @@
 // the GPU. The parts of a tile are joined in their order by whoever arrives last: first in
 // groups of kJoin neighbours, then the groups' results.
 //
-// What bounds it. Many rows: the vector unit, which converts 64 codes a lane and step and
-// takes eight exponentials a row block (195 vector and 48 matrix instructions a step of 48
-// rows; 2 x 2048 prompt tokens over 8192 keys 524 us, 918 TFLOP/s of the 1280 that a large
-// BF16 product reaches). Few rows, many keys: memory (64 x 8192 keys 165 us, 6.5 TB/s;
+// What bounds it. Many rows: vector instructions (64 codes converted a lane and step, eight
+// exponentials a row block: 195 of them and 48 matrix instructions a step of 48 rows) that
+// hardly overlap with the matrix unit: it works in 37 % of the cycles and they issue in 60 %,
+// as a wave's steps depend on each other and registers allow two waves a SIMD (2 x 2048 prompt
+// tokens over 8192 keys 524 us, 918 TFLOP/s of the 1280 that a large BF16 product reaches). Few rows, many keys: memory (64 x 8192 keys 165 us, 6.5 TB/s;
 // 64 users of 500 to 8192 keys 112 us, 5.4 TB/s). Little work: latencies, in us for one user
 // of 777 keys 1.4 to find the unit, 1.2 to the first keys, 0.8 a step, 0.9 to join the waves,
 // 1.1 to hand over to the last arriver, 0.4 and 1.0 to join the parts and write: 8.1 in all.
@@ -101,7 +102,10 @@ constexpr __host__ __device__ int up128(int keys) { return (int)(((uint32_t)keys
 static_assert(pieces(kMostKeys, kWhole) == 1 && pieces(kMostKeys, up128((int)(float)kWhole)) == 1 && up128(kMostKeys) == kMostKeys);
 static_assert((int64_t)kMostKeys + 64 * 32 <= INT32_MAX);
 
-// What a sequence asks for: its row tiles, and the most keys that one of them reads.
+// What a sequence asks for: its row tiles, and the most keys that one of them reads. With a
+// window that is an upper bound, as if a tile held all new tokens: with the tile's own tokens
+// alone 4 x 300 tokens in a window of 1024 take 45 us in place of 48, but 2048 tokens of eight
+// heads on one key head 42 in place of 29.
 struct Demand {
   int tiles, keys;
 };
@@ -548,7 +552,7 @@ constexpr int attention_residents(int D, int R) { return D == 64 ? (R == 1 ? 4 :
 // users of 8192 keys: 183 us without, 165 with, 6.5 TB/s) and costs 4% where many tiles
 // share them (2048 prompt tokens in 32-row tiles: 488 and 506 us).
 // WIDE: pages hold 32 keys and more, so that a step has one scale of each kind. Worth 4%
-// where the vector unit sets the pace (2 x 2048 prompt tokens over 8192 keys: 544 us without,
+// where vector instructions set the pace (2 x 2048 prompt tokens over 8192 keys: 544 us without,
 // 524 with, 918 TFLOP/s), nothing where memory does, so only shared tiles have it.
 template <int D, int R, bool STREAM, bool WIDE>
 __global__ void __launch_bounds__(256, attention_residents(D, R)) attention_kernel(const AttentionParams p) {

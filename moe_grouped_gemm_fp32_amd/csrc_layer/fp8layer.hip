@@ -117,8 +117,9 @@ void with_shape(NormShape s, F f) {
   }
 }
 // Whether M rows of K columns, `bytes` each, are read with the hint that they are read once:
-// where they do not fit the L2 caches (8 of 4 MB). 4096 x 7168 BF16, without and with: norm
-// 46.0 and 40.5 us, gradient 49.0 and 45.6; the gradient of 333 x 2048 FP32, which fits: 7.3 and 8.0.
+// above 32 MB, the sum of the eight L2 caches, each of which gets its own workgroups' rows. 4096
+// x 7168 BF16, without and with: norm 46.0 and 40.5 us, gradient 49.0 and 45.6; the gradient of
+// 333 x 2048 FP32, 5 MB: 7.3 and 8.0.
 bool streams(int M, int64_t K, size_t bytes) { return (size_t)M * K * bytes > ((size_t)32 << 20); }
 // Whether a gradient is taken in one launch, which reads the rows twice: where they are 32 MB
 // at most and a row's chunks are one a thread. In two launches and in one, in a graph: FP32

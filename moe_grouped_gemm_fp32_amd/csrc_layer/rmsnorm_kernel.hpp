@@ -53,7 +53,7 @@ __device__ __forceinline__ float quotient(float y, float s, float r) {
 // Forward: sum of squares, then y = (h * rstd) * w in FP32, its maximum over the 16 lanes
 // of a block, and the codes. Bound by memory: 4096 x 7168 BF16 with the residual 40.4 us,
 // 5.1 TB/s (a large copy reaches 4.8 to 5.3); 1537 x 2048 FP32 6.8 us; one row of 7168
-// 3.7 us, most of it the launch.
+// 3.2 us, most of it the launch.
 template <typename T, int WPR, int CH, bool STREAM>
 __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quantize_kernel(const NormParams p) {
   constexpr int kRows = WPR > 4 ? 1 : 4 / WPR;  // rows of a workgroup
@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormGradPa
 // Backward of few rows, in one launch, for a dX that is not in dY's place (both are read by
 // other workgroups while it is written): neither result needs the other, as rstd is given. The
 // first workgroups sum dW of 128 bytes of columns each, a thread eight columns over every
-// 128th (FP32: 256th) row; the others take 16 / WPR rows each for dX. The rows are read twice, the
-// second time from L2. 333 x 2048 FP32 4.9 us, 64 x 7168 BF16 3.7, where the kernels above
+// 128th (FP32: 256th) row; the others take 16 / WPR rows each for dX. The rows are read twice, by
+// workgroups that are mostly on different XCDs: the second time from the last-level cache. 333 x 2048 FP32 4.9 us, 64 x 7168 BF16 3.7, where the kernels above
 // take 7.4 and 7.6 and cost the host two launches.
 template <typename T, int WPR>
 __global__ void __launch_bounds__(1024) rmsnorm_backward_few_kernel(const NormGradParams p, float* dW) {
