@@ -639,3 +639,8 @@ from .layer import (PagedKVCache, attention_workspace_size, make_attention_works
                     paged_attention, rmsnorm_backward, rmsnorm_quantize_1x128, rope_append_paged_kv)
 
 __all__ += _layer.__all__
+from . import moe as _moe  # noqa: E402
+from .moe import (MoeLayout, make_moe_layout, moe_combine, moe_combine_backward, moe_dispatch, moe_gather, moe_route,  # noqa: E402
+                  moe_route_backward, moe_rows, qk_norm_rope, qk_norm_rope_backward)
+
+__all__ += _moe.__all__

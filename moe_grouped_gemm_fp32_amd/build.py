@@ -15,7 +15,8 @@ import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRCS = [os.path.join(PKG, "csrc", "fp8gemm.hip"), os.path.join(PKG, "csrc_layer", "fp8layer.hip")]
+SRCS = [os.path.join(PKG, "csrc", "fp8gemm.hip"), os.path.join(PKG, "csrc_layer", "fp8layer.hip"),
+        os.path.join(PKG, "csrc_moe", "fp8moe.hip")]
 LIB = os.path.join(PKG, "libfp8gemm.so")
 CALL_SRC = os.path.join(PKG, "csrc_layer", "binding.cpp")
 CALL = os.path.join(PKG, "_layer_call.so")
@@ -33,12 +34,12 @@ FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          # MFMA results in VGPRs: the FP32 promotion FMAs read them directly
          "-mllvm", "-amdgpu-mfma-vgpr-form",
-         "-I", os.path.join(ROOT, "include")]
+         "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc_layer")]
 
 
 def sources() -> list:
     """Every file that the library is built from."""
-    return [f for d in ("csrc", "csrc_layer") for f in sorted(glob.glob(os.path.join(PKG, d, "*")))] + \
+    return [f for d in ("csrc", "csrc_layer", "csrc_moe") for f in sorted(glob.glob(os.path.join(PKG, d, "*")))] + \
         sorted(glob.glob(os.path.join(ROOT, "include", "*.h"))) + [os.path.abspath(__file__)]
 
 

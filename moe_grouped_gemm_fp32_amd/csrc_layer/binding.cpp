@@ -19,6 +19,8 @@
 
 #include <climits>
 #include <cmath>
+#include <cstring>
+#include <utility>
 
 #include "fp8gemm.h"
 #include "fp8layer.h"
@@ -392,23 +394,32 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// Sets f to the address that a dict has under `name`.
+template <typename F>
+void set_address(PyObject* dict, F& f, const char* name) {
+  TORCH_CHECK_TYPE(PyDict_Check(dict), "expected a dict of addresses");
+  PyObject* at = PyDict_GetItemString(dict, name);
+  TORCH_CHECK_VALUE(at != nullptr, "no address of ", name);
+  f = reinterpret_cast<F>(PyLong_AsVoidPtr(at));
+  if (!f) throw python_error();
+}
+
+}  // namespace
+
+#include "../csrc_moe/binding_moe.hpp"
+
+namespace {
+
 // The library's functions as a dict of addresses by name, check, current_stream, external_stream
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arguments(n, 4);
-  TORCH_CHECK_TYPE(PyDict_Check(a[0]), "expected a dict of addresses");
-  auto set = [&](auto& f, const char* name) {
-    PyObject* at = PyDict_GetItemString(a[0], name);
-    TORCH_CHECK_VALUE(at != nullptr, "no address of ", name);
-    f = reinterpret_cast<std::decay_t<decltype(f)>>(PyLong_AsVoidPtr(at));
-    if (!f) throw python_error();
-  };
-  set(library.norm, "fp8_rmsnorm_quantize_1x128");
-  set(library.norm_grad, "fp8_rmsnorm_backward");
-  set(library.norm_grad_workspace, "fp8_rmsnorm_backward_workspace_size");
-  set(library.append, "fp8_rope_append_paged_kv");
-  set(library.attend, "fp8_paged_attention");
-  set(library.scale_ld, "fp8_gemm_scale_ld");
+  set_address(a[0], library.norm, "fp8_rmsnorm_quantize_1x128");
+  set_address(a[0], library.norm_grad, "fp8_rmsnorm_backward");
+  set_address(a[0], library.norm_grad_workspace, "fp8_rmsnorm_backward_workspace_size");
+  set_address(a[0], library.append, "fp8_rope_append_paged_kv");
+  set_address(a[0], library.attend, "fp8_paged_attention");
+  set_address(a[0], library.scale_ld, "fp8_gemm_scale_ld");
   Py_INCREF(a[1]), Py_INCREF(a[2]), Py_INCREF(a[3]);
   library.check = a[1], library.current_stream = a[2], library.external_stream = a[3];
   Py_RETURN_NONE;
@@ -425,6 +436,15 @@ PyMethodDef methods[] = {
     {"rmsnorm_backward", fast(rmsnorm_backward), METH_FASTCALL, nullptr},
     {"rope_append", fast(rope_append), METH_FASTCALL, nullptr},
     {"attend", fast(attend), METH_FASTCALL, nullptr},
+    {"bind_moe", fast(bind_moe), METH_FASTCALL, nullptr},
+    {"moe_route", fast(moe_route), METH_FASTCALL, nullptr},
+    {"moe_route_backward", fast(moe_route_backward), METH_FASTCALL, nullptr},
+    {"moe_dispatch", fast(moe_dispatch), METH_FASTCALL, nullptr},
+    {"moe_gather", fast(moe_gather), METH_FASTCALL, nullptr},
+    {"moe_combine", fast(moe_combine), METH_FASTCALL, nullptr},
+    {"moe_combine_backward", fast(moe_combine_backward), METH_FASTCALL, nullptr},
+    {"qk_norm_rope", fast(qk_norm_rope), METH_FASTCALL, nullptr},
+    {"qk_norm_rope_backward", fast(qk_norm_rope_backward), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -4,53 +4,14 @@
 
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
 #include <cmath>
-#include <cstring>
-#include <mutex>
 
 #include "attention_kernel.hpp"
+#include "host.hpp"
 #include "kvcache_kernel.hpp"
 #include "rmsnorm_kernel.hpp"
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// FP8GEMM_OK and the current device's compute units if it is a gfx950. The units are capped
-// by fp8_gemm_set_num_cus, like those of the GEMMs' grids.
-int device(int* cus) {
-  struct Info {
-    int status = 1, cus = 0;
-  };
-  static Info infos[kMaxDevices];
-  static std::mutex mutex;
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return FP8GEMM_ERR_DEVICE;
-  std::lock_guard<std::mutex> lock(mutex);
-  Info& d = infos[dev];
-  if (d.status == 1) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return FP8GEMM_ERR_DEVICE;
-    d.cus = prop.multiProcessorCount;
-    d.status = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? FP8GEMM_OK : FP8GEMM_ERR_DEVICE;
-  }
-  const int cap = fp8_gemm_get_num_cus();
-  *cus = cap > 0 ? std::min(cap, d.cus) : d.cus;
-  return d.status;
-}
-
-// Launches so many workgroups in slices: a launch takes less than 2^32 threads, and those past
-// that are left out without an error. f(first, groups) launches one slice.
-template <typename F>
-void in_slices(int64_t groups, int threads, F f) {
-  const int64_t most = UINT32_MAX / threads;
-  for (int64_t first = 0; first < groups; first += most) f((int)first, dim3((unsigned)std::min(most, groups - first)));
-}
-int launched() { return hipGetLastError() == hipSuccess ? FP8GEMM_OK : FP8GEMM_ERR_LAUNCH; }
 
 // ---------------------------------------------------------------------------- RMS norm
 
@@ -85,20 +46,7 @@ NormShape norm_grad_shape(int K) {
   return {16, 8};
 }
 
-bool norm_dtype(int t) { return t == FP8GEMM_QUANT_BF16 || t == FP8GEMM_QUANT_FP32; }
-// row stride of a [.., K] array of x_dtype elements whose rows are read 16 bytes at a time
-bool norm_rows(const void* p, int64_t ld, int K, int dtype) {
-  return aligned(p, 16) && ld >= K && ld % (dtype == FP8GEMM_QUANT_BF16 ? 8 : 4) == 0;
-}
-
-// Calls f(T{}, waves, chunks) with the rows' type and the shape as compile-time values.
-template <int N>
-using Int = std::integral_constant<int, N>;
-template <typename F>
-void with_type(int dtype, F f) {
-  if (dtype == FP8GEMM_QUANT_BF16) f(uint16_t{});
-  else f(float{});
-}
+// Calls f(waves, chunks) with the shape as compile-time values.
 template <typename F>
 void with_shape(NormShape s, F f) {
   if (s.waves == 1) {
@@ -116,11 +64,6 @@ void with_shape(NormShape s, F f) {
     f(Int<16>{}, Int<8>{});
   }
 }
-// Whether M rows of K columns, `bytes` each, are read with the hint that they are read once:
-// above 32 MB, the sum of the eight L2 caches, each of which gets its own workgroups' rows. 4096
-// x 7168 BF16, without and with: norm 46.0 and 40.5 us, gradient 49.0 and 45.6; the gradient of
-// 333 x 2048 FP32, 5 MB: 7.3 and 8.0.
-bool streams(int M, int64_t K, size_t bytes) { return (size_t)M * K * bytes > ((size_t)32 << 20); }
 // Whether a gradient is taken in one launch, which reads the rows twice: where they are 32 MB
 // at most and a row's chunks are one a thread. In two launches and in one, in a graph: FP32
 // 16 x 1536 5.7 and 3.5 us, 512 x 2048 8.4 and 6.1, 1024 x 512 6.3 and 4.8, 1024 x 2048 10.5 and
@@ -137,11 +80,6 @@ bool norm_grad_few(int M, int K, size_t bytes, bool fp32, int cus) {
 bool rows_meet(const void* dX, int64_t lddx, const void* p, int64_t ld, int M, int K, size_t size) {
   const uintptr_t a = (uintptr_t)dX, b = (uintptr_t)p;
   return a < b + ((size_t)(M - 1) * ld + K) * size && b < a + ((size_t)(M - 1) * lddx + K) * size;
-}
-template <typename F>
-void with_flag(bool flag, F f) {
-  if (flag) f(std::true_type{});
-  else f(std::false_type{});
 }
 template <typename F>
 void with_grad_shape(NormShape s, F f) {

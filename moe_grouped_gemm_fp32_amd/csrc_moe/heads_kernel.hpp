@@ -1,0 +1,216 @@
+// Device code of the norm of queries and keys for each head with their rotation, and of its
+// gradients.
+//
+// D / 16 lanes hold a head: each 16 of its columns, both members of eight pairs where they
+// turn, so that neither the rotation nor the norm needs another lane's columns, only the sum
+// of squares (or the gradient's dot product) goes over the lanes.
+#pragma once
+
+#include "common.hpp"
+
+namespace fp8moe {
+
+using namespace fp8layer;
+
+// The two groups of eight columns that a lane holds of a head, and whether they turn.
+struct Columns {
+  int lo, hi;
+  bool turns;
+};
+__device__ __forceinline__ Columns columns_of(int i, int rot_dim, int interleaved) {
+  const bool turns = 16 * i < rot_dim;
+  const bool halves = turns && !interleaved;
+  return {halves ? 8 * i : 16 * i, halves ? (rot_dim >> 1) + 8 * i : 16 * i + 8, turns};
+}
+
+// Turns the pairs of a and b by angles of cosine c and sine s (`back`: by their negatives).
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8], int interleaved, bool back) {
+  const float sign = back ? -1.0f : 1.0f;
+  if (interleaved) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a1 = a[2 * j], a2 = a[2 * j + 1], b1 = b[2 * j], b2 = b[2 * j + 1];
+      const float sa = sign * s[j], sb = sign * s[4 + j];
+      a[2 * j] = a1 * c[j] - a2 * sa;
+      a[2 * j + 1] = a2 * c[j] + a1 * sa;
+      b[2 * j] = b1 * c[4 + j] - b2 * sb;
+      b[2 * j + 1] = b2 * c[4 + j] + b1 * sb;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x1 = a[j], x2 = b[j], sj = sign * s[j];
+      a[j] = x1 * c[j] - x2 * sj;
+      b[j] = x2 * c[j] + x1 * sj;
+    }
+  }
+}
+
+// Sum over LANES (4, 8 or 16) neighbouring lanes, in every one of them.
+template <int LANES>
+__device__ __forceinline__ float head_sum(float v) {
+  v += dpp<kSwap1>(v, v);
+  v += dpp<kSwap2>(v, v);
+  if constexpr (LANES >= 8) v += dpp<kHalfMirror>(v, v);
+  if constexpr (LANES >= 16) v += dpp<kMirror>(v, v);
+  return v;
+}
+
+__device__ __forceinline__ void head_weight(const void* w, int w_fp32, int c, float (&x)[8]) {
+  if (w_fp32) load8(static_cast<const float*>(w) + c, x);
+  else load8(static_cast<const uint16_t*>(w) + c, x);
+}
+
+struct HeadsParams {
+  const void *q, *k, *qw, *kw;
+  void *q_out, *k_out;
+  const float* cos_sin;
+  const int32_t* positions;
+  int64_t ldq, ldk, ldqo, ldko, ld_cs;
+  float eps;
+  int T, Hq, Hk, w_fp32, max_pos, rot_dim, interleaved;
+  int first_group;  // the launch's first workgroup of the call's
+};
+
+// One head for D / 16 lanes.
+template <typename T, int D, bool STREAM>
+__global__ void __launch_bounds__(256) heads_kernel(const HeadsParams p) {
+  constexpr int kLanes = D / 16, kHeads = 256 / kLanes;
+  const int64_t item = ((int64_t)p.first_group + blockIdx.x) * kHeads + threadIdx.x / kLanes;
+  const int i = threadIdx.x % kLanes, heads = p.Hq + p.Hk;
+  const int token = (int)((uint32_t)item / (uint32_t)heads);
+  if (token >= p.T) return;
+  int h = (int)item - token * heads;
+  const bool key = h >= p.Hq;
+  if (key) h -= p.Hq;
+  const Columns at = columns_of(i, p.rot_dim, p.interleaved);
+  const T* x = key ? static_cast<const T*>(p.k) + token * p.ldk + h * D : static_cast<const T*>(p.q) + token * p.ldq + h * D;
+  T* y = key ? static_cast<T*>(p.k_out) + token * p.ldko + h * D : static_cast<T*>(p.q_out) + token * p.ldqo + h * D;
+  float a[8], b[8], wa[8], wb[8], c[8], s[8];
+  load8<STREAM>(x + at.lo, a);
+  load8<STREAM>(x + at.hi, b);
+  if (at.turns) {
+    const int position = min(max(p.positions ? p.positions[token] : token, 0), p.max_pos - 1);
+    const float* row = p.cos_sin + position * p.ld_cs + 8 * i;
+    load8(row, c);
+    load8(row + (p.rot_dim >> 1), s);
+  }
+  const void* w = key ? p.kw : p.qw;
+  head_weight(w, p.w_fp32, at.lo, wa);
+  head_weight(w, p.w_fp32, at.hi, wb);
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) ss += a[j] * a[j] + b[j] * b[j];
+  const float rstd = 1.0f / sqrtf(head_sum<kLanes>(ss) * (1.0f / D) + p.eps);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a[j] *= rstd * wa[j], b[j] *= rstd * wb[j];
+  if (at.turns) turn(a, b, c, s, p.interleaved, false);
+  store8(y + at.lo, a);
+  store8(y + at.hi, b);
+}
+
+struct HeadsGradParams {
+  const void *dq, *dk, *q, *k, *qw, *kw;
+  void *dq_out, *dk_out;
+  const float* cos_sin;
+  const int32_t* positions;
+  float* part;  // [gridDim.x][D]: each workgroup's sums for its weight's gradient
+  int64_t lddq, lddk, ldq, ldk, lddqo, lddko, ld_cs;
+  float eps;
+  int T, Hq, Hk, w_fp32, max_pos, rot_dim, interleaved;
+  int q_groups;  // workgroups of queries; the others take keys
+};
+
+// A workgroup takes heads of queries, or of keys, and keeps its sums for dw in registers over
+// all of them.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) heads_backward_kernel(const HeadsGradParams p) {
+  constexpr int kLanes = D / 16, kHeads = 256 / kLanes;
+  __shared__ __align__(16) float sums[4][D];
+  const bool key = (int)blockIdx.x >= p.q_groups;
+  const int heads = key ? p.Hk : p.Hq;
+  const int group = key ? blockIdx.x - p.q_groups : blockIdx.x, groups = key ? gridDim.x - p.q_groups : p.q_groups;
+  const int i = threadIdx.x % kLanes;
+  const Columns at = columns_of(i, p.rot_dim, p.interleaved);
+  const T* dy = static_cast<const T*>(key ? p.dk : p.dq);
+  const T* x = static_cast<const T*>(key ? p.k : p.q);
+  T* dx = static_cast<T*>(key ? p.dk_out : p.dq_out);
+  const int64_t lddy = key ? p.lddk : p.lddq, ldx = key ? p.ldk : p.ldq, lddx = key ? p.lddko : p.lddqo;
+  float wa[8], wb[8], da[8] = {}, db[8] = {};
+  const void* w = key ? p.kw : p.qw;
+  head_weight(w, p.w_fp32, at.lo, wa);
+  head_weight(w, p.w_fp32, at.hi, wb);
+  const int64_t items = (int64_t)p.T * heads;
+  for (int64_t item = (int64_t)group * kHeads + threadIdx.x / kLanes; item < items; item += (int64_t)groups * kHeads) {
+    const int token = (int)((uint32_t)item / (uint32_t)heads), h = (int)item - token * heads;
+    float ga[8], gb[8], xa[8], xb[8];
+    load8(dy + token * lddy + h * D + at.lo, ga);
+    load8(dy + token * lddy + h * D + at.hi, gb);
+    load8(x + token * ldx + h * D + at.lo, xa);
+    load8(x + token * ldx + h * D + at.hi, xb);
+    if (at.turns) {
+      float c[8], s[8];
+      const int position = min(max(p.positions ? p.positions[token] : token, 0), p.max_pos - 1);
+      const float* row = p.cos_sin + position * p.ld_cs + 8 * i;
+      load8(row, c);
+      load8(row + (p.rot_dim >> 1), s);
+      turn(ga, gb, c, s, p.interleaved, true);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss += xa[j] * xa[j] + xb[j] * xb[j];
+    const float rstd = 1.0f / sqrtf(head_sum<kLanes>(ss) * (1.0f / D) + p.eps);
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      xa[j] *= rstd, xb[j] *= rstd;
+      da[j] += ga[j] * xa[j], db[j] += gb[j] * xb[j];
+      ga[j] *= wa[j], gb[j] *= wb[j];
+      dot += ga[j] * xa[j] + gb[j] * xb[j];
+    }
+    const float mean = head_sum<kLanes>(dot) * (1.0f / D);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      ga[j] = rstd * (ga[j] - xa[j] * mean);
+      gb[j] = rstd * (gb[j] - xb[j] * mean);
+    }
+    store8(dx + token * lddx + h * D + at.lo, ga);
+    store8(dx + token * lddx + h * D + at.hi, gb);
+  }
+  // over the wave's heads, then over the waves
+#pragma unroll
+  for (int off = kLanes; off < 64; off <<= 1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) da[j] += __shfl_xor(da[j], off, 64), db[j] += __shfl_xor(db[j], off, 64);
+  }
+  if ((threadIdx.x & 63) < kLanes) {
+    store8(&sums[threadIdx.x >> 6][at.lo], da);
+    store8(&sums[threadIdx.x >> 6][at.hi], db);
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sum += sums[v][threadIdx.x];
+    p.part[(int64_t)blockIdx.x * D + threadIdx.x] = sum;
+  }
+}
+
+// dw of queries (workgroup 0) and keys (1): the sums of their workgroups, in a fixed order.
+__global__ void __launch_bounds__(1024) heads_weight_grad_kernel(const float* __restrict__ part, int q_groups, int groups, int D,
+                                                                 float* dqw, float* dkw) {
+  __shared__ float slices[1024];
+  const int first = blockIdx.x == 0 ? 0 : q_groups, last = blockIdx.x == 0 ? q_groups : groups;
+  const int column = threadIdx.x % D, slice = threadIdx.x / D, count = 1024 / D;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int g = first + slice; g < last; g += count) sum += part[(int64_t)g * D + column];
+  slices[threadIdx.x] = sum;
+  __syncthreads();
+  float* to = blockIdx.x == 0 ? dqw : dkw;
+  if (slice > 0 || !to) return;
+  for (int s = 1; s < count; ++s) sum += slices[s * D + column];
+  to[column] = sum;
+}
+
+}  // namespace fp8moe
