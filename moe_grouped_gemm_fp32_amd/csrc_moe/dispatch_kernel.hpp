@@ -1,11 +1,10 @@
 // Device code of the dispatch of tokens to experts: a stable counting sort of the choices by
 // expert, and the copy of the tokens' 8-bit rows and scales to their places.
 //
-// The choices are cut into pieces of kPiece, a workgroup each. Counting: a histogram of each
-// piece. Placing: each workgroup adds up the histograms before its own and all of them, which
-// gives every expert's segment and the first place of its own choices in it; equal experts
-// among 64 choices are found by comparing the bits of their numbers across the wave, so a
-// place depends on the order of choices alone, not on that of any atomics.
+// Every place is the beginning of its expert's segment, plus the choices of that expert in
+// the pieces before its own, plus those before it in the piece. Equal experts among 64
+// choices are found by comparing the bits of their numbers across the wave, so a place
+// depends on the order of choices alone, not on that of any atomics.
 #pragma once
 
 #include "common.hpp"
@@ -15,49 +14,104 @@ namespace fp8moe {
 using namespace fp8layer;
 
 constexpr int kMaxExperts = 1024;
-constexpr int kPiece = 1024;   // choices of a counting or placing workgroup
-constexpr int kAlign = 128;    // rows that a segment of the contiguous layout begins at multiples of
+constexpr int kPiece = 1024;     // choices of a counting or placing workgroup, a thread each
+constexpr int kFewChoices = 64;  // of a workgroup that dispatches a few tokens at once
+constexpr int kAlign = 128;      // rows that a segment of the contiguous layout begins at multiples of
 
 struct LayoutParams {
   const int32_t* ids;
-  int32_t* counted;  // [pieces][E]
+  int32_t* counted;  // [pieces + 1][E]: choices of each piece, then of those before it; last, all
   int32_t *positions, *sources, *m_indices, *counts;
   int64_t rows;
   int n, E, bits, max_m, pieces;
 };
 
-// Histogram of a piece.
-__global__ void __launch_bounds__(256) count_kernel(const LayoutParams p) {
+// Choices of each expert in a piece.
+__global__ void __launch_bounds__(kPiece) count_kernel(const LayoutParams p) {
   __shared__ int32_t histogram[kMaxExperts];
-  for (int e = threadIdx.x; e < p.E; e += 256) histogram[e] = 0;
+  for (int e = threadIdx.x; e < p.E; e += kPiece) histogram[e] = 0;
   __syncthreads();
-  const int first = blockIdx.x * kPiece, last = min(first + kPiece, p.n);
-  for (int i = first + threadIdx.x; i < last; i += 256) {
-    const int id = p.ids[i];
-    if ((unsigned)id < (unsigned)p.E) atomicAdd(&histogram[id], 1);
-  }
+  const int c = blockIdx.x * kPiece + threadIdx.x;
+  const int id = c < p.n ? p.ids[c] : -1;
+  if ((unsigned)id < (unsigned)p.E) atomicAdd(&histogram[id], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += 256) p.counted[(int64_t)blockIdx.x * p.E + e] = histogram[e];
+  for (int e = threadIdx.x; e < p.E; e += kPiece) p.counted[(int64_t)blockIdx.x * p.E + e] = histogram[e];
 }
 
-// Exclusive prefix sums of value(e), e < E, into out[0 .. E]; all 256 threads, at most 4 experts each.
+// From the pieces' counts those of the pieces before each, and the sums. 64 experts a
+// workgroup, a lane each; the pieces are cut among the waves, and read twice.
+__global__ void __launch_bounds__(1024) scan_kernel(const LayoutParams p) {
+  __shared__ int32_t sums[16][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, e = blockIdx.x * 64 + lane;
+  const int share = (p.pieces + 15) / 16, first = wave * share, last = min(first + share, p.pieces);
+  int32_t* column = p.counted + min(e, p.E - 1);
+  int sum = 0;
+#pragma unroll 8
+  for (int b = first; b < last; ++b) sum += column[(int64_t)b * p.E];
+  sums[wave][lane] = sum;
+  __syncthreads();
+  if (e >= p.E) return;
+  int before = 0;
+  for (int w = 0; w < wave; ++w) before += sums[w][lane];
+  if (wave == 15) column[(int64_t)p.pieces * p.E] = before + sum;
+#pragma unroll 8
+  for (int b = first; b < last; ++b) {
+    const int count = column[(int64_t)b * p.E];
+    column[(int64_t)b * p.E] = before;
+    before += count;
+  }
+}
+
+// Counts the choices before `first` into `before`, the others into `rest` (both zeroed). Eight
+// loads of a thread are in flight at once.
+template <int THREADS>
+__device__ __forceinline__ void count_all(const LayoutParams& p, int first, int32_t* before, int32_t* rest) {
+  for (int begin = 0; begin < p.n; begin += 8 * THREADS) {
+    int id[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = begin + j * THREADS + threadIdx.x;
+      id[j] = i < p.n ? p.ids[i] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = begin + j * THREADS + threadIdx.x;
+      if ((unsigned)id[j] < (unsigned)p.E) atomicAdd(i < first ? &before[id[j]] : &rest[id[j]], 1);
+    }
+  }
+}
+
+// Exclusive prefix sums of value(e), e < E, into out; by all threads, at most 4 experts each of
+// the first 256. `waves`: scratch for four.
 template <typename F>
 __device__ __forceinline__ void prefix(int E, int32_t* out, int32_t* waves, F value) {
-  const int each = (E + 255) / 256, begin = threadIdx.x * each;
-  int sum = 0;
-  for (int j = 0; j < each; ++j) sum += begin + j < E ? value(begin + j) : 0;
-  const int scan = wave_scan(sum), wave = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 63) waves[wave] = scan;
-  __syncthreads();
-  int at = scan - sum;
-  for (int w = 0; w < wave; ++w) at += waves[w];
-  for (int j = 0; j < each; ++j) {
-    if (begin + j > E) break;
-    out[begin + j] = at;
-    at += begin + j < E ? value(begin + j) : 0;
+  const int each = (E + 255) / 256, begin = threadIdx.x * each, wave = threadIdx.x >> 6;
+  int sum = 0, scan = 0;
+  if (wave < 4) {
+    for (int j = 0; j < each; ++j) sum += begin + j < E ? value(begin + j) : 0;
+    scan = wave_scan(sum);
+    if ((threadIdx.x & 63) == 63) waves[wave] = scan;
   }
-  if (begin + each == E) out[E] = at;
   __syncthreads();
+  if (wave < 4) {
+    int at = scan - sum;
+    for (int w = 0; w < wave; ++w) at += waves[w];
+    for (int j = 0; j < each; ++j) {
+      if (begin + j >= E) break;
+      out[begin + j] = at;
+      at += value(begin + j);
+    }
+  }
+  __syncthreads();
+}
+// The beginning of each expert's segment.
+__device__ __forceinline__ void segments(const LayoutParams& p, const int32_t* total, int32_t* start, int32_t* waves, int threads) {
+  if (p.max_m == 0) {
+    prefix(p.E, start, waves, [&](int e) { return (total[e] + kAlign - 1) / kAlign * kAlign; });
+  } else {
+    for (int e = threadIdx.x; e < p.E; e += threads) start[e] = e * p.max_m;
+    __syncthreads();
+  }
 }
 
 // Lanes whose number equals this lane's, among those that are `there`.
@@ -69,108 +123,90 @@ __device__ __forceinline__ uint64_t equals(int v, bool there, int bits) {
   }
   return same;
 }
+__device__ __forceinline__ int below(uint64_t lanes, int lane) { return __popcll(lanes & ((1ull << lane) - 1)); }
 
-// The layout. Workgroup b places the choices of its piece and marks its share of the rows
-// that hold none. LOCAL: the histograms are counted here, by every workgroup for itself.
-template <bool LOCAL>
-__global__ void __launch_bounds__(256) place_kernel(const LayoutParams p) {
-  __shared__ int32_t total[kMaxExperts], start[kMaxExperts + 1], at[4][kMaxExperts], waves[4];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int first = blockIdx.x * kPiece;
-  for (int e = threadIdx.x; e < p.E; e += 256) {
-    int before = 0, sum = 0;
-    if constexpr (!LOCAL) {
-#pragma unroll 8
-      for (int b = 0; b < p.pieces; ++b) {
-        const int c = p.counted[(int64_t)b * p.E + e];
-        before += b < (int)blockIdx.x ? c : 0;
-        sum += c;
-      }
+// Choice c of expert id goes to the rank-th row of its segment, if that is there.
+__device__ __forceinline__ int place(const LayoutParams& p, int id, int rank, const int32_t* start) {
+  const int64_t row = (int64_t)start[id] + rank;
+  return (p.max_m ? rank < p.max_m : row < p.rows) ? (int)row : -1;
+}
+
+// Marks the rows that hold no choice, and the experts of the others; `unit` of `units` waves.
+__device__ __forceinline__ void mark(const LayoutParams& p, const int32_t* total, const int32_t* start, int unit, int units) {
+  const int lane = threadIdx.x & 63;
+  if (p.max_m) {
+    const int runs = (p.max_m + 63) / 64;
+    for (int u = unit; u < p.E * runs; u += units) {
+      const int e = u / runs, r = (u - e * runs) * 64 + lane;
+      if (r < p.max_m && r >= total[e]) p.sources[(int64_t)e * p.max_m + r] = -1;
     }
-    total[e] = sum;
-    at[0][e] = before;
-    at[1][e] = at[2][e] = at[3][e] = 0;
+    return;
   }
-  __syncthreads();
-  if constexpr (LOCAL) {
-    for (int i = threadIdx.x; i < p.n; i += 256) {
-      const int id = p.ids[i];
-      if ((unsigned)id >= (unsigned)p.E) continue;
-      atomicAdd(&total[id], 1);
-      if (i < first) atomicAdd(&at[0][id], 1);
-    }
-    __syncthreads();
-  }
-  if (p.max_m == 0) {
-    prefix(p.E, start, waves, [&](int e) { return (total[e] + kAlign - 1) / kAlign * kAlign; });
-  } else {
-    for (int e = threadIdx.x; e <= p.E; e += 256) start[e] = e * p.max_m;
-    __syncthreads();
-  }
-  // A quarter of the piece for each wave: how many it has of each expert ..
-  constexpr int kShare = kPiece / 4;
-  const int begin = first + wave * kShare;
-  int ids[kShare / 64];
-#pragma unroll
-  for (int i = 0; i < kShare / 64; ++i) {
-    const int c = begin + i * 64 + lane;
-    ids[i] = c < p.n ? p.ids[c] : -1;
-    if ((unsigned)ids[i] >= (unsigned)p.E) ids[i] = -1;
-    if (ids[i] >= 0 && wave < 3) atomicAdd(&at[wave + 1][ids[i]], 1);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += 256) {
-    int sum = at[0][e];
-    for (int w = 1; w < 4; ++w) sum += at[w][e], at[w][e] = sum;
-  }
-  __syncthreads();
-  // .. then their ranks in the expert's segment, 64 choices at a time.
-#pragma unroll
-  for (int i = 0; i < kShare / 64; ++i) {
-    const int c = begin + i * 64 + lane, id = ids[i];
-    const uint64_t same = equals(id, id >= 0, p.bits);
-    if (id >= 0) {
-      const int rank = at[wave][id] + __popcll(same & ((1ull << lane) - 1));
-      const int64_t row = (int64_t)start[id] + rank;
-      const bool fits = p.max_m ? rank < p.max_m : row < p.rows;
-      p.positions[c] = fits ? (int)row : -1;
-      if (fits) p.sources[row] = c;
-    } else if (c < p.n) {
-      p.positions[c] = -1;
-    }
-    __builtin_amdgcn_wave_barrier();  // every lane has read its count before it grows
-    if (id >= 0 && (same >> lane) == 1) at[wave][id] += __popcll(same);
-    __builtin_amdgcn_wave_barrier();
-  }
-  if (blockIdx.x == 0) {
-    for (int e = threadIdx.x; e < p.E; e += 256) {
-      const int64_t room = p.max_m ? p.max_m : max((int64_t)0, p.rows - start[e]);
-      p.counts[e] = (int)min((int64_t)total[e], room);
-    }
-  }
-  // The rows' marks: 128 at a time, which lie in one segment of the contiguous layout.
-  const int64_t blocks = (p.rows + 127) / 128;
-  for (int64_t b = (int64_t)blockIdx.x * 4 + wave; b < blocks; b += (int64_t)gridDim.x * 4) {
-    if (p.max_m) {
-      for (int64_t r = b * 128 + lane; r < min(b * 128 + 128, p.rows); r += 64) {
-        const int e = (int)(r / p.max_m);
-        if ((int)(r - (int64_t)e * p.max_m) >= total[e]) p.sources[r] = -1;
-      }
-      continue;
-    }
+  const int blocks = (int)(p.rows / kAlign);
+  for (int b = unit; b < blocks; b += units) {
     // the last expert whose segment begins at or before the block; an empty one shares its place with the next
     int low = 0, high = p.E - 1;
     while (low < high) {
       const int mid = (low + high + 1) / 2;
-      if (start[mid] <= b * 128) low = mid;
+      if (start[mid] <= b * kAlign) low = mid;
       else high = mid - 1;
     }
     const int64_t end = (int64_t)start[low] + total[low];
-    for (int64_t r = b * 128 + lane; r < b * 128 + 128; r += 64) {
+#pragma unroll
+    for (int i = 0; i < kAlign; i += 64) {
+      const int64_t r = (int64_t)b * kAlign + i + lane;
       p.m_indices[r] = r < end ? low : -1;
       if (r >= end) p.sources[r] = -1;
     }
   }
+}
+__device__ __forceinline__ void write_counts(const LayoutParams& p, const int32_t* total, const int32_t* start, int threads) {
+  for (int e = threadIdx.x; e < p.E; e += threads) {
+    const int64_t room = p.max_m ? p.max_m : max((int64_t)0, p.rows - start[e]);
+    p.counts[e] = (int)min((int64_t)total[e], room);
+  }
+}
+
+// The layout, a piece a workgroup. LOCAL: every workgroup counts all choices for itself, which
+// saves the two launches that count.
+template <bool LOCAL>
+__global__ void __launch_bounds__(kPiece) place_kernel(const LayoutParams p) {
+  constexpr int kWaves = kPiece / 64;
+  __shared__ int32_t total[kMaxExperts], start[kMaxExperts], at[kWaves][kMaxExperts], waves[4];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int c = blockIdx.x * kPiece + threadIdx.x;
+  int id = c < p.n ? p.ids[c] : -1;
+  if ((unsigned)id >= (unsigned)p.E) id = -1;
+  for (int e = threadIdx.x; e < p.E; e += kPiece) {
+    total[e] = LOCAL ? 0 : p.counted[(int64_t)p.pieces * p.E + e];
+    at[0][e] = LOCAL ? 0 : p.counted[(int64_t)blockIdx.x * p.E + e];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) at[w][e] = 0;
+  }
+  __syncthreads();
+  if constexpr (LOCAL) {
+    count_all<kPiece>(p, blockIdx.x * kPiece, at[0], total);
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kPiece) total[e] += at[0][e];
+    __syncthreads();
+  }
+  // a wave's choices count for those after it
+  const uint64_t same = equals(id, id >= 0, p.bits);
+  if (id >= 0 && wave + 1 < kWaves && below(same, lane) == 0) at[wave + 1][id] = __popcll(same);
+  segments(p, total, start, waves, kPiece);  // and its barriers
+  for (int e = threadIdx.x; e < p.E; e += kPiece) {
+    int sum = at[0][e];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) sum += at[w][e], at[w][e] = sum;
+  }
+  __syncthreads();
+  if (c < p.n) {
+    const int row = id >= 0 ? place(p, id, at[wave][id] + below(same, lane), start) : -1;
+    p.positions[c] = row;
+    if (row >= 0) p.sources[row] = c;
+  }
+  if (blockIdx.x == 0) write_counts(p, total, start, kPiece);
+  mark(p, total, start, blockIdx.x * kWaves + wave, gridDim.x * kWaves);
 }
 
 struct GatherParams {
@@ -190,34 +226,51 @@ struct GatherParams {
 constexpr int kSlice = 64 * 16 * 4;   // bytes of a row that a wave holds
 constexpr int kScaleBlocks = 8;       // K blocks of a wave's scales
 
-// Rows and scales. A wave reads a slice of a token's codes once and writes it to each of the
-// token's places. Scales, which lie across the rows, are copied the other way: a wave takes
-// 64 neighbouring rows, whose scales it writes as whole lines.
+// Rows and scales. LANES lanes read a token's codes (a wave: a slice of them) once and write
+// them to each of the token's places. Scales, which lie across the rows, are copied the other
+// way: a wave takes 64 neighbouring rows, whose scales it writes as whole lines.
+template <int LANES>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
   const int lane = threadIdx.x & 63;
   const int64_t group = (int64_t)p.first_group + blockIdx.x;
   if (group < p.code_groups) {
-    const int64_t unit = group * 4 + (threadIdx.x >> 6);
-    const int64_t token = unit / p.slices;
-    if (token >= p.T) return;
-    const int column = (int)(unit - token * p.slices) * kSlice + lane * 16;
-    const uint8_t* from = p.Q + token * p.ldq + column;
-    uint4 v[4];
+    if constexpr (LANES < 64) {
+      const int64_t token = group * (256 / LANES) + threadIdx.x / LANES;
+      const int column = threadIdx.x % LANES * 16;
+      if (token >= p.T || column >= p.K) return;
+      const uint4 v = *reinterpret_cast<const uint4*>(p.Q + token * p.ldq + column);
+      const int32_t* positions = p.positions + token * p.top_k;
+      for (int first = 0; first < p.top_k; first += 4) {  // four choices' rows are looked up at once
+        int row[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (column + i * 1024 < p.K) v[i] = *reinterpret_cast<const uint4*>(from + i * 1024);
-    for (int j = 0; j < p.top_k; ++j) {
-      const int64_t row = p.positions[token * p.top_k + j];
-      if (row < 0 || row >= p.rows) continue;
-      uint8_t* to = p.Qx + row * p.ldqx + column;
+        for (int j = 0; j < 4; ++j) row[j] = first + j < p.top_k ? positions[first + j] : -1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (column + i * 1024 < p.K) *reinterpret_cast<uint4*>(to + i * 1024) = v[i];
+        for (int j = 0; j < 4; ++j)
+          if (row[j] >= 0 && row[j] < p.rows) *reinterpret_cast<uint4*>(p.Qx + row[j] * p.ldqx + column) = v;
+      }
+    } else {
+      const int64_t unit = group * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      const int64_t token = p.slices == 1 ? unit : unit / p.slices;
+      if (token >= p.T) return;
+      const int column = (int)(unit - token * p.slices) * kSlice + lane * 16;
+      const uint8_t* from = p.Q + token * p.ldq;
+      v4u v[kSlice / 1024];  // past the row's end its last ones again: branches around the loads cost registers
+#pragma unroll
+      for (int i = 0; i < kSlice / 1024; ++i) v[i] = *reinterpret_cast<const v4u*>(from + min(column + i * 1024, p.K - 16));
+      const int rows = lane < p.top_k ? p.positions[token * p.top_k + lane] : -1;
+      for (int j = 0; j < p.top_k; ++j) {
+        const int row = __builtin_amdgcn_readlane(rows, j);
+        if (row < 0 || row >= p.rows) continue;
+        uint8_t* to = p.Qx + row * p.ldqx + column;
+#pragma unroll
+        for (int i = 0; i < kSlice / 1024; ++i)
+          if (column + i * 1024 < p.K) *reinterpret_cast<v4u*>(to + i * 1024) = v[i];
+      }
     }
     return;
   }
   const int blocks = p.K >> 7, parts = (blocks + kScaleBlocks - 1) / kScaleBlocks;
-  const int64_t unit = (group - p.code_groups) * 4 + (threadIdx.x >> 6);
+  const int64_t unit = (group - p.code_groups) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t run = unit / parts;
   const int first = (int)(unit - run * parts) * kScaleBlocks;
   int64_t row, column;
@@ -237,9 +290,77 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
   const int token = source / p.top_k;
   const float w = p.weights ? p.weights[source] : 1.0f;
   const float* from = p.sa + token;
+  float s[kScaleBlocks];
 #pragma unroll
   for (int i = 0; i < kScaleBlocks; ++i)
-    if (first + i < blocks) to[(first + i) * p.ld_sax + column] = from[(first + i) * p.ld_sa] * w;
+    if (first + i < blocks) s[i] = from[(first + i) * p.ld_sa];
+#pragma unroll
+  for (int i = 0; i < kScaleBlocks; ++i)
+    if (first + i < blocks) to[(first + i) * p.ld_sax + column] = s[i] * w;
+}
+
+// Layout and rows of a few tokens in one launch: a workgroup takes `tokens` of them, at most
+// kFewChoices choices, counts all choices for itself, places its own and copies a slice of
+// their rows. Here scales are written one by one; there are few.
+struct FewParams {
+  LayoutParams layout;
+  GatherParams copy;
+  int tokens, slices, slice;  // slice: columns, a multiple of 128
+};
+__global__ void __launch_bounds__(256) dispatch_few_kernel(const FewParams f) {
+  __shared__ int32_t total[kMaxExperts], start[kMaxExperts], before[kMaxExperts], waves[4], rows[kFewChoices];
+  const LayoutParams& p = f.layout;
+  const GatherParams& g = f.copy;
+  const int part = blockIdx.x % f.slices, group = blockIdx.x / f.slices;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int first = group * f.tokens * g.top_k, mine = min(f.tokens * g.top_k, p.n - first);
+  for (int e = threadIdx.x; e < p.E; e += 256) total[e] = 0, before[e] = 0;
+  __syncthreads();
+  count_all<256>(p, first, before, total);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += 256) total[e] += before[e];
+  __syncthreads();
+  segments(p, total, start, waves, 256);
+  if (wave == 0) {
+    const int c = first + lane;
+    int id = lane < mine ? p.ids[c] : -1;
+    if ((unsigned)id >= (unsigned)p.E) id = -1;
+    const uint64_t same = equals(id, id >= 0, p.bits);
+    const int row = id >= 0 ? place(p, id, before[id] + below(same, lane), start) : -1;
+    rows[lane] = row;
+    if (part == 0 && lane < mine) {
+      p.positions[c] = row;
+      if (row >= 0) p.sources[row] = c;
+    }
+  }
+  __syncthreads();
+  const int begin = part * f.slice, end = min(begin + f.slice, g.K);
+  for (int t = 0; t * g.top_k < mine; ++t) {
+    const int64_t token = group * f.tokens + t;
+    for (int column = begin + threadIdx.x * 16; column < end; column += 256 * 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(g.Q + token * g.ldq + column);
+      for (int j = 0; j < g.top_k; ++j) {
+        const int row = rows[t * g.top_k + j];
+        if (row >= 0) *reinterpret_cast<uint4*>(g.Qx + row * g.ldqx + column) = v;
+      }
+    }
+    const int blocks = (end - begin) >> 7;
+    for (int i = threadIdx.x; i < blocks * g.top_k; i += 256) {
+      const int j = i / blocks, kb = (begin >> 7) + i - j * blocks;
+      const int row = rows[t * g.top_k + j];
+      if (row < 0) continue;
+      float s = g.sa[kb * g.ld_sa + token];
+      if (g.weights) s *= g.weights[token * g.top_k + j];
+      int64_t line = kb, at = row;
+      if (p.max_m) {
+        const int e = row / p.max_m;
+        line += (int64_t)e * (g.K >> 7), at = row - e * p.max_m;
+      }
+      g.sax[line * g.ld_sax + at] = s;
+    }
+  }
+  if (blockIdx.x == 0) write_counts(p, total, start, 256);
+  mark(p, total, start, blockIdx.x * 4 + wave, gridDim.x * 4);
 }
 
 }  // namespace fp8moe

@@ -106,8 +106,11 @@ int64_t fp8_moe_rows(int T, int top_k, int E) {
 namespace {
 
 // Choices up to which every placing workgroup counts them all itself, and the counting launch
-// is saved.
-constexpr int kCountedByAll = 4096;
+// and the one that adds up are saved.
+constexpr int kCountedByAll = 65536;
+// Choices up to which layout and rows are one launch, and the workgroups that tokens are cut into.
+constexpr int kFew = 4096;
+constexpr int kFewGroups = 512;
 
 bool gather_layout(const void* Q, int64_t ldq, const float* sa, int64_t ld_sa, const float* weights, const void* Qx, int64_t ldqx,
                    const float* sax, int64_t ld_sax, int64_t rows, int max_m, int T, int K) {
@@ -121,21 +124,30 @@ bool dispatch_shape(int64_t rows, int max_m, int T, int top_k, int E) {
 }
 bool gather_cols(int K) { return K >= 128 && K % 128 == 0 && K <= 65536; }
 
-int gather(const void* Q, int64_t ldq, const float* sa, int64_t ld_sa, const float* weights, void* Qx, int64_t ldqx, float* sax,
-           int64_t ld_sax, const int32_t* positions, const int32_t* sources, int64_t rows, int max_m, int T, int top_k, int E, int K,
-           hipStream_t stream) {
-  fp8moe::GatherParams p{static_cast<const uint8_t*>(Q), sa, weights, static_cast<uint8_t*>(Qx), sax, positions, sources, ldq, ld_sa,
-                         ldqx, ld_sax, rows, max_m, T, top_k, E, K, (int)ceil_div(K, fp8moe::kSlice), 0, 0, 0};
-  p.code_groups = ceil_div((int64_t)T * p.slices, 4);
-  p.row_groups = (int)ceil_div(max_m ? max_m : rows, 64);
-  const int64_t scale_units = (max_m ? E : 1) * (int64_t)p.row_groups * ceil_div(K / 128, fp8moe::kScaleBlocks);
-  const int64_t all = p.code_groups + ceil_div(scale_units, 4);
-  if (all > INT32_MAX) return FP8GEMM_ERR_SHAPE;
-  in_slices(all, 256, [&](int first, dim3 grid) {
-    p.first_group = first;
-    hipLaunchKernelGGL(fp8moe::gather_kernel, grid, dim3(256), 0, stream, p);
-  });
-  return launched();
+fp8moe::GatherParams gather_params(const void* Q, int64_t ldq, const float* sa, int64_t ld_sa, const float* weights, void* Qx,
+                                   int64_t ldqx, float* sax, int64_t ld_sax, const int32_t* positions, const int32_t* sources,
+                                   int64_t rows, int max_m, int T, int top_k, int E, int K) {
+  return {static_cast<const uint8_t*>(Q), sa, weights, static_cast<uint8_t*>(Qx), sax, positions, sources, ldq, ld_sa,
+          ldqx, ld_sax, rows, max_m, T, top_k, E, K, (int)ceil_div(K, fp8moe::kSlice), 0, (int)ceil_div(max_m ? max_m : rows, 64), 0};
+}
+int gather(fp8moe::GatherParams p, hipStream_t stream) {
+  auto go = [&](auto lanes) -> int {
+    constexpr int kLanes = decltype(lanes)::value;
+    p.code_groups = kLanes < 64 ? ceil_div(p.T, 256 / kLanes) : ceil_div((int64_t)p.T * p.slices, 4);
+    const int64_t scale_units = (p.max_m ? p.E : 1) * (int64_t)p.row_groups * ceil_div(p.K / 128, fp8moe::kScaleBlocks);
+    const int64_t all = p.code_groups + ceil_div(scale_units, 4);
+    if (all > INT32_MAX) return FP8GEMM_ERR_SHAPE;
+    in_slices(all, 256, [&](int first, dim3 grid) {
+      p.first_group = first;
+      hipLaunchKernelGGL(fp8moe::gather_kernel<kLanes>, grid, dim3(256), 0, stream, p);
+    });
+    return launched();
+  };
+  // lanes of 16 bytes: as many as a row has, where a wave can take several rows
+  if (p.K <= 128) return go(Int<8>{});
+  if (p.K <= 256) return go(Int<16>{});
+  if (p.K <= 512) return go(Int<32>{});
+  return go(Int<64>{});
 }
 
 }  // namespace
@@ -145,7 +157,7 @@ extern "C" {
 size_t fp8_moe_dispatch_workspace_size(int T, int top_k, int E) {
   if (T < 0 || top_k < 1 || top_k > kMaxChoices || E < 1 || E > kMaxExperts) return 0;
   const int64_t n = (int64_t)T * top_k;
-  return n <= kCountedByAll || n > kMost ? 0 : (size_t)ceil_div(n, kPiece) * E * sizeof(int32_t);
+  return n <= kCountedByAll || n > kMost ? 0 : (size_t)(ceil_div(n, kPiece) + 1) * E * sizeof(int32_t);
 }
 
 int fp8_moe_dispatch(const void* Q, int64_t ldq, const float* sa, int64_t ld_sa, const int32_t* ids, const float* weights, void* Qx,
@@ -171,15 +183,26 @@ int fp8_moe_dispatch(const void* Q, int64_t ldq, const float* sa, int64_t ld_sa,
   while ((1 << bits) < E) ++bits;
   const fp8moe::LayoutParams p{ids,  static_cast<int32_t*>(workspace), positions, sources, m_indices, counts, rows, n, E, bits, max_m,
                                std::max(1, (int)ceil_div(n, kPiece))};
+  const fp8moe::GatherParams copy =
+      gather_params(Q, ldq, sa, ld_sa, weights, Qx, ldqx, sax, ld_sax, positions, sources, rows, max_m, T, top_k, E, moves ? K : 0);
+  if (moves && n <= kFew) {
+    fp8moe::FewParams f{p, copy, (int)ceil_div(T, kFewGroups), 1, K};
+    const int groups = (int)ceil_div(T, f.tokens);
+    // slices of 4096 columns (16 a thread) where that gives more CUs a part
+    f.slices = (int)std::min<int64_t>(ceil_div(K, 4096), std::max(1, kFewGroups / groups));
+    f.slice = (int)ceil_div(ceil_div(K, f.slices), 128) * 128;
+    hipLaunchKernelGGL(fp8moe::dispatch_few_kernel, dim3(groups * f.slices), dim3(256), 0, stream, f);
+    return launched();
+  }
   if (need) {
-    hipLaunchKernelGGL(fp8moe::count_kernel, dim3(p.pieces), dim3(256), 0, stream, p);
-    hipLaunchKernelGGL(fp8moe::place_kernel<false>, dim3(p.pieces), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL(fp8moe::count_kernel, dim3(p.pieces), dim3(kPiece), 0, stream, p);
+    hipLaunchKernelGGL(fp8moe::scan_kernel, dim3((unsigned)ceil_div(E, 64)), dim3(1024), 0, stream, p);
+    hipLaunchKernelGGL(fp8moe::place_kernel<false>, dim3(p.pieces), dim3(kPiece), 0, stream, p);
   } else {
-    hipLaunchKernelGGL(fp8moe::place_kernel<true>, dim3(p.pieces), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL(fp8moe::place_kernel<true>, dim3(p.pieces), dim3(kPiece), 0, stream, p);
   }
   const int rc = launched();
-  if (rc != FP8GEMM_OK || !moves) return rc;
-  return gather(Q, ldq, sa, ld_sa, weights, Qx, ldqx, sax, ld_sax, positions, sources, rows, max_m, T, top_k, E, K, stream);
+  return rc != FP8GEMM_OK || !moves ? rc : gather(copy, stream);
 }
 
 int fp8_moe_gather(const void* Q, int64_t ldq, const float* sa, int64_t ld_sa, const float* weights, void* Qx, int64_t ldqx,
@@ -194,7 +217,7 @@ int fp8_moe_gather(const void* Q, int64_t ldq, const float* sa, int64_t ld_sa, c
   int cus;
   const int st = device(&cus);
   if (st != FP8GEMM_OK) return st;
-  return gather(Q, ldq, sa, ld_sa, weights, Qx, ldqx, sax, ld_sax, positions, sources, rows, max_m, T, top_k, E, K, stream);
+  return gather(gather_params(Q, ldq, sa, ld_sa, weights, Qx, ldqx, sax, ld_sax, positions, sources, rows, max_m, T, top_k, E, K), stream);
 }
 
 }  // extern "C"
