@@ -292,7 +292,7 @@ int fp8_moe_combine_backward(const void* dO, int64_t lddo, const void* Y, int64_
 namespace {
 
 // Workgroups of a gradient, at most: their sums are what the workspace holds.
-constexpr int kHeadGroups = 2048;
+constexpr int kHeadGroups = 1024;
 
 bool heads_shape(int T, int Hq, int Hk, int D, int max_pos, int rot_dim) {
   return T >= 0 && Hq >= 0 && Hk >= 0 && (D == 64 || D == 128 || D == 256) && rot_dim >= 0 && rot_dim <= D && rot_dim % 16 == 0 &&
@@ -349,7 +349,7 @@ int fp8_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int
 }
 
 size_t fp8_qk_norm_rope_backward_workspace_size(int D) {
-  return D == 64 || D == 128 || D == 256 ? (size_t)(2 * kHeadGroups) * D * sizeof(float) : 0;
+  return D == 64 || D == 128 || D == 256 ? (size_t)(kHeadGroups + 2) * D * sizeof(float) : 0;
 }
 
 int fp8_qk_norm_rope_backward(const void* dq, int64_t lddq, const void* dk, int64_t lddk, const void* q, int64_t ldq, const void* k,
@@ -376,13 +376,10 @@ int fp8_qk_norm_rope_backward(const void* dq, int64_t lddq, const void* dk, int6
   int cus;
   const int st = device(&cus);
   if (st != FP8GEMM_OK) return st;
-  // Workgroups in proportion to the heads, one pass over the heads if they are few.
-  const int64_t per_group = 256 * 16 / D;
-  const int64_t most = std::min<int64_t>(4 * (int64_t)cus, kHeadGroups), all = (int64_t)T * (Hq + Hk);
-  auto groups_of = [&](int64_t items) {
-    return items == 0 ? 0 : (int)std::max<int64_t>(1, std::min(ceil_div(items, per_group), most * items / all));
-  };
-  const int q_groups = groups_of((int64_t)T * Hq), k_groups = groups_of((int64_t)T * Hk);
+  // Every workgroup takes the same number of turns, of 4096 / D heads each; two workgroups a CU.
+  const int64_t per_turn = 256 * 16 / D, q_turns = ceil_div((int64_t)T * Hq, per_turn), k_turns = ceil_div((int64_t)T * Hk, per_turn);
+  const int64_t turns = std::max<int64_t>(1, ceil_div(q_turns + k_turns, std::min(2 * cus, kHeadGroups)));
+  const int q_groups = (int)ceil_div(q_turns, turns), k_groups = (int)ceil_div(k_turns, turns);
   const int groups = q_groups + k_groups;
   if (groups && (!workspace || workspace_bytes < (size_t)groups * D * sizeof(float))) return FP8GEMM_ERR_WORKSPACE;
   float* part = static_cast<float*>(workspace);
@@ -398,7 +395,8 @@ int fp8_qk_norm_rope_backward(const void* dq, int64_t lddq, const void* dk, int6
     const int rc = launched();
     if (rc != FP8GEMM_OK) return rc;
   }
-  hipLaunchKernelGGL(fp8moe::heads_weight_grad_kernel, dim3(2), dim3(1024), 0, stream, part, q_groups, groups, D, dqw, dkw);
+  hipLaunchKernelGGL(fp8moe::heads_weight_grad_kernel, dim3(2 * D / 16), dim3(1024), 0, stream, part, q_groups, groups, D, dqw,
+                     dkw);
   return launched();
 }
 

@@ -46,6 +46,8 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (
   }
 }
 
+constexpr int kTurn = 0x120;  // of a row's 16 lanes, by so many
+
 // Sum over LANES (4, 8 or 16) neighbouring lanes, in every one of them.
 template <int LANES>
 __device__ __forceinline__ float head_sum(float v) {
@@ -122,11 +124,11 @@ struct HeadsGradParams {
 };
 
 // A workgroup takes heads of queries, or of keys, and keeps its sums for dw in registers over
-// all of them.
+// all of them; the next heads are loaded while the present ones are worked on.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) heads_backward_kernel(const HeadsGradParams p) {
   constexpr int kLanes = D / 16, kHeads = 256 / kLanes;
-  __shared__ __align__(16) float sums[4][D];
+  __shared__ __align__(16) float sums[16][D];  // a row of 16 lanes each
   const bool key = (int)blockIdx.x >= p.q_groups;
   const int heads = key ? p.Hk : p.Hq;
   const int group = key ? blockIdx.x - p.q_groups : blockIdx.x, groups = key ? gridDim.x - p.q_groups : p.q_groups;
@@ -140,22 +142,31 @@ __global__ void __launch_bounds__(256) heads_backward_kernel(const HeadsGradPara
   const void* w = key ? p.kw : p.qw;
   head_weight(w, p.w_fp32, at.lo, wa);
   head_weight(w, p.w_fp32, at.hi, wb);
-  const int64_t items = (int64_t)p.T * heads;
-  for (int64_t item = (int64_t)group * kHeads + threadIdx.x / kLanes; item < items; item += (int64_t)groups * kHeads) {
-    const int token = (int)((uint32_t)item / (uint32_t)heads), h = (int)item - token * heads;
-    float ga[8], gb[8], xa[8], xb[8];
-    load8(dy + token * lddy + h * D + at.lo, ga);
-    load8(dy + token * lddy + h * D + at.hi, gb);
-    load8(x + token * ldx + h * D + at.lo, xa);
-    load8(x + token * ldx + h * D + at.hi, xb);
+  const int64_t items = (int64_t)p.T * heads, step = (int64_t)groups * kHeads;
+  Eight<T> ga0, gb0, xa0, xb0;
+  int token = 0, h = 0, position = 0;
+  auto fetch = [&](int64_t item) {
+    if (item >= items) return;
+    token = (int)((uint32_t)item / (uint32_t)heads), h = (int)item - token * heads;
+    ga0.load(dy + token * lddy + h * D + at.lo);
+    gb0.load(dy + token * lddy + h * D + at.hi);
+    xa0.load(x + token * ldx + h * D + at.lo);
+    xb0.load(x + token * ldx + h * D + at.hi);
+    position = p.positions ? p.positions[token] : token;
+  };
+  int64_t item = (int64_t)group * kHeads + threadIdx.x / kLanes;
+  fetch(item);
+  for (; item < items; item += step) {
+    float ga[8], gb[8], xa[8], xb[8], c[8], s[8];
+    ga0.get(ga), gb0.get(gb), xa0.get(xa), xb0.get(xb);
+    T* to = dx + token * lddx + h * D;
     if (at.turns) {
-      float c[8], s[8];
-      const int position = min(max(p.positions ? p.positions[token] : token, 0), p.max_pos - 1);
-      const float* row = p.cos_sin + position * p.ld_cs + 8 * i;
+      const float* row = p.cos_sin + min(max(position, 0), p.max_pos - 1) * p.ld_cs + 8 * i;
       load8(row, c);
       load8(row + (p.rot_dim >> 1), s);
-      turn(ga, gb, c, s, p.interleaved, true);
     }
+    fetch(item + step);
+    if (at.turns) turn(ga, gb, c, s, p.interleaved, true);
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss += xa[j] * xa[j] + xb[j] * xb[j];
@@ -174,42 +185,46 @@ __global__ void __launch_bounds__(256) heads_backward_kernel(const HeadsGradPara
       ga[j] = rstd * (ga[j] - xa[j] * mean);
       gb[j] = rstd * (gb[j] - xb[j] * mean);
     }
-    store8(dx + token * lddx + h * D + at.lo, ga);
-    store8(dx + token * lddx + h * D + at.hi, gb);
+    store8(to + at.lo, ga);
+    store8(to + at.hi, gb);
   }
-  // over the wave's heads, then over the waves
+  // over the heads of a row of lanes, then over the rows
 #pragma unroll
-  for (int off = kLanes; off < 64; off <<= 1) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) da[j] += __shfl_xor(da[j], off, 64), db[j] += __shfl_xor(db[j], off, 64);
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (kLanes <= 8) da[j] += dpp<kTurn + 8>(da[j], da[j]), db[j] += dpp<kTurn + 8>(db[j], db[j]);
+    if constexpr (kLanes <= 4) da[j] += dpp<kTurn + 4>(da[j], da[j]), db[j] += dpp<kTurn + 4>(db[j], db[j]);
   }
-  if ((threadIdx.x & 63) < kLanes) {
-    store8(&sums[threadIdx.x >> 6][at.lo], da);
-    store8(&sums[threadIdx.x >> 6][at.hi], db);
+  if ((threadIdx.x & 15) < kLanes) {
+    store8(&sums[threadIdx.x >> 4][at.lo], da);
+    store8(&sums[threadIdx.x >> 4][at.hi], db);
   }
   __syncthreads();
   if (threadIdx.x < D) {
     float sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) sum += sums[v][threadIdx.x];
+    for (int v = 0; v < 16; ++v) sum += sums[v][threadIdx.x];
     p.part[(int64_t)blockIdx.x * D + threadIdx.x] = sum;
   }
 }
 
-// dw of queries (workgroup 0) and keys (1): the sums of their workgroups, in a fixed order.
+// dw of queries, then of keys: the sums of their workgroups, in a fixed order, 16 columns a
+// workgroup by 64 slices of the parts.
 __global__ void __launch_bounds__(1024) heads_weight_grad_kernel(const float* __restrict__ part, int q_groups, int groups, int D,
                                                                  float* dqw, float* dkw) {
-  __shared__ float slices[1024];
-  const int first = blockIdx.x == 0 ? 0 : q_groups, last = blockIdx.x == 0 ? q_groups : groups;
-  const int column = threadIdx.x % D, slice = threadIdx.x / D, count = 1024 / D;
+  __shared__ float slices[64][16];
+  const bool key = (int)blockIdx.x * 16 >= D;
+  float* to = key ? dkw : dqw;
+  if (!to) return;
+  const int column = blockIdx.x * 16 - (key ? D : 0) + (threadIdx.x & 15), slice = threadIdx.x >> 4;
+  const int first = key ? q_groups : 0, last = key ? groups : q_groups;
   float sum = 0.f;
 #pragma unroll 4
-  for (int g = first + slice; g < last; g += count) sum += part[(int64_t)g * D + column];
-  slices[threadIdx.x] = sum;
+  for (int g = first + slice; g < last; g += 64) sum += part[(int64_t)g * D + column];
+  slices[slice][threadIdx.x & 15] = sum;
   __syncthreads();
-  float* to = blockIdx.x == 0 ? dqw : dkw;
-  if (slice > 0 || !to) return;
-  for (int s = 1; s < count; ++s) sum += slices[s * D + column];
+  if (slice > 0) return;
+#pragma unroll
+  for (int s = 1; s < 64; ++s) sum += slices[s][threadIdx.x];
   to[column] = sum;
 }
 
