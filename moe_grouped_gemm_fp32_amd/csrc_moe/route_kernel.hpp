@@ -12,22 +12,17 @@ constexpr float kNone = -__builtin_huge_valf();
 constexpr float kNanKey = -1e30f;  // below every key that is a number of any use
 constexpr float kTiny = 1e-20f;    // what a sum of chosen scores is divided with at least
 
-// exp(x) for x <= 0 or so: 2^(x log2 e) with the product's rounding error put back, which
-// would otherwise be |x| 2^-24 of the result.
+// exp(x): 2^(x log2 e) with the product's rounding error put back, which would otherwise be
+// |x| 2^-24 of the result.
 __device__ __forceinline__ float exp_near(float x) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746887e-8f;
   const float t = x * kLog2e;
   const float r = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t);
-  return t > -126.f && t < 127.f ? __builtin_fmaf(e, r * 0.693147180559945309f, e) : e;  // r is NaN or meaningless out there
+  return fabsf(t) < 126.f ? __builtin_fmaf(e, r * 0.693147180559945309f, e) : e;  // r is meaningless out there
 }
-
-// 1 / x to an ulp or so, for 1 <= x.
-__device__ __forceinline__ float reciprocal(float x) {
-  const float r = __builtin_amdgcn_rcpf(x);
-  return x < 0x1p100f ? __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r) : r;  // a step would turn 1 / inf into NaN
-}
-__device__ __forceinline__ float sigmoid(float x) { return reciprocal(1.0f + exp_near(-x)); }
+// Within 3 ulp: the exponential, the sum, the reciprocal.
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_near(-x)); }
 
 // A wave's maximum of doubles, in every lane (a rare path: through shuffles).
 __device__ __forceinline__ double wave_max(double v) {
@@ -69,60 +64,120 @@ __device__ __forceinline__ void own_lds() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 // A lane of the wave gets what the lane before it has; lane 0 its own.
-template <typename V>
-__device__ __forceinline__ V from_before(V v) {
-  return dpp<0x138>(v, v);
-}
-// v as an integer of the same order, and back.
+__device__ __forceinline__ int from_before(int v) { return dpp<0x138>(v, v); }
+
+// Keys are compared as integers of the floats' order (0 has one sign): the wave's data-parallel
+// maxima are single instructions then.
 __device__ __forceinline__ int ordered(float v) {
-  const int i = __float_as_int(v);
+  const int i = __float_as_int(v + 0.f);
   return i ^ ((i >> 31) & 0x7FFFFFFF);
 }
-__device__ __forceinline__ float ordered_back(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ float uniform(float v) { return __int_as_float(uniform(__float_as_int(v))); }
+__device__ __forceinline__ float value_of(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
+constexpr int kNoKey = (int)0x807FFFFF;  // of -inf
+constexpr int kLowest = (int)0x80000000;
 
-// Leaves the keys of the best groups, the others become -inf. A group's lanes are neighbours.
-// False where FP32 leaves open which groups are best (`tell`: keys are off by `slack`, as
-// described at choose()).
-template <int VPL, typename K>
-__device__ __forceinline__ bool keep_groups(const RouteParams& p, K (&key)[VPL], int lane, bool tell, float slack) {
-  const K none = (K)kNone;
-  K best = none, second = none;
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int max_with(int v) {
+  // all rows: every lane has a source
+  return max(v, __builtin_amdgcn_update_dpp(kLowest, v, CTRL, ROWS, 0xF, ROWS == 0xF));
+}
+template <int CTRL>
+__device__ __forceinline__ int moved(int v) {
+  return __builtin_amdgcn_update_dpp(kLowest, v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ int wave_max(int v) {
+  v = max_with<kMirror>(max_with<kHalfMirror>(max_with<kSwap2>(max_with<kSwap1>(v))));
+  return last_lane(max_with<kLast31, 0xC>(max_with<kLast15, 0xA>(v)));
+}
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int lanes_of(bool b) { return __popcll(__ballot(b)); }
+
+// Whether the lane's group is among the best. A group's lanes are neighbours. `sure` becomes
+// false where FP32 leaves that open (`tell`: keys are off by `slack`, as described at
+// choose()).
+template <int VPL>
+__device__ __forceinline__ bool best_groups(const RouteParams& p, const int (&key)[VPL], int lane, bool tell, float slack, bool& sure) {
+  int best = key[0], second = kNoKey;
+#pragma unroll
+  for (int j = 1; j < VPL; ++j) {
+    second = max(second, min(best, key[j]));
+    best = max(best, key[j]);
+  }
+  auto join = [&](int b, int s) {
+    second = max(max(second, s), min(best, b));
+    best = max(best, b);
+  };
+  // halves and rows are mirrored where the lanes below agree already
+  if (p.log_lanes > 0) join(moved<kSwap1>(best), moved<kSwap1>(second));
+  if (p.log_lanes > 1) join(moved<kSwap2>(best), moved<kSwap2>(second));
+  if (p.log_lanes > 2) join(moved<kHalfMirror>(best), moved<kHalfMirror>(second));
+  if (p.log_lanes > 3) join(moved<kMirror>(best), moved<kMirror>(second));
+  if (p.log_lanes > 4) join(__shfl_xor(best, 16, 64), __shfl_xor(second, 16, 64));
+  int score = best;
+  if (p.group_best == 2 && second > kNoKey) score = ordered(value_of(best) + value_of(second));
+  const int mine = lane >> p.log_lanes;
+  const bool there = mine < p.groups;
+  int rank = 0;
+  for (int g = 0; g < p.groups; ++g) rank += lane_value(score, g << p.log_lanes) > score;
+  // the ranks of different scores sum up to this; of equal ones the first groups are better
+  if (last_lane(wave_scan(there ? rank : 0)) >> p.log_lanes != p.groups * (p.groups - 1) / 2) {
+    for (int g = 0; g < p.groups; ++g) rank += lane_value(score, g << p.log_lanes) == score && g < mine;
+  }
+  if (tell) {
+    const int least = lane_value(score, __ffsll((unsigned long long)__ballot(there && rank == p.top_groups - 1)) - 1);
+    const int most = lane_value(score, __ffsll((unsigned long long)__ballot(there && rank == p.top_groups)) - 1);
+    // where nobody is left out, nothing was decided
+    sure = most == kNoKey || value_of(least) - value_of(most) > 2.f * (slack + 0x1p-22f * fabsf(value_of(most)));
+  }
+  return there && rank < p.top_groups;
+}
+
+// The same of keys in FP64.
+template <int VPL>
+__device__ __forceinline__ bool best_groups(const RouteParams& p, const double (&key)[VPL], int lane) {
+  const double none = (double)kNone;
+  double best = none, second = none;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     second = fmax(second, fmin(best, key[j]));
     best = fmax(best, key[j]);
   }
-  auto join = [&](K b, K s) {
+  for (int off = 1; off < 1 << p.log_lanes; off <<= 1) {
+    const double b = __shfl_xor(best, off, 64), s = __shfl_xor(second, off, 64);
     second = fmax(fmax(second, s), fmin(best, b));
     best = fmax(best, b);
-  };
-  if constexpr (sizeof(K) == 4) {
-    // halves and rows are mirrored where the lanes below agree already
-    if (p.log_lanes > 0) join(dpp<kSwap1>(best, best), dpp<kSwap1>(second, second));
-    if (p.log_lanes > 1) join(dpp<kSwap2>(best, best), dpp<kSwap2>(second, second));
-    if (p.log_lanes > 2) join(dpp<kHalfMirror>(best, best), dpp<kHalfMirror>(second, second));
-    if (p.log_lanes > 3) join(dpp<kMirror>(best, best), dpp<kMirror>(second, second));
-    if (p.log_lanes > 4) join(__shfl_xor(best, 16, 64), __shfl_xor(second, 16, 64));
-  } else {
-    for (int off = 1; off < 1 << p.log_lanes; off <<= 1) join(__shfl_xor(best, off, 64), __shfl_xor(second, off, 64));
   }
-  const K score = p.group_best == 2 && second > none ? best + second : best;
+  const double score = p.group_best == 2 && second > none ? best + second : best;
   const int mine = lane >> p.log_lanes;
   int rank = 0;
   for (int g = 0; g < p.groups; ++g) {
-    const K other = lane_value(score, g << p.log_lanes);
+    const double other = lane_value(score, g << p.log_lanes);
     rank += other > score || (other == score && g < mine);
   }
-  const bool kept = rank < p.top_groups;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) key[j] = kept ? key[j] : none;
-  if (!tell) return true;
-  const K least = -wave_max(kept && score > none ? -score : none), most = wave_max(!kept ? score : none);
-  // without a group that is left out, or with too few groups that have anyone, nothing was decided
-  return !(most > none) || least - most > (K)2 * (K)(slack + 0x1p-22f * (float)fabs(most));
+  return mine < p.groups && rank < p.top_groups;
 }
+
+// A row's keys in FP64.
+struct Exactly {
+  bool sigmoid, by_score;
+  double top, sum;  // of the softmax
+  template <int VPL>
+  __device__ __forceinline__ Exactly(bool sigmoid, bool by_score, float top, const float (&x)[VPL])
+      : sigmoid(sigmoid), by_score(by_score), top(top), sum(0.0) {
+    if (sigmoid || !by_score) return;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) sum += exp((double)x[j] - this->top);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  }
+  __device__ __forceinline__ double key(float x, float bias) const {
+    if (x == kNone) return (double)kNone;
+    double k = x;
+    if (by_score) k = (sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - top) / sum) + (double)bias;
+    return k == k ? k : (double)kNanKey;
+  }
+};
 
 // Which experts a row's keys choose, one maximum over the wave after another, in FP64: lane i <
 // top_k gets the i-th choice, -1 where none is left. A lane's experts are `base` and those
@@ -130,7 +185,6 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& p, K (&key)[VPL],
 template <int VPL>
 __device__ __forceinline__ int choose_slowly(const RouteParams& p, double (&key)[VPL], int base, int lane) {
   const double none = (double)kNone;
-  if (p.top_groups < p.groups) keep_groups<VPL, double>(p, key, lane, false, 0.f);
   int id = -1;
   for (int i = 0; i < p.top_k; ++i) {
     double top = key[0];
@@ -141,7 +195,7 @@ __device__ __forceinline__ int choose_slowly(const RouteParams& p, double (&key)
     const double m = wave_max(top);
     if (!(m > none)) break;
     const int from = __ffsll((unsigned long long)__ballot(top == m)) - 1;
-    const int e = __builtin_amdgcn_readlane(base + at, from);
+    const int e = lane_value(base + at, from);
     if (lane == i) id = e;
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
@@ -153,111 +207,134 @@ __device__ __forceinline__ int choose_slowly(const RouteParams& p, double (&key)
 constexpr int kEnough = 8;  // candidates beyond those needed that are ranked rather than searched on
 
 // The same in FP32, by a threshold that a few more keys than needed reach: those become
-// candidates, one a lane, and each counts the larger ones. Returns whether every decision was
-// wider than what FP32 leaves open, `slack` + 2^-22 of a key (0: the keys are exact); equal
-// keys of equal logits and biases are no question. `place`: LDS for 64 keys and numbers.
+// candidates, one a lane, and each counts the larger ones. A decision is sure where two keys
+// are further apart than FP32 leaves open, `slack` + 2^-22 of a key (without `tell` the keys
+// are exact), or have equal logits and biases. Otherwise the candidates, and whatever could
+// be among them, are ranked in FP64; false if they are too many for that. `place`: LDS for
+// 64 keys and numbers.
 template <int VPL, typename T>
-__device__ __forceinline__ bool choose(const RouteParams& p, float (&key)[VPL], int base, int lane, bool tell, float slack, const T* logits,
-                                       uint2* place, int& id, float& chosen) {
+__device__ __forceinline__ bool choose(const RouteParams& p, const int (&key)[VPL], const float (&x)[VPL], int base, int lane, bool tell,
+                                       float slack, float top_logit, const T* logits, int2* place, int& id) {
   id = -1;
-  int live = 0;
-  float top = kNone;
+  int live = 0, top = key[0];
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    live += __popcll(__ballot(key[j] > kNone));
-    top = fmaxf(top, key[j]);
+    live += lanes_of(key[j] > kNoKey);
+    top = max(top, key[j]);
   }
-  live = uniform(live);
   if (live == 0) return true;
-  const int need = min(p.top_k + (tell ? 1 : 0), live);  // one more: the first that is not chosen
+  const int need = min(p.top_k + (int)tell, live);  // one more: the first that is not chosen
   if (need > 64) return false;
   // Every run of lanes that has a key has one that reaches the least of the runs' maxima: the
   // longest runs, of up to 16 lanes, of which there are enough.
-  float run = top, least;
-  {
-    auto low = [&](float v) { return -wave_max(v > kNone ? -v : kNone); };
-    auto enough = [&](float v, int log) { return __popcll(__ballot(v > kNone)) >> log >= need; };
-    const float r1 = fmaxf(top, dpp<kSwap1>(top, top)), r2 = fmaxf(r1, dpp<kSwap2>(r1, r1));
-    const float r3 = fmaxf(r2, dpp<kHalfMirror>(r2, r2)), r4 = fmaxf(r3, dpp<kMirror>(r3, r3));
-    if (enough(r4, 4)) run = r4;
-    else if (enough(r3, 3)) run = r3;
-    else if (enough(r2, 2)) run = r2;
-    else if (enough(r1, 1)) run = r1;
-    least = enough(run, 0) ? low(run) : -__builtin_huge_valf();
-  }
-  auto reach = [&](float t) {
+  const int r1 = max_with<kSwap1>(top), r2 = max_with<kSwap2>(r1), r3 = max_with<kHalfMirror>(r2), r4 = max_with<kMirror>(r3);
+  int run = top;
+  if (lanes_of(r4 > kNoKey) >> 4 >= need) run = r4;
+  else if (lanes_of(r3 > kNoKey) >> 3 >= need) run = r3;
+  else if (lanes_of(r2 > kNoKey) >> 2 >= need) run = r2;
+  else if (lanes_of(r1 > kNoKey) >> 1 >= need) run = r1;
+  // `low` is reached by enough, `high` by too few
+  int low = kNoKey + 1, high = last_lane(max_with<kLast31, 0xC>(max_with<kLast15, 0xA>(r4))) + 1, count = live;
+  auto reach = [&](int t) {
     int n = 0;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) n += __popcll(__ballot(key[j] >= t));
-    return uniform(n);
+    for (int j = 0; j < VPL; ++j) n += lanes_of(key[j] >= t);
+    return n;
   };
-  // ``low`` is reached by enough, ``high`` by too few
-  int low = least > kNone ? ordered(least) : ordered(kNone) + 1, high = ordered(wave_max(top)) + 1;
-  int count = least > kNone ? reach(least) : live;
-  while (count > min(need + kEnough, 64) && (int64_t)high - low > 1) {
-    const int mid = (int)(((int64_t)low + high) >> 1);
-    const int n = reach(ordered_back(mid));
-    if (n >= need) low = mid, count = n;
-    else high = mid;
+  const int limit = min(need + kEnough, 64);
+  if (count > limit) {
+    if (lanes_of(run > kNoKey) >= need) {
+      low = ~wave_max(run > kNoKey ? ~run : kLowest);  // ~ turns the order of integers
+      count = reach(low);
+    }
+    while (count > limit && (unsigned)high - (unsigned)low > 1) {
+      const int mid = low + (int)(((unsigned)high - (unsigned)low) >> 1);
+      const int n = reach(mid);
+      if (n >= need) low = mid, count = n;
+      else high = mid;
+    }
   }
-  const float threshold = ordered_back(low);
   // Candidates in the order of experts. More than 64 are left only where no number lies between
   // the threshold and what too few reach: fewer than 64 keys are above it, and the first of
   // those that equal it come after them.
-  int mine = 0, first = 0;
-  if (count <= 64) {
+  auto candidates = [&](int t) {
+    int mine = 0;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) mine += key[j] >= threshold;
-    first = wave_scan(mine) - mine;
+    for (int j = 0; j < VPL; ++j) mine += key[j] >= t;
+    int first = wave_scan(mine) - mine;
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
-      if (key[j] >= threshold) place[first++] = make_uint2(__float_as_uint(key[j]), base + j);
+      if (key[j] >= t) place[first++] = make_int2(key[j], base + j);
+  };
+  if (count <= 64) {
+    candidates(low);
   } else {
-    int equal = 0;
+    int mine = 0, equal = 0;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) mine += key[j] > threshold, equal += key[j] == threshold;
+    for (int j = 0; j < VPL; ++j) mine += key[j] > low, equal += key[j] == low;
     const int scan = wave_scan(mine);
-    first = scan - mine;
-    int next = last_lane(scan) + wave_scan(equal) - equal;
+    int first = scan - mine, next = last_lane(scan) + wave_scan(equal) - equal;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      if (key[j] > threshold) place[first++] = make_uint2(__float_as_uint(key[j]), base + j);
-      if (key[j] == threshold && next < 64) place[next] = make_uint2(__float_as_uint(key[j]), base + j);
-      next += key[j] == threshold;
+      if (key[j] > low) place[first++] = make_int2(key[j], base + j);
+      if (key[j] == low && next < 64) place[next] = make_int2(key[j], base + j);
+      next += key[j] == low;
     }
     count = 64;
   }
   own_lds();
-  uint2 own = lane < count ? place[lane] : make_uint2(__float_as_uint(kNone), 0);
-  const float value = __uint_as_float(own.x);
+  int2 own = place[lane];
+  if (lane >= count) own.x = kLowest;
   int rank = 0;
-  for (int c = 0; c < count; ++c) rank += lane_value(value, c) > value;
-  if (lane >= count) rank = 0;
+  for (int c = 0; c < count; c += 4) {  // four at a time, at most 64; the lanes past the candidates are larger than none
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rank += lane_value(own.x, c + i) > own.x;
+  }
   // the ranks of different keys sum up to this; equal ones go by their order
-  if (last_lane(wave_scan(rank)) != count * (count - 1) / 2) {
-    for (int c = 0; c < count; ++c) rank += c < lane && lane_value(value, c) == value;
+  if (last_lane(wave_scan(lane < count ? rank : 0)) != count * (count - 1) / 2) {
+    for (int c = 0; c < count; ++c) rank += c < lane && lane_value(own.x, c) == own.x;
   }
   if (lane >= count) rank = lane;
-  const float sorted = __int_as_float(__builtin_amdgcn_ds_permute(rank * 4, __float_as_int(value)));
-  const int e = __builtin_amdgcn_ds_permute(rank * 4, (int)own.y);
-  id = lane < min(p.top_k, need) ? e : -1;
-  chosen = sorted;
-  if (!tell) return true;
-  const float before = from_before(sorted);
-  const int last = from_before(e);
-  bool open = lane > 0 && lane < need && !(before - sorted > slack + 0x1p-22f * fabsf(sorted));
-  if (__ballot(open) == 0) return true;
-  if (open) open = !(logit(logits + last) == logit(logits + e) && (!p.bias || p.bias[last] == p.bias[e]));
-  return __ballot(open) == 0;
+  int e = __builtin_amdgcn_ds_permute(rank * 4, own.y);
+  const int chosen = min(p.top_k, need);
+  if (tell) {
+    const int sorted = __builtin_amdgcn_ds_permute(rank * 4, own.x);
+    const float v = value_of(sorted), before = value_of(from_before(sorted));
+    bool open = lane > 0 && lane < need && !(before - v > slack + 0x1p-22f * fabsf(v));
+    if (__ballot(open) != 0) {
+      const int last = from_before(e);
+      if (open) open = !(logit(logits + last) == logit(logits + e) && (!p.bias || p.bias[last] == p.bias[e]));
+      if (__ballot(open) != 0) {
+        const float t = value_of(low);
+        low = ordered(t - (slack + 0x1p-22f * fabsf(t)));  // what does not reach this is less than those that are needed
+        count = low > kNoKey ? reach(low) : live;          // also where it is no number
+        if (count > 64) return false;
+        candidates(max(low, kNoKey + 1));
+        own_lds();
+        const Exactly exactly(p.sigmoid, true, top_logit, x);
+        e = lane < count ? place[lane].y : 0;
+        const double k = lane < count ? exactly.key(logit(logits + e), p.bias ? p.bias[e] : 0.f) : (double)kNone;
+        rank = 0;
+        for (int c = 0; c < count; ++c) {
+          const double other = lane_value(k, c);
+          rank += other > k || (other == k && c < lane);
+        }
+        if (lane >= count) rank = lane;
+        e = __builtin_amdgcn_ds_permute(rank * 4, e);
+      }
+    }
+  }
+  id = lane < chosen ? e : -1;
+  return true;
 }
 
-// One row a wave. The keys stay in registers, a group's in neighbouring lanes. Keys are FP32; a
-// row with a decision that FP32 leaves open (0.5% of rows of 256 sigmoid scores with a bias)
-// is decided again in FP64. Without a bias experts are compared by their logits, exactly.
+// One row a wave. The keys stay in registers, a group's in neighbouring lanes. Keys are FP32;
+// what they leave open (in 1% of rows of 256 sigmoid scores with a bias) is decided in FP64.
+// Without a bias experts are compared by their logits, exactly.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
-  __shared__ uint2 places[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ int2 places[4][64];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int64_t row = ((int64_t)p.first_group + blockIdx.x) * 4 + wave;
   if (row >= p.T) return;
   const T* logits = static_cast<const T*>(p.logits) + row * p.ldl;
@@ -267,71 +344,85 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
   const int base = group * p.size + begin;
   const bool limited = p.top_groups < p.groups;
   const bool by_score = p.bias || (p.group_best == 2 && limited);  // else the logits' order is the scores'
-  float x[VPL], key[VPL];
+  float x[VPL], s[VPL];
+  int key[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) x[j] = logit(logits + min(base + j, p.E - 1));
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) s[j] = p.bias ? p.bias[min(base + j, p.E - 1)] : 0.f;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) x[j] = j < count ? x[j] : kNone;
+  float top = 0.f, inverse = 0.f;
+  if (!p.sigmoid) {
+    int most = kLowest;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) most = max(most, x[j] == x[j] ? ordered(x[j]) : kLowest);
+    most = wave_max(most);
+    top = most > kNoKey ? value_of(most) : 0.f;
+    float total = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) total += exp_near(x[j] - top);  // 0 past the experts
+    total = wave_sum(total);
+    inverse = total == 0.f ? 0.f : 1.0f / total;
+  }
+  float slack = 0.f;
+  if (by_score || p.scores) {
+    float sc[VPL], largest = 0.f;
+    if (p.sigmoid) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) sc[j] = sigmoid(x[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) sc[j] = exp_near(x[j] - top) * inverse;
+    }
+    if (p.scores) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (j < count) p.scores[row * p.lds + base + j] = sc[j];
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      largest = fmaxf(largest, sc[j]);
+      s[j] += sc[j];
+    }
+    // The scores' error: the exponential, the sum's (common to a row) and the reciprocal. They
+    // are not negative, so their bits have their order.
+    slack = (p.sigmoid ? 0x1p-18f : 0x1p-17f) * __int_as_float(wave_max(__float_as_int(largest)));
+  }
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    x[j] = j < count ? logit(logits + base + j) : kNone;
-    key[j] = p.bias && j < count ? p.bias[base + j] : 0.f;
+    const float k = by_score ? s[j] : x[j];
+    key[j] = x[j] == kNone ? kNoKey : ordered(k == k ? k : kNanKey);
   }
-  float top = kNone, total = 0.f;
-  if (!p.sigmoid) {
+  auto exact_keys = [&](double (&wide)[VPL]) {
+    const Exactly exactly(p.sigmoid, by_score, top, x);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) top = fmaxf(top, x[j]);
-    top = wave_max(top);
-    if (!(top > kNone)) top = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) total += j < count ? exp_near(x[j] - top) : 0.f;
-    total = wave_sum(total);
-  }
-  const float inverse = total == 0.f ? 0.f : 1.0f / total;
-  auto score = [&](float v) { return p.sigmoid ? sigmoid(v) : exp_near(v - top) * inverse; };
-  float largest = kNone;
-  if (by_score || p.scores) {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const float s = score(x[j]);
-      if (j < count) {
-        largest = fmaxf(largest, s);
-        if (p.scores) p.scores[row * p.lds + base + j] = s;
-      }
-      const float k = s + key[j];
-      key[j] = x[j] == kNone ? kNone : k == k ? k : kNanKey;
+    for (int j = 0; j < VPL; ++j) wide[j] = exactly.key(x[j], p.bias ? p.bias[min(base + j, p.E - 1)] : 0.f);
+  };
+  if (limited) {
+    bool sure = true, kept = best_groups<VPL>(p, key, lane, by_score, slack, sure);
+    if (!sure) {
+      double wide[VPL];
+      exact_keys(wide);
+      kept = best_groups<VPL>(p, wide, lane);
     }
-  }
-  if (!by_score) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = x[j] == x[j] ? x[j] : kNanKey;
+    for (int j = 0; j < VPL; ++j) key[j] = kept ? key[j] : kNoKey;
   }
-  // The scores' error: the exponential, the sum's (common to a row) and the reciprocal.
-  const float slack = by_score ? (p.sigmoid ? 0x1p-18f : 0x1p-17f) * wave_max(largest) : 0.f;
   int id;
-  float chosen;
-  bool sure = !limited || keep_groups<VPL, float>(p, key, lane, by_score, slack);
-  if (sure) sure = choose<VPL>(p, key, base, lane, by_score, slack, logits, places[wave], id, chosen);
-  if (!sure) {
-    double wide[VPL], sum = 0.0;
+  if (!choose<VPL>(p, key, x, base, lane, by_score, slack, top, logits, places[wave], id)) {
+    double wide[VPL];
+    exact_keys(wide);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      x[j] = j < count ? logit(logits + base + j) : kNone;
-      if (!p.sigmoid) sum += j < count ? exp((double)x[j] - (double)top) : 0.0;
-    }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      double k = x[j];
-      if (by_score) {
-        k = p.sigmoid ? 1.0 / (1.0 + exp(-(double)x[j])) : exp((double)x[j] - (double)top) / sum;
-        if (p.bias && j < count) k += (double)p.bias[base + j];
-      }
-      wide[j] = x[j] == kNone ? (double)kNone : k == k ? k : (double)kNanKey;
-    }
+    for (int j = 0; j < VPL; ++j) wide[j] = key[j] == kNoKey ? (double)kNone : wide[j];
     id = choose_slowly<VPL>(p, wide, base, lane);
   }
-  float s = 0.f;
-  if (id >= 0) s = score(sure && !by_score && chosen > kNanKey ? chosen : logit(logits + id));
-  float w = s;
-  if (p.renormalize) w = s / (wave_sum(s) + kTiny);
+  float w = 0.f;
+  if (id >= 0) {
+    const float v = logit(logits + id);
+    w = p.sigmoid ? sigmoid(v) : exp_near(v - top) * inverse;
+  }
+  if (p.renormalize) w = w / (wave_sum(w) + kTiny);
   if (lane >= p.top_k) return;
   const int64_t out = row * p.top_k + lane;
   p.ids[out] = id;
