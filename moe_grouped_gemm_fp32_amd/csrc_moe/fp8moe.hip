@@ -25,11 +25,12 @@ bool rows_dtype(int t) { return norm_dtype(t); }
 bool narrow_rows(const void* p, int64_t ld, int E, size_t size) { return aligned(p, size) && ld >= E; }
 size_t size_of(int dtype) { return dtype == FP8GEMM_QUANT_BF16 ? 2 : 4; }
 
-// Calls f with the smallest power of two that is not below n, up to MOST, as a compile-time value.
-template <int MOST, int V = 1, typename F>
+// Calls f with the first of some counts in rising order that is not below n, or the last, as a
+// compile-time value.
+template <int V, int... MORE, typename F>
 void with_count(int n, F f) {
-  if constexpr (V < MOST) {
-    if (n > V) return with_count<MOST, 2 * V>(n, f);
+  if constexpr (sizeof...(MORE) > 0) {
+    if (n > V) return with_count<MORE...>(n, f);
   }
   f(Int<V>{});
 }
@@ -59,7 +60,7 @@ int fp8_moe_route(const void* logits, int64_t ldl, int dtype, const float* bias,
   fp8moe::RouteParams p{logits, bias,       ids,        weights,    scores,      ldl,         lds,  scale,     T,    E,
                         top_k,  groups,     top_groups, group_best, scoring == FP8MOE_SIGMOID, renormalize != 0, size, log_lanes, each, 0};
   with_type(dtype, [&](auto t) {
-    with_count<32>(each, [&](auto count) {
+    with_count<1, 2, 3, 4, 6, 8, 16, 32>(each, [&](auto count) {
       in_slices(ceil_div(T, 4), 256, [&](int first, dim3 grid) {
         p.first_group = first;
         hipLaunchKernelGGL((fp8moe::route_kernel<decltype(t), decltype(count)::value>), grid, dim3(256), 0, stream, p);
@@ -85,7 +86,7 @@ int fp8_moe_route_backward(const float* dweights, const void* logits, int64_t ld
   fp8moe::RouteGradParams p{dweights, dscores, logits, ids, dlogits, ldl, ldds, lddl, scale, T, E, top_k, scoring == FP8MOE_SIGMOID,
                             renormalize != 0, 0};
   with_type(dtype, [&](auto t) {
-    with_count<16>((int)ceil_div(E, 64), [&](auto count) {
+    with_count<1, 2, 3, 4, 6, 8, 12, 16>((int)ceil_div(E, 64), [&](auto count) {
       in_slices(ceil_div(T, 4), 256, [&](int first, dim3 grid) {
         p.first_group = first;
         hipLaunchKernelGGL((fp8moe::route_backward_kernel<decltype(t), decltype(count)::value>), grid, dim3(256), 0, stream, p);
@@ -376,9 +377,9 @@ int fp8_qk_norm_rope_backward(const void* dq, int64_t lddq, const void* dk, int6
   int cus;
   const int st = device(&cus);
   if (st != FP8GEMM_OK) return st;
-  // Every workgroup takes the same number of turns, of 4096 / D heads each; two workgroups a CU.
+  // Every workgroup takes the same number of turns, of 4096 / D heads each; four workgroups a CU.
   const int64_t per_turn = 256 * 16 / D, q_turns = ceil_div((int64_t)T * Hq, per_turn), k_turns = ceil_div((int64_t)T * Hk, per_turn);
-  const int64_t turns = std::max<int64_t>(1, ceil_div(q_turns + k_turns, std::min(2 * cus, kHeadGroups)));
+  const int64_t turns = std::max<int64_t>(1, ceil_div(q_turns + k_turns, std::min(4 * cus, kHeadGroups)));
   const int q_groups = (int)ceil_div(q_turns, turns), k_groups = (int)ceil_div(k_turns, turns);
   const int groups = q_groups + k_groups;
   if (groups && (!workspace || workspace_bytes < (size_t)groups * D * sizeof(float))) return FP8GEMM_ERR_WORKSPACE;

@@ -124,7 +124,8 @@ struct HeadsGradParams {
 };
 
 // A workgroup takes heads of queries, or of keys, and keeps its sums for dw in registers over
-// all of them; the next heads are loaded while the present ones are worked on.
+// all of them. Loading the next heads while the present ones are worked on changed nothing
+// (5003 x 32 heads of 64: 19.2 us with, 18.9 without, both launches).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) heads_backward_kernel(const HeadsGradParams p) {
   constexpr int kLanes = D / 16, kHeads = 256 / kLanes;
@@ -143,30 +144,22 @@ __global__ void __launch_bounds__(256) heads_backward_kernel(const HeadsGradPara
   head_weight(w, p.w_fp32, at.lo, wa);
   head_weight(w, p.w_fp32, at.hi, wb);
   const int64_t items = (int64_t)p.T * heads, step = (int64_t)groups * kHeads;
-  Eight<T> ga0, gb0, xa0, xb0;
-  int token = 0, h = 0, position = 0;
-  auto fetch = [&](int64_t item) {
-    if (item >= items) return;
-    token = (int)((uint32_t)item / (uint32_t)heads), h = (int)item - token * heads;
-    ga0.load(dy + token * lddy + h * D + at.lo);
-    gb0.load(dy + token * lddy + h * D + at.hi);
-    xa0.load(x + token * ldx + h * D + at.lo);
-    xb0.load(x + token * ldx + h * D + at.hi);
-    position = p.positions ? p.positions[token] : token;
-  };
-  int64_t item = (int64_t)group * kHeads + threadIdx.x / kLanes;
-  fetch(item);
-  for (; item < items; item += step) {
-    float ga[8], gb[8], xa[8], xb[8], c[8], s[8];
-    ga0.get(ga), gb0.get(gb), xa0.get(xa), xb0.get(xb);
+  for (int64_t item = (int64_t)group * kHeads + threadIdx.x / kLanes; item < items; item += step) {
+    const int token = (int)((uint32_t)item / (uint32_t)heads), h = (int)item - token * heads;
+    float ga[8], gb[8], xa[8], xb[8];
+    load8(dy + token * lddy + h * D + at.lo, ga);
+    load8(dy + token * lddy + h * D + at.hi, gb);
+    load8(x + token * ldx + h * D + at.lo, xa);
+    load8(x + token * ldx + h * D + at.hi, xb);
     T* to = dx + token * lddx + h * D;
     if (at.turns) {
+      float c[8], s[8];
+      const int position = p.positions ? p.positions[token] : token;
       const float* row = p.cos_sin + min(max(position, 0), p.max_pos - 1) * p.ld_cs + 8 * i;
       load8(row, c);
       load8(row + (p.rot_dim >> 1), s);
+      turn(ga, gb, c, s, p.interleaved, true);
     }
-    fetch(item + step);
-    if (at.turns) turn(ga, gb, c, s, p.interleaved, true);
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss += xa[j] * xa[j] + xb[j] * xb[j];
@@ -211,20 +204,23 @@ __global__ void __launch_bounds__(256) heads_backward_kernel(const HeadsGradPara
 // workgroup by 64 slices of the parts.
 __global__ void __launch_bounds__(1024) heads_weight_grad_kernel(const float* __restrict__ part, int q_groups, int groups, int D,
                                                                  float* dqw, float* dkw) {
-  __shared__ float slices[64][16];
+  __shared__ float waves[16][16];
   const bool key = (int)blockIdx.x * 16 >= D;
   float* to = key ? dkw : dqw;
   if (!to) return;
   const int column = blockIdx.x * 16 - (key ? D : 0) + (threadIdx.x & 15), slice = threadIdx.x >> 4;
   const int first = key ? q_groups : 0, last = key ? groups : q_groups;
   float sum = 0.f;
-#pragma unroll 4
+#pragma unroll 16
   for (int g = first + slice; g < last; g += 64) sum += part[(int64_t)g * D + column];
-  slices[slice][threadIdx.x & 15] = sum;
+  sum += __shfl_xor(sum, 16, 64);
+  sum += __shfl_xor(sum, 32, 64);
+  if ((threadIdx.x & 63) < 16) waves[threadIdx.x >> 6][threadIdx.x & 15] = sum;
   __syncthreads();
-  if (slice > 0) return;
+  if (threadIdx.x >= 16) return;
+  sum = 0.f;
 #pragma unroll
-  for (int s = 1; s < 64; ++s) sum += slices[s][threadIdx.x];
+  for (int w = 0; w < 16; ++w) sum += waves[w][threadIdx.x];
   to[column] = sum;
 }
 

@@ -89,6 +89,15 @@ __device__ __forceinline__ int wave_max(int v) {
   v = max_with<kMirror>(max_with<kHalfMirror>(max_with<kSwap2>(max_with<kSwap1>(v))));
   return last_lane(max_with<kLast31, 0xC>(max_with<kLast15, 0xA>(v)));
 }
+// The row's largest logit that is a number; 0 where there is none above -inf.
+template <int VPL>
+__device__ __forceinline__ float largest_number(const float (&x)[VPL]) {
+  float top = kNone;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) top = fmaxf(top, x[j]);
+  const int most = wave_max(ordered(top));
+  return most > kNoKey ? value_of(most) : 0.f;
+}
 __device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int lanes_of(bool b) { return __popcll(__ballot(b)); }
@@ -354,11 +363,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
   for (int j = 0; j < VPL; ++j) x[j] = j < count ? x[j] : kNone;
   float top = 0.f, inverse = 0.f;
   if (!p.sigmoid) {
-    int most = kLowest;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) most = max(most, x[j] == x[j] ? ordered(x[j]) : kLowest);
-    most = wave_max(most);
-    top = most > kNoKey ? value_of(most) : 0.f;
+    top = largest_number(x);
     float total = 0.f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) total += exp_near(x[j] - top);  // 0 past the experts
@@ -445,7 +450,7 @@ struct RouteGradParams {
 template <typename T, int VPL>
 __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradParams p) {
   __shared__ float spread[4][64 * VPL];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int64_t row = ((int64_t)p.first_group + blockIdx.x) * 4 + wave;
   if (row >= p.T) return;
   const T* logits = static_cast<const T*>(p.logits) + row * p.ldl;
@@ -457,20 +462,19 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradPara
     g = p.dweights[row * p.top_k + lane] * p.scale;
   }
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) x[j] = lane + 64 * j < p.E ? logit(logits + lane + 64 * j) : kNone;
+  for (int j = 0; j < VPL; ++j) x[j] = logit(logits + min(lane + 64 * j, p.E - 1));
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    ds[j] = p.dscores && lane + 64 * j < p.E ? p.dscores[row * p.ldds + lane + 64 * j] : 0.f;
+    ds[j] = p.dscores ? p.dscores[row * p.ldds + min(lane + 64 * j, p.E - 1)] : 0.f;
     spread[wave][lane + 64 * j] = 0.f;
   }
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) x[j] = lane + 64 * j < p.E ? x[j] : kNone;
   if ((unsigned)id >= (unsigned)p.E) id = -1, g = 0.f;
   if (id >= 0) xi = logit(logits + id);
-  float top = kNone, total = 0.f;
+  float top = 0.f, total = 0.f;
   if (!p.sigmoid) {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) top = fmaxf(top, x[j]);
-    top = wave_max(top);
-    if (!(top > kNone)) top = 0.f;
+    top = largest_number(x);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       x[j] = exp_near(x[j] - top);  // 0 past the experts
@@ -481,8 +485,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradPara
   const float inverse = total == 0.f ? 0.f : 1.0f / total;
   const float s = id < 0 ? 0.f : p.sigmoid ? sigmoid(xi) : exp_near(xi - top) * inverse;
   if (p.renormalize) {
-    const float sum = wave_sum(s) + kTiny, dot = wave_sum(g * s);
-    g = (g - dot / sum) / sum;
+    const float over = 1.0f / (wave_sum(s) + kTiny);
+    g = (g - wave_sum(g * s) * over) * over;
   }
   own_lds();
   if (id >= 0) atomicAdd(&spread[wave][id], g);
