@@ -58,9 +58,11 @@ int fp8_moe_route(const void* logits, int64_t ldl, int dtype, const float* bias,
   while ((1 << log_groups) < groups) ++log_groups;
   const int log_lanes = 6 - log_groups, size = E / groups, each = (int)ceil_div(size, 1 << log_lanes);
   fp8moe::RouteParams p{logits, bias,       ids,        weights,    scores,      ldl,         lds,  scale,     T,    E,
-                        top_k,  groups,     top_groups, group_best, scoring == FP8MOE_SIGMOID, renormalize != 0, size, log_lanes, each, 0};
+                        top_k,  groups,     top_groups, group_best, scoring == FP8MOE_SIGMOID, renormalize != 0, size, log_lanes, each,
+                        0,      0};
   with_type(dtype, [&](auto t) {
     with_count<1, 2, 3, 4, 6, 8, 16, 32>(each, [&](auto count) {
+      p.even = size == decltype(count)::value << log_lanes && groups == 1 << log_groups;
       in_slices(ceil_div(T, 4), 256, [&](int first, dim3 grid) {
         p.first_group = first;
         hipLaunchKernelGGL((fp8moe::route_kernel<decltype(t), decltype(count)::value>), grid, dim3(256), 0, stream, p);

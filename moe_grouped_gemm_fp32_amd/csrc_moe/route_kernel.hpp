@@ -23,6 +23,10 @@ __device__ __forceinline__ float exp_near(float x) {
 }
 // Within 3 ulp: the exponential, the sum, the reciprocal.
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_near(-x)); }
+// For keys: off by s (3 + 2 |x| (1 - s)) 2^-24.
+__device__ __forceinline__ float sigmoid_for_order(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269502162933349609375f));
+}
 
 // A wave's maximum of doubles, in every lane (a rare path: through shuffles).
 __device__ __forceinline__ double wave_max(double v) {
@@ -54,6 +58,7 @@ struct RouteParams {
   int size;       // experts of a group
   int log_lanes;  // lanes of a group: 64 over the power of two that is not below `groups`
   int each;       // experts of a lane, at most VPL
+  int even;       // whether every lane has VPL
   int first_group;  // the launch's first workgroup of the call's
 };
 
@@ -353,51 +358,73 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
   const int base = group * p.size + begin;
   const bool limited = p.top_groups < p.groups;
   const bool by_score = p.bias || (p.group_best == 2 && limited);  // else the logits' order is the scores'
-  float x[VPL], s[VPL];
+  float x[VPL], bias[VPL];
   int key[VPL];
+  if (p.even) {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) x[j] = logit(logits + min(base + j, p.E - 1));
+    for (int j = 0; j < VPL; ++j) x[j] = logit(logits + base + j);
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) s[j] = p.bias ? p.bias[min(base + j, p.E - 1)] : 0.f;
+    for (int j = 0; j < VPL; ++j) bias[j] = p.bias ? p.bias[base + j] : 0.f;
+  } else {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) x[j] = j < count ? x[j] : kNone;
-  float top = 0.f, inverse = 0.f;
+    for (int j = 0; j < VPL; ++j) x[j] = logit(logits + min(base + j, p.E - 1));
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) bias[j] = p.bias ? p.bias[min(base + j, p.E - 1)] : 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) x[j] = j < count ? x[j] : kNone;
+  }
+  float top = 0.f, inverse = 0.f, slack = 0.f;
+  float s[VPL];  // scores
   if (!p.sigmoid) {
     top = largest_number(x);
     float total = 0.f;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) total += exp_near(x[j] - top);  // 0 past the experts
+    for (int j = 0; j < VPL; ++j) {
+      s[j] = exp_near(x[j] - top);  // 0 past the experts
+      total += s[j];
+    }
     total = wave_sum(total);
     inverse = total == 0.f ? 0.f : 1.0f / total;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) s[j] *= inverse;
+  } else if (p.scores) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) s[j] = sigmoid(x[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) s[j] = sigmoid_for_order(x[j]);
   }
-  float slack = 0.f;
-  if (by_score || p.scores) {
-    float sc[VPL], largest = 0.f;
-    if (p.sigmoid) {
+  if (p.scores) {
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) sc[j] = sigmoid(x[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) sc[j] = exp_near(x[j] - top) * inverse;
-    }
-    if (p.scores) {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (j < count) p.scores[row * p.lds + base + j] = sc[j];
-    }
+    for (int j = 0; j < VPL; ++j)
+      if (j < count) p.scores[row * p.lds + base + j] = s[j];
+  }
+  if (by_score) {
+    float largest = 0.f, sum = 0.f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      largest = fmaxf(largest, sc[j]);
-      s[j] += sc[j];
+      largest = fmaxf(largest, s[j]);
+      s[j] += bias[j];
     }
-    // The scores' error: the exponential, the sum's (common to a row) and the reciprocal. They
-    // are not negative, so their bits have their order.
-    slack = (p.sigmoid ? 0x1p-18f : 0x1p-17f) * __int_as_float(wave_max(__float_as_int(largest)));
-  }
+    // What two scores' errors come to, twice over. They are not negative, so their bits have
+    // their order. Sigmoids: s |x| (1 - s) grows up to s = 1/4 and then stays below 0.28, and
+    // |x| < 0.7 (e + 1) for a largest score of 2^-e. Softmax: three roundings and the exponent's,
+    // and the sum's, common to a row, of up to 38 terms and levels.
+    const int bits = wave_max(__float_as_int(largest));
+    slack = __int_as_float(bits) * (p.sigmoid ? 0x1p-19f + 0x1p-21f * (float)(127 - (bits >> 23)) : 0x1p-17f);
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const float k = by_score ? s[j] : x[j];
-    key[j] = x[j] == kNone ? kNoKey : ordered(k == k ? k : kNanKey);
+    for (int j = 0; j < VPL; ++j) {
+      key[j] = x[j] == kNone ? kNoKey : ordered(s[j]);
+      sum += s[j];
+    }
+    if (__ballot(sum != sum) != 0) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (s[j] != s[j] && x[j] != kNone) key[j] = ordered(kNanKey);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = x[j] == x[j] ? ordered(x[j]) : ordered(kNanKey);
   }
   auto exact_keys = [&](double (&wide)[VPL]) {
     const Exactly exactly(p.sigmoid, by_score, top, x);

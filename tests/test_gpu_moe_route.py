@@ -95,6 +95,20 @@ def test_many_rows_where_keys_lie_close(cuda_device):
     assert fg.moe_route(y, 1, scoring="sigmoid")[0].flatten().tolist() == [0, 99, 200]
 
 
+@pytest.mark.parametrize("center", [-60.0, -30.0, -12.0, 0.0, 9.0])
+def test_keys_that_differ_by_a_few_roundings_at_every_size(cuda_device, center):
+    """Sigmoids of any magnitude, made almost equal by their biases."""
+    T, E, k = 300, 128, 8
+    g = synth.make_generator(11, cuda_device)
+    x = center + torch.randn(T, E, generator=g, device=cuda_device) * 1e-3
+    base = torch.sigmoid(x[0].double())
+    bias = (base.max() * 2 - base).float()
+    x[1:] = x[0] + torch.randint(-3, 4, (T - 1, E), generator=g, device=cuda_device) * abs(center) * 2.0 ** -23
+    check(x, k, bias, "sigmoid")
+    check(x, k, bias, "sigmoid", groups=4, top_groups=2, group_best=2)
+    check(x, k, bias, "softmax")
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_experts_that_are_not_there(cuda_device, scoring):
     T, E, k = 50, 96, 6
