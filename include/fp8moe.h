@@ -18,7 +18,8 @@
  * of rows are FP8GEMM_QUANT_BF16 and FP8GEMM_QUANT_FP32. Sums are FP32 in an order that the
  * shapes fix, so equal inputs give equal bits. Expert and row numbers on the device are not
  * trusted with addresses: one outside its range counts as none. A call without tokens
- * (T == 0) looks at no pointer to tokens' data. Arrays do not overlap, except where said.
+ * (T == 0) looks at no pointer to tokens' data. Arrays do not overlap, except where said;
+ * calls that may run at the same time do not share a workspace.
  */
 #ifndef FP8MOE_H_
 #define FP8MOE_H_
