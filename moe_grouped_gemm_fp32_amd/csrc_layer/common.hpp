@@ -99,7 +99,7 @@ __device__ __forceinline__ float dpp(float old, float v) {
   return __int_as_float(dpp<CTRL, ROWS>(__float_as_int(old), __float_as_int(v)));
 }
 constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;  // of a row's lanes
-constexpr int kShift = 0x110, kLast15 = 0x142, kLast31 = 0x143;
+constexpr int kShift = 0x110, kTurn = 0x120, kLast15 = 0x142, kLast31 = 0x143;  // shifts and turns of a row by 1 to 15
 
 // Inclusive prefix sum.
 template <typename T>

@@ -60,7 +60,23 @@ int fp8_moe_route(const void* logits, int64_t ldl, int dtype, const float* bias,
   fp8moe::RouteParams p{logits, bias,       ids,        weights,    scores,      ldl,         lds,  scale,     T,    E,
                         top_k,  groups,     top_groups, group_best, scoring == FP8MOE_SIGMOID, renormalize != 0, size, log_lanes, each,
                         0,      0};
+  // Experts of a lane where 16 lanes hold a row, and a group some of them. A wave for four rows,
+  // and for one, sigmoid with a bias: 16 experts, 1 token 2.3 and 2.6 us, 16384 5.2 and 7.4; 32, 1
+  // token 2.9 and 2.7, 65536 12.8 and 23.6, in 4 groups 4096 6.6 and 4.7 (a row that is done again
+  // waits for its wave), 16384 7.6 and 10.0; 64 experts, 16384 12.0 and 8.8.
+  const int of_16 = log_groups <= 4 ? (int)ceil_div(size, 1 << (log_lanes - 2)) : 0;
+  const bool four_rows = of_16 == 1 || (of_16 == 2 && T > 32 * cus);
   with_type(dtype, [&](auto t) {
+    if (four_rows) {
+      p.even = size == 1 << log_lanes && groups == 1 << log_groups;
+      with_count<1, 2>(of_16, [&](auto count) {
+        in_slices(ceil_div(T, 16), 256, [&](int first, dim3 grid) {
+          p.first_group = first;
+          hipLaunchKernelGGL((fp8moe::route_rows_kernel<decltype(t), decltype(count)::value>), grid, dim3(256), 0, stream, p);
+        });
+      });
+      return;
+    }
     with_count<1, 2, 3, 4, 6, 8, 16, 32>(each, [&](auto count) {
       p.even = size == decltype(count)::value << log_lanes && groups == 1 << log_groups;
       in_slices(ceil_div(T, 4), 256, [&](int first, dim3 grid) {

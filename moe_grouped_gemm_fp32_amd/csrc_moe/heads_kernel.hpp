@@ -46,8 +46,6 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (
   }
 }
 
-constexpr int kTurn = 0x120;  // of a row's 16 lanes, by so many
-
 // Sum over LANES (4, 8 or 16) neighbouring lanes, in every one of them.
 template <int LANES>
 __device__ __forceinline__ float head_sum(float v) {

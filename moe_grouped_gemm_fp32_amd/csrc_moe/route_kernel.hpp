@@ -2,6 +2,8 @@
 // the gradient of the logits.
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace fp8moe {
@@ -342,15 +344,19 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const int (&key)[VP
   return true;
 }
 
-// One row a wave. The keys stay in registers, a group's in neighbouring lanes. Keys are FP32;
+// How far two keys' errors come to, twice over, for a row's largest score, whose bits have the
+// order of what is not negative. Sigmoids: s |x| (1 - s) grows up to s = 1/4 and then stays below
+// 0.28, and |x| < 0.7 (e + 1) for a largest score of 2^-e. Softmax: three roundings and the
+// exponent's, and the sum's, common to a row, of up to 38 terms and levels.
+__device__ __forceinline__ float slack_of(int largest, int sigmoid) {
+  return __int_as_float(largest) * (sigmoid ? 0x1p-19f + 0x1p-21f * (float)(127 - (largest >> 23)) : 0x1p-17f);
+}
+
+// One row, by a wave. The keys stay in registers, a group's in neighbouring lanes. Keys are FP32;
 // what they leave open (in 1% of rows of 256 sigmoid scores with a bias) is decided in FP64.
 // Without a bias experts are compared by their logits, exactly.
 template <typename T, int VPL>
-__global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
-  __shared__ int2 places[4][64];
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int64_t row = ((int64_t)p.first_group + blockIdx.x) * 4 + wave;
-  if (row >= p.T) return;
+__device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int lane, int2* place) {
   const T* logits = static_cast<const T*>(p.logits) + row * p.ldl;
   const int group = lane >> p.log_lanes, sub = lane & ((1 << p.log_lanes) - 1);
   const int begin = sub * p.each;  // within the group
@@ -406,12 +412,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
       largest = fmaxf(largest, s[j]);
       s[j] += bias[j];
     }
-    // What two scores' errors come to, twice over. They are not negative, so their bits have
-    // their order. Sigmoids: s |x| (1 - s) grows up to s = 1/4 and then stays below 0.28, and
-    // |x| < 0.7 (e + 1) for a largest score of 2^-e. Softmax: three roundings and the exponent's,
-    // and the sum's, common to a row, of up to 38 terms and levels.
-    const int bits = wave_max(__float_as_int(largest));
-    slack = __int_as_float(bits) * (p.sigmoid ? 0x1p-19f + 0x1p-21f * (float)(127 - (bits >> 23)) : 0x1p-17f);
+    slack = slack_of(wave_max(__float_as_int(largest)), p.sigmoid);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       key[j] = x[j] == kNone ? kNoKey : ordered(s[j]);
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
     for (int j = 0; j < VPL; ++j) key[j] = kept ? key[j] : kNoKey;
   }
   int id;
-  if (!choose<VPL>(p, key, x, base, lane, by_score, slack, top, logits, places[wave], id)) {
+  if (!choose<VPL>(p, key, x, base, lane, by_score, slack, top, logits, place, id)) {
     double wide[VPL];
     exact_keys(wide);
 #pragma unroll
@@ -455,10 +456,201 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
     w = p.sigmoid ? sigmoid(v) : exp_near(v - top) * inverse;
   }
   if (p.renormalize) w = w / (wave_sum(w) + kTiny);
-  if (lane >= p.top_k) return;
-  const int64_t out = row * p.top_k + lane;
-  p.ids[out] = id;
-  p.weights[out] = w * p.scale;
+  if (lane < p.top_k) {
+    const int64_t out = row * p.top_k + lane;
+    p.ids[out] = id;
+    p.weights[out] = w * p.scale;
+  }
+}
+
+// What the lanes of a row of 16 hold comes by every lane of it in turn: f(values, turn).
+template <int D>
+__device__ __forceinline__ int turned(int v) {
+  if constexpr (D == 0) return v;
+  else return moved<kTurn + D>(v);
+}
+template <int D = 0, int VPL, typename F>
+__device__ __forceinline__ void each_turn(const int (&key)[VPL], F f) {
+  int other[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) other[j] = turned<D>(key[j]);
+  f(other, std::integral_constant<int, D>{});
+  if constexpr (D < 15) each_turn<D + 1>(key, f);
+}
+__device__ __forceinline__ int row16_max(int v) { return max_with<kMirror>(max_with<kHalfMirror>(max_with<kSwap2>(max_with<kSwap1>(v)))); }
+template <typename V>
+__device__ __forceinline__ V row16_sum(V v) {
+  v += dpp<kSwap1>(v, v);
+  v += dpp<kSwap2>(v, v);
+  v += dpp<kHalfMirror>(v, v);
+  return v + dpp<kMirror>(v, v);
+}
+
+template <typename T, int VPL>
+__global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
+  __shared__ int2 places[4][64];
+  const int wave = uniform(threadIdx.x >> 6);
+  const int64_t row = ((int64_t)p.first_group + blockIdx.x) * 4 + wave;
+  if (row < p.T) route_row<T, VPL>(p, row, threadIdx.x & 63, places[wave]);
+}
+
+// Four rows a wave, of few experts: 16 lanes hold a row, VPL experts each, and every key counts
+// the larger ones of its row as they come by. A row that FP32 leaves open is done again by
+// route_row().
+template <typename T, int VPL>
+__global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
+  __shared__ int2 places[4][64];
+  __shared__ int2 order[4][4][16 * VPL];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), sub16 = lane & 15, mine = lane >> 4;
+  const int64_t first_row = (((int64_t)p.first_group + blockIdx.x) * 4 + wave) * 4;
+  if (first_row >= p.T) return;
+  const int64_t row = min(first_row + mine, (int64_t)p.T - 1);  // rows past the last are done and not written
+  const bool there = first_row + mine < p.T;
+  const int log_lanes = p.log_lanes - 2, each = (p.size + (1 << log_lanes) - 1) >> log_lanes;
+  const T* logits = static_cast<const T*>(p.logits) + row * p.ldl;
+  const int group = sub16 >> log_lanes, begin = (sub16 & ((1 << log_lanes) - 1)) * each;
+  const int count = group < p.groups ? min(max(p.size - begin, 0), each) : 0;
+  const int base = group * p.size + begin;
+  const bool limited = p.top_groups < p.groups;
+  const bool by_score = p.bias || (p.group_best == 2 && limited);
+  float x[VPL], s[VPL];
+  int key[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) x[j] = logit(logits + min(base + j, p.E - 1));
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) x[j] = j < count ? x[j] : kNone;
+  float top = 0.f, inverse = 0.f, slack = 0.f;
+  if (p.sigmoid) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) s[j] = sigmoid(x[j]);
+  } else {
+    float most = kNone, total = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) most = fmaxf(most, x[j]);
+    const int bits = row16_max(ordered(most));
+    top = bits > kNoKey ? value_of(bits) : 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      s[j] = exp_near(x[j] - top);
+      total += s[j];
+    }
+    total = row16_sum(total);
+    inverse = total == 0.f ? 0.f : 1.0f / total;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) s[j] *= inverse;
+  }
+  if (p.scores && there) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (j < count) p.scores[row * p.lds + base + j] = s[j];
+  }
+  if (by_score) {
+    float largest = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      largest = fmaxf(largest, s[j]);
+      const float k = p.bias ? s[j] + p.bias[min(base + j, p.E - 1)] : s[j];
+      key[j] = x[j] == kNone ? kNoKey : ordered(k == k ? k : kNanKey);
+    }
+    slack = slack_of(row16_max(__float_as_int(largest)), p.sigmoid);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = ordered(x[j] == x[j] ? x[j] : kNanKey);
+  }
+  bool open = false;
+  if (limited) {
+    int best = key[0], second = kNoKey;
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) {
+      second = max(second, min(best, key[j]));
+      best = max(best, key[j]);
+    }
+    auto join = [&](int b, int t) {
+      second = max(max(second, t), min(best, b));
+      best = max(best, b);
+    };
+    if (log_lanes > 0) join(moved<kSwap1>(best), moved<kSwap1>(second));
+    if (log_lanes > 1) join(moved<kSwap2>(best), moved<kSwap2>(second));
+    if (log_lanes > 2) join(moved<kHalfMirror>(best), moved<kHalfMirror>(second));
+    int score[1] = {best}, number[1] = {group};
+    if (p.group_best == 2 && second > kNoKey) score[0] = ordered(value_of(best) + value_of(second));
+    int rank = 0;  // in lanes
+    each_turn(score, [&](const int (&other)[1], auto) { rank += other[0] > score[0]; });
+    const bool is = group < p.groups;
+    if (__ballot(row16_sum(is ? rank : 0) != p.groups * (p.groups - 1) / 2 << 2 * log_lanes) != 0) {
+      each_turn(number, [&](const int (&other)[1], auto d) {
+        rank += turned<decltype(d)::value>(score[0]) == score[0] && other[0] < group;
+      });
+    }
+    rank >>= log_lanes;
+    if (by_score) {
+      const int least = row16_max(is && rank == p.top_groups - 1 ? score[0] : kNoKey), most = row16_max(is && rank == p.top_groups ? score[0] : kNoKey);
+      open = most != kNoKey && !(value_of(least) - value_of(most) > 2.f * (slack + 0x1p-22f * fabsf(value_of(most))));
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = is && rank < p.top_groups ? key[j] : kNoKey;
+  }
+  int live = 0, rank[VPL], sum = 0;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) live += key[j] > kNoKey, rank[j] = 0;
+  live = row16_sum(live);
+  each_turn(key, [&](const int (&other)[VPL], auto) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) rank[j] += other[i] > key[j];
+  });
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) sum += key[j] > kNoKey ? rank[j] : 0;
+  if (__ballot(row16_sum(sum) != live * (live - 1) / 2) != 0) {  // equal keys go by their numbers
+    int number[1] = {base};
+    each_turn(number, [&](const int (&other)[1], auto d) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int theirs = turned<decltype(d)::value>(key[i]);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) rank[j] += theirs == key[j] && other[0] + i < base + j;
+      }
+    });
+  }
+  if (by_score) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (key[j] > kNoKey) order[wave][mine][rank[j]] = make_int2(key[j], base + j);
+    own_lds();
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      if (key[j] == kNoKey || rank[j] >= p.top_k || rank[j] + 1 >= live) continue;
+      const int2 next = order[wave][mine][rank[j] + 1];
+      const float v = value_of(key[j]), after = value_of(next.x);
+      if (!(v - after > slack + 0x1p-22f * fabsf(after)))
+        open = open || !(x[j] == logit(logits + next.y) && (!p.bias || p.bias[base + j] == p.bias[next.y]));
+    }
+  }
+  uint64_t left = __ballot(open && there);
+  const bool again = (left >> (lane & 48) & 0xFFFF) != 0;
+  float w[VPL], total = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    w[j] = key[j] > kNoKey && rank[j] < p.top_k ? s[j] : 0.f;
+    total += w[j];
+  }
+  const float over = p.renormalize ? p.scale / (row16_sum(total) + kTiny) : p.scale;
+  if (there && !again) {
+    const int64_t out = row * p.top_k;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      if (key[j] == kNoKey || rank[j] >= p.top_k) continue;
+      p.ids[out + rank[j]] = base + j;
+      p.weights[out + rank[j]] = w[j] * over;
+    }
+    for (int i = live + sub16; i < p.top_k; i += 16) p.ids[out + i] = -1, p.weights[out + i] = 0.f;
+  }
+  while (left != 0) {
+    const int which = uniform((__ffsll((unsigned long long)left) - 1) >> 4);
+    left &= ~(0xFFFFull << 16 * which);
+    route_row<T, 1>(p, first_row + which, lane, places[wave]);
+  }
 }
 
 struct RouteGradParams {

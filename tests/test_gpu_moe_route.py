@@ -77,6 +77,24 @@ def test_groups(cuda_device, best, scoring, E, groups, top_groups, k):
             check(x, k, b, scoring, groups=groups, top_groups=top_groups, group_best=best)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,top_groups,best", [(203, 2, 1, 1, 1, 1), (1, 16, 16, 1, 1, 1), (17, 17, 3, 1, 1, 1), (98, 32, 4, 4, 2, 2),
+                                                          (350, 48, 6, 3, 2, 2), (62, 64, 8, 8, 4, 2), (33, 64, 64, 1, 1, 1), (35, 64, 6, 16, 3, 1),
+                                                          (500, 60, 7, 15, 4, 2), (31, 40, 40, 5, 5, 1), (64, 16, 2, 16, 9, 2),
+                                                          (8201, 32, 5, 4, 2, 2), (8200, 20, 3, 2, 1, 1), (8300, 32, 15, 1, 1, 1)])
+def test_few_experts(cuda_device, scoring, T, E, k, groups, top_groups, best):
+    bias = torch.randn(E, generator=synth.make_generator(2, cuda_device), device=cuda_device) * 0.1
+    for dtype in (FP32, BF16):
+        x = logits_of(T, E, dtype, 13, cuda_device, pad=1)
+        x[T // 2, E // 2:] = -float("inf")
+        x[T - 1] = x[T - 1, 0]  # ties
+        for b in (None, bias, torch.zeros_like(bias)):
+            check(x, k, b, scoring, groups=groups, top_groups=top_groups, group_best=best, scale=-0.5)
+    x = x.float()
+    x[:, 1:] = x[:, :1] + torch.randint(-2, 3, (T, E - 1), generator=synth.make_generator(3, cuda_device), device=cuda_device) * 2.0 ** -24
+    check(x, k, bias * 2.0 ** -18, scoring, groups=groups, top_groups=top_groups, group_best=best)
+
+
 def test_many_rows_where_keys_lie_close(cuda_device):
     """Keys nearer to each other than FP32 can tell: spaced by 2^-30 of a score, and equal ones."""
     T, E, k = 400, 256, 8
