@@ -104,12 +104,16 @@ int fp8_moe_route_backward(const float* dweights, const void* logits, int64_t ld
   fp8moe::RouteGradParams p{dweights, dscores, logits, ids, dlogits, ldl, ldds, lddl, scale, T, E, top_k, scoring == FP8MOE_SIGMOID,
                             renormalize != 0, 0};
   with_type(dtype, [&](auto t) {
-    with_count<1, 2, 3, 4, 6, 8, 12, 16>((int)ceil_div(E, 64), [&](auto count) {
-      in_slices(ceil_div(T, 4), 256, [&](int first, dim3 grid) {
+    auto go = [&](auto count, auto lanes) {
+      constexpr int kLanes = decltype(lanes)::value;
+      in_slices(ceil_div(T, 256 / kLanes), 256, [&](int first, dim3 grid) {
         p.first_group = first;
-        hipLaunchKernelGGL((fp8moe::route_backward_kernel<decltype(t), decltype(count)::value>), grid, dim3(256), 0, stream, p);
+        hipLaunchKernelGGL((fp8moe::route_backward_kernel<decltype(t), decltype(count)::value, kLanes>), grid, dim3(256), 0, stream, p);
       });
-    });
+    };
+    // A lane holds a choice: four rows a wave where 16 lanes are enough for that and for a few experts.
+    if (E <= 64 && top_k <= 16) with_count<1, 2, 4>((int)ceil_div(E, 16), [&](auto count) { go(count, Int<16>{}); });
+    else with_count<1, 2, 3, 4, 6, 8, 12, 16>((int)ceil_div(E, 64), [&](auto count) { go(count, Int<64>{}); });
   });
   return launched();
 }

@@ -664,14 +664,24 @@ struct RouteGradParams {
   int first_group;
 };
 
-// One row a wave; expert lane + 64 j is a lane's j-th. The few gradients of the chosen scores
-// are spread to their experts through LDS.
-template <typename T, int VPL>
+// Over the lanes of a row, 16 or the wave.
+template <int LANES>
+__device__ __forceinline__ float row_sum_of(float v) {
+  if constexpr (LANES == 16) return row16_sum(v);
+  else return wave_sum(v);
+}
+
+// LANES lanes hold a row, 16 or 64; expert lane + LANES j is a lane's j-th. The few gradients of
+// the chosen scores are spread to their experts through LDS.
+template <typename T, int VPL, int LANES>
 __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradParams p) {
-  __shared__ float spread[4][64 * VPL];
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int64_t row = ((int64_t)p.first_group + blockIdx.x) * 4 + wave;
-  if (row >= p.T) return;
+  constexpr int kRows = 256 / LANES;
+  __shared__ float spread[kRows][LANES * VPL];
+  const int lane = threadIdx.x % LANES, at = LANES == 64 ? uniform(threadIdx.x / LANES) : threadIdx.x / LANES;
+  const int64_t first = ((int64_t)p.first_group + blockIdx.x) * kRows;
+  // rows past the last are done and not written, in a wave that has any before it
+  if (first + (threadIdx.x & ~63) / LANES >= p.T) return;
+  const int64_t row = LANES == 64 ? first + at : min(first + at, (int64_t)p.T - 1);
   const T* logits = static_cast<const T*>(p.logits) + row * p.ldl;
   float x[VPL], ds[VPL];
   int id = -1;
@@ -681,49 +691,54 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradPara
     g = p.dweights[row * p.top_k + lane] * p.scale;
   }
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) x[j] = logit(logits + min(lane + 64 * j, p.E - 1));
+  for (int j = 0; j < VPL; ++j) x[j] = logit(logits + min(lane + LANES * j, p.E - 1));
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    ds[j] = p.dscores ? p.dscores[row * p.ldds + min(lane + 64 * j, p.E - 1)] : 0.f;
-    spread[wave][lane + 64 * j] = 0.f;
+    ds[j] = p.dscores ? p.dscores[row * p.ldds + min(lane + LANES * j, p.E - 1)] : 0.f;
+    spread[at][lane + LANES * j] = 0.f;
   }
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) x[j] = lane + 64 * j < p.E ? x[j] : kNone;
+  for (int j = 0; j < VPL; ++j) x[j] = lane + LANES * j < p.E ? x[j] : kNone;
   if ((unsigned)id >= (unsigned)p.E) id = -1, g = 0.f;
   if (id >= 0) xi = logit(logits + id);
-  float top = 0.f, total = 0.f;
+  float top = 0.f, inverse = 0.f;
   if (!p.sigmoid) {
-    top = largest_number(x);
+    float most = kNone, total = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) most = fmaxf(most, x[j]);
+    const int bits = LANES == 16 ? row16_max(ordered(most)) : wave_max(ordered(most));
+    top = bits > kNoKey ? value_of(bits) : 0.f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       x[j] = exp_near(x[j] - top);  // 0 past the experts
       total += x[j];
     }
-    total = wave_sum(total);
+    total = row_sum_of<LANES>(total);
+    inverse = total == 0.f ? 0.f : 1.0f / total;
   }
-  const float inverse = total == 0.f ? 0.f : 1.0f / total;
   const float s = id < 0 ? 0.f : p.sigmoid ? sigmoid(xi) : exp_near(xi - top) * inverse;
   if (p.renormalize) {
-    const float over = 1.0f / (wave_sum(s) + kTiny);
-    g = (g - wave_sum(g * s) * over) * over;
+    const float over = 1.0f / (row_sum_of<LANES>(s) + kTiny);
+    g = (g - row_sum_of<LANES>(g * s) * over) * over;
   }
   own_lds();
-  if (id >= 0) atomicAdd(&spread[wave][id], g);
+  if (id >= 0) atomicAdd(&spread[at][id], g);
   own_lds();
   T* out = static_cast<T*>(p.dlogits) + row * p.lddl;
   float dot = 0.f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    ds[j] += spread[wave][lane + 64 * j];
+    ds[j] += spread[at][lane + LANES * j];
     if (!p.sigmoid) {
       x[j] *= inverse;
       dot += ds[j] * x[j];
     }
   }
-  if (!p.sigmoid) dot = wave_sum(dot);
+  if (!p.sigmoid) dot = row_sum_of<LANES>(dot);
+  if (first + at >= p.T) return;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    const int e = lane + 64 * j;
+    const int e = lane + LANES * j;
     float dx;
     if (p.sigmoid) dx = ds[j] == 0.f ? 0.f : ds[j] * sigmoid(x[j]) * sigmoid(-x[j]);  // 1 - s without a cancellation
     else dx = x[j] * (ds[j] - dot);

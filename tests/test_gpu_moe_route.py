@@ -192,7 +192,8 @@ def check_grad(dw, x, ids, scoring, renormalize, scale, ds, **kw):
 
 @pytest.mark.parametrize("dtype", [FP32, BF16])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 5, 5), (70, 60, 6), (5, 64, 64), (130, 256, 8), (4, 257, 9), (3, 1024, 64)])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 5, 5), (70, 60, 6), (5, 64, 64), (130, 256, 8), (4, 257, 9), (3, 1024, 64), (33, 16, 16),
+                                   (31, 32, 17), (18, 33, 4), (1000, 64, 8)])
 def test_gradient(cuda_device, dtype, scoring, T, E, k):
     x = logits_of(T, E, dtype, 1, cuda_device, pad=5)
     g = synth.make_generator(3, cuda_device)
