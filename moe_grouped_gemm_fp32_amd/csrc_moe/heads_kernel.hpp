@@ -1,9 +1,11 @@
 // Device code of the norm of queries and keys for each head with their rotation, and of its
 // gradients.
 //
-// D / 16 lanes hold a head: each 16 of its columns, both members of eight pairs where they
-// turn, so that neither the rotation nor the norm needs another lane's columns, only the sum
-// of squares (or the gradient's dot product) goes over the lanes.
+// D / 16 lanes hold a head, each two groups of eight of its columns that hold whole pairs: of
+// halves, both members of eight pairs; interleaved, four pairs in each group. So neither the
+// rotation nor the norm needs another lane's columns, only the sum of squares (or the gradient's
+// dot product) goes over the lanes. The first groups of neighbouring lanes are neighbours, and so
+// are the second ones: a load reads 64 bytes or more in a piece.
 #pragma once
 
 #include "common.hpp"
@@ -12,39 +14,61 @@ namespace fp8moe {
 
 using namespace fp8layer;
 
-// The two groups of eight columns that a lane holds of a head, and whether they turn.
+// The first columns of a lane's two groups, and whether they turn.
 struct Columns {
   int lo, hi;
-  bool turns;
+  bool lo_turns, hi_turns;
 };
+template <int D>
 __device__ __forceinline__ Columns columns_of(int i, int rot_dim, int interleaved) {
-  const bool turns = 16 * i < rot_dim;
-  const bool halves = turns && !interleaved;
-  return {halves ? 8 * i : 16 * i, halves ? (rot_dim >> 1) + 8 * i : 16 * i + 8, turns};
+  if (interleaved) return {8 * i, D / 2 + 8 * i, 8 * i < rot_dim, D / 2 + 8 * i < rot_dim};
+  if (16 * i < rot_dim) return {8 * i, (rot_dim >> 1) + 8 * i, true, true};
+  const int rest = rot_dim + 8 * (i - (rot_dim >> 4));
+  return {rest, rest + ((D - rot_dim) >> 1), false, false};
 }
 
-// Turns the pairs of a and b by angles of cosine c and sine s (`back`: by their negatives).
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8], int interleaved, bool back) {
-  const float sign = back ? -1.0f : 1.0f;
-  if (interleaved) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a1 = a[2 * j], a2 = a[2 * j + 1], b1 = b[2 * j], b2 = b[2 * j + 1];
-      const float sa = sign * s[j], sb = sign * s[4 + j];
-      a[2 * j] = a1 * c[j] - a2 * sa;
-      a[2 * j + 1] = a2 * c[j] + a1 * sa;
-      b[2 * j] = b1 * c[4 + j] - b2 * sb;
-      b[2 * j + 1] = b2 * c[4 + j] + b1 * sb;
+// Cosines and sines of a lane's pairs; interleaved, four of each group.
+struct Angles {
+  float c[8], s[8];
+  __device__ __forceinline__ void load(const float* row, const Columns& at, int rot_dim, int interleaved) {
+    const float* sines = row + (rot_dim >> 1);
+    if (!interleaved) {
+      if (!at.lo_turns) return;
+      load8(row + at.lo, c);
+      load8(sines + at.lo, s);
+      return;
     }
-  } else {
+    auto four = [](const float* from, float* to) {
+      const float4 v = *reinterpret_cast<const float4*>(from);
+      to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+    };
+    if (at.lo_turns) four(row + at.lo / 2, c), four(sines + at.lo / 2, s);
+    if (at.hi_turns) four(row + at.hi / 2, c + 4), four(sines + at.hi / 2, s + 4);
+  }
+  // Turns the pairs of a and b (BACK: by the angles' negatives).
+  template <bool BACK>
+  __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const Columns& at, int interleaved) const {
+    auto pair = [](float& x1, float& x2, float cosine, float sine) {
+      const float y = BACK ? -sine : sine, x = x1;
+      x1 = x * cosine - x2 * y;
+      x2 = x2 * cosine + x * y;
+    };
+    if (!interleaved) {
+      if (!at.lo_turns) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x1 = a[j], x2 = b[j], sj = sign * s[j];
-      a[j] = x1 * c[j] - x2 * sj;
-      b[j] = x2 * c[j] + x1 * sj;
+      for (int j = 0; j < 8; ++j) pair(a[j], b[j], c[j], s[j]);
+      return;
+    }
+    if (at.lo_turns) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pair(a[2 * j], a[2 * j + 1], c[j], s[j]);
+    }
+    if (at.hi_turns) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pair(b[2 * j], b[2 * j + 1], c[4 + j], s[4 + j]);
     }
   }
-}
+};
 
 // Sum over LANES (4, 8 or 16) neighbouring lanes, in every one of them.
 template <int LANES>
@@ -83,17 +107,16 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadsParams p) {
   int h = (int)item - token * heads;
   const bool key = h >= p.Hq;
   if (key) h -= p.Hq;
-  const Columns at = columns_of(i, p.rot_dim, p.interleaved);
+  const Columns at = columns_of<D>(i, p.rot_dim, p.interleaved);
   const T* x = key ? static_cast<const T*>(p.k) + token * p.ldk + h * D : static_cast<const T*>(p.q) + token * p.ldq + h * D;
   T* y = key ? static_cast<T*>(p.k_out) + token * p.ldko + h * D : static_cast<T*>(p.q_out) + token * p.ldqo + h * D;
-  float a[8], b[8], wa[8], wb[8], c[8], s[8];
+  float a[8], b[8], wa[8], wb[8];
+  Angles angles;
   load8<STREAM>(x + at.lo, a);
   load8<STREAM>(x + at.hi, b);
-  if (at.turns) {
+  if (at.lo_turns) {  // where the second group turns, the first does
     const int position = min(max(p.positions ? p.positions[token] : token, 0), p.max_pos - 1);
-    const float* row = p.cos_sin + position * p.ld_cs + 8 * i;
-    load8(row, c);
-    load8(row + (p.rot_dim >> 1), s);
+    angles.load(p.cos_sin + position * p.ld_cs, at, p.rot_dim, p.interleaved);
   }
   const void* w = key ? p.kw : p.qw;
   head_weight(w, p.w_fp32, at.lo, wa);
@@ -104,7 +127,7 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadsParams p) {
   const float rstd = 1.0f / sqrtf(head_sum<kLanes>(ss) * (1.0f / D) + p.eps);
 #pragma unroll
   for (int j = 0; j < 8; ++j) a[j] *= rstd * wa[j], b[j] *= rstd * wb[j];
-  if (at.turns) turn(a, b, c, s, p.interleaved, false);
+  angles.turn<false>(a, b, at, p.interleaved);
   store8(y + at.lo, a);
   store8(y + at.hi, b);
 }
@@ -132,7 +155,7 @@ __global__ void __launch_bounds__(256) heads_backward_kernel(const HeadsGradPara
   const int heads = key ? p.Hk : p.Hq;
   const int group = key ? blockIdx.x - p.q_groups : blockIdx.x, groups = key ? gridDim.x - p.q_groups : p.q_groups;
   const int i = threadIdx.x % kLanes;
-  const Columns at = columns_of(i, p.rot_dim, p.interleaved);
+  const Columns at = columns_of<D>(i, p.rot_dim, p.interleaved);
   const T* dy = static_cast<const T*>(key ? p.dk : p.dq);
   const T* x = static_cast<const T*>(key ? p.k : p.q);
   T* dx = static_cast<T*>(key ? p.dk_out : p.dq_out);
@@ -150,13 +173,11 @@ __global__ void __launch_bounds__(256) heads_backward_kernel(const HeadsGradPara
     load8(x + token * ldx + h * D + at.lo, xa);
     load8(x + token * ldx + h * D + at.hi, xb);
     T* to = dx + token * lddx + h * D;
-    if (at.turns) {
-      float c[8], s[8];
+    if (at.lo_turns) {
+      Angles angles;
       const int position = p.positions ? p.positions[token] : token;
-      const float* row = p.cos_sin + min(max(position, 0), p.max_pos - 1) * p.ld_cs + 8 * i;
-      load8(row, c);
-      load8(row + (p.rot_dim >> 1), s);
-      turn(ga, gb, c, s, p.interleaved, true);
+      angles.load(p.cos_sin + min(max(position, 0), p.max_pos - 1) * p.ld_cs, at, p.rot_dim, p.interleaved);
+      angles.turn<true>(ga, gb, at, p.interleaved);
     }
     float ss = 0.f;
 #pragma unroll
