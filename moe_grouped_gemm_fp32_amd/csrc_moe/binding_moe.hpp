@@ -123,6 +123,13 @@ MoeRows layout_of(PyObject* o) {
   return r;
 }
 
+// Stride of the rows of a 3-D tensor, which has to be one for all; `alone` for a single row.
+int64_t one_stride(const Tensor& t, const char* name, int64_t alone) {
+  if (t.size(1) <= 1) return t.size(0) > 1 ? t.stride(0) : alone;
+  TORCH_CHECK_VALUE(t.size(0) <= 1 || t.stride(0) == t.size(1) * t.stride(1), name, "'s rows must lie at one stride");
+  return t.stride(1);
+}
+
 // What a dispatch and a gather have in common: the tokens' rows, and the expanded ones.
 struct MoeCopy {
   Tensor Qx, sax;
@@ -149,14 +156,13 @@ MoeCopy copy_of(const Launch& launch, const Tensor& Q, PyObject* sa_o, PyObject*
     c.Qx = launch.output(Qx_o, "Qx", {E, max_m, K}, at::kByte);
     c.sax = launch.output(sax_o, "sax", {E, blocks, library.scale_ld(max_m)}, at::kFloat);
     TORCH_CHECK_VALUE(c.Qx.dim() == 3 && c.Qx.size(0) == E && c.Qx.size(1) == max_m && c.Qx.size(2) == K && codes_type(c.Qx) &&
-                          c.Qx.device() == dev && c.Qx.stride(2) == 1 && (E <= 1 || c.Qx.stride(0) == max_m * c.Qx.stride(1)),
-                      "Qx must be uint8 or float8_e4m3fn [", E, ", ", max_m, ", ", K, "] on ", dev, ", its rows at one stride");
-    c.ldqx = c.Qx.stride(1);
+                          c.Qx.device() == dev && c.Qx.stride(2) == 1,
+                      "Qx must be uint8 or float8_e4m3fn [", E, ", ", max_m, ", ", K, "] on ", dev, " with a unit inner stride");
+    c.ldqx = one_stride(c.Qx, "Qx", K);
     TORCH_CHECK_VALUE(c.sax.dim() == 3 && c.sax.size(0) == E && c.sax.size(1) == blocks && c.sax.size(2) >= max_m &&
-                          c.sax.scalar_type() == at::kFloat && c.sax.device() == dev && (c.sax.size(2) <= 1 || c.sax.stride(2) == 1) &&
-                          (E <= 1 || c.sax.stride(0) == blocks * c.sax.stride(1)),
-                      "sax must be float32 [", E, ", ", blocks, ", >= ", max_m, "] on ", dev, ", its rows at one stride");
-    c.ld_sax = c.sax.stride(1);
+                          c.sax.scalar_type() == at::kFloat && c.sax.device() == dev && (c.sax.size(2) <= 1 || c.sax.stride(2) == 1),
+                      "sax must be float32 [", E, ", ", blocks, ", >= ", max_m, "] on ", dev, " with a unit inner stride");
+    c.ld_sax = one_stride(c.sax, "sax", library.scale_ld(c.sax.size(2)));
   } else {
     c.Qx = launch.output(Qx_o, "Qx", {rows, K}, at::kByte);
     c.sax = launch.output(sax_o, "sax", {blocks, library.scale_ld(rows)}, at::kFloat);
@@ -258,8 +264,7 @@ std::pair<int64_t, int64_t> expert_rows(const Tensor& t, const char* name, int64
   TORCH_CHECK_VALUE((t.dim() == 2 || t.dim() == 3) && t.size(-1) == N && t.scalar_type() == type && t.device() == dev && t.stride(-1) == 1,
                     name, " must be ", type, " [rows, ", N, "] or [E, max_m, ", N, "] on ", dev, " with a unit inner stride");
   if (t.dim() == 2) return {t.size(0), row_stride(t)};
-  TORCH_CHECK_VALUE(t.size(0) <= 1 || t.stride(0) == t.size(1) * t.stride(1), name, "'s rows must lie at one stride");
-  return {t.size(0) * t.size(1), t.size(0) * t.size(1) > 1 ? t.stride(1) : N};
+  return {t.size(0) * t.size(1), one_stride(t, name, N)};
 }
 const Tensor& experts_tensor(PyObject* o, const char* name) {
   const Tensor& t = tensor(o, name);

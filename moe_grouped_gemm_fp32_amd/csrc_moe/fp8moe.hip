@@ -343,11 +343,13 @@ int fp8_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int
                      const float* cos_sin, int64_t ld_cs, int max_pos, int rot_dim, int interleaved, const int32_t* positions,
                      float eps, void* q_out, int64_t ldqo, void* k_out, int64_t ldko, int T, int Hq, int Hk, int D,
                      hipStream_t stream) {
+  if (Hq == 0) q = q_out = nullptr;  // no heads have no address
+  if (Hk == 0) k = k_out = nullptr;
+  if (T != 0 && ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) || (q && !qw) || (k && !kw) ||
+                 (rot_dim > 0 && !cos_sin)))
+    return FP8GEMM_ERR_NULL;
   if (!q) Hq = 0;
   if (!k) Hk = 0;
-  if (T != 0 && ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) || (q && !qw) || (k && !kw) ||
-                 (!q && !k) || (rot_dim > 0 && !cos_sin)))
-    return FP8GEMM_ERR_NULL;
   if (!heads_shape(T, Hq, Hk, D, max_pos, rot_dim) || !(eps >= 0.f)) return FP8GEMM_ERR_SHAPE;
   if (!norm_dtype(dtype) || !norm_dtype(w_dtype)) return FP8GEMM_ERR_LAYOUT;
   if (T == 0 || Hq + Hk == 0) return FP8GEMM_OK;
@@ -387,15 +389,15 @@ int fp8_qk_norm_rope_backward(const void* dq, int64_t lddq, const void* dk, int6
   if (!queries) Hq = 0;
   if (!keys) Hk = 0;
   if (!queries && !keys) return FP8GEMM_ERR_NULL;
-  if (T != 0 && ((queries && (!dq || !q || !qw || !dq_out)) || (keys && (!dk || !k || !kw || !dk_out)) || (rot_dim > 0 && !cos_sin)))
+  if (T != 0 && ((Hq != 0 && (!dq || !q || !qw || !dq_out)) || (Hk != 0 && (!dk || !k || !kw || !dk_out)) || (rot_dim > 0 && !cos_sin)))
     return FP8GEMM_ERR_NULL;
   if (!heads_shape(T, Hq, Hk, D, max_pos, rot_dim) || !(eps >= 0.f)) return FP8GEMM_ERR_SHAPE;
   if (!norm_dtype(dtype) || !norm_dtype(w_dtype) || !aligned(dqw, 4) || !aligned(dkw, 4) || !aligned(workspace, 16))
     return FP8GEMM_ERR_LAYOUT;
   if (T != 0 &&
-      ((queries && (!head_rows(dq, lddq, (int64_t)Hq * D, dtype) || !head_rows(q, ldq, (int64_t)Hq * D, dtype) ||
+      ((Hq != 0 && (!head_rows(dq, lddq, (int64_t)Hq * D, dtype) || !head_rows(q, ldq, (int64_t)Hq * D, dtype) ||
                     !head_rows(dq_out, lddqo, (int64_t)Hq * D, dtype) || !aligned(qw, 16))) ||
-       (keys && (!head_rows(dk, lddk, (int64_t)Hk * D, dtype) || !head_rows(k, ldk, (int64_t)Hk * D, dtype) ||
+       (Hk != 0 && (!head_rows(dk, lddk, (int64_t)Hk * D, dtype) || !head_rows(k, ldk, (int64_t)Hk * D, dtype) ||
                  !head_rows(dk_out, lddko, (int64_t)Hk * D, dtype) || !aligned(kw, 16))) ||
        (rot_dim > 0 && (ld_cs < rot_dim || ld_cs % 4 || !aligned(cos_sin, 16))) || !aligned(positions, 4)))
     return FP8GEMM_ERR_LAYOUT;

@@ -177,3 +177,22 @@ def test_refusals(cuda_device):
     for bad in (dict(Q=Q[:5]), dict(weights=ids), dict(Qx=Qx[:3]), dict(layout=masked, Qx=Qx)):
         with pytest.raises(ValueError):
             fg.moe_gather(**{"Q": Q, "sa": sa, "layout": at, **bad})
+
+
+def test_masked_rows_of_one_stride(cuda_device):
+    """One row an expert of a larger buffer, and one K block, lie at one stride as well."""
+    T, E, K = 5, 4, 128
+    Q, sa = tokens_of(T, K, 9, cuda_device)
+    ids = torch.tensor([[2], [0], [2], [3], [0]], dtype=I32, device=cuda_device)
+    base, scales = torch.zeros(E, 3, K, dtype=U8, device=cuda_device), torch.zeros(E, 2, 8, device=cuda_device)
+    _, _, at = fg.moe_dispatch(Q, sa, ids, E, max_m=1, Qx=base[:, :1], sax=scales[:, :1])
+    torch.cuda.synchronize()
+    assert at.positions.flatten().tolist() == [2, 0, -1, 3, -1] and at.counts.tolist() == [1, 0, 1, 1]
+    for e, t in ((2, 0), (0, 1), (3, 3)):
+        assert torch.equal(base[e, 0], Q[t]) and float(scales[e, 0, 0]) == float(sa[0, t])
+    assert int(base[:, 1:].max()) == 0 and int((scales != 0).sum()) == 3
+    y = torch.randn(E, 3, 16, device=cuda_device)[:, 1:2]
+    out = fg.moe_combine(y, at.positions)
+    assert torch.equal(out, torch.where(at.positions >= 0, y[:, 0][at.positions[:, 0].clamp(min=0).long()], 0.0))
+    with pytest.raises(ValueError):
+        fg.moe_combine(torch.randn(E, 3, 16, device=cuda_device)[:, :2], at.positions)

@@ -86,6 +86,10 @@ def test_zero_rows_extremes_and_no_tokens(cuda_device):
     assert q.shape == k.shape == (0, 2, 64)
     none = fg.qk_norm_rope(x, x[:, :0], *ws, table)
     assert none[1].shape == (4, 0, 64)
+    grad = fg.qk_norm_rope_backward(x, x[:, :0], x, x[:, :0], *ws, table)
+    assert grad[1].shape == (4, 0, 64) and bool((grad[3] == 0).all())
+    alone = fg.qk_norm_rope_backward(x, None, x, None, ws[0], None, table)
+    assert torch.equal(grad[0], alone[0]) and torch.equal(grad[2], alone[2])
 
 
 def test_the_append_of_what_comes_out(cuda_device):

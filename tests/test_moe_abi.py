@@ -92,7 +92,7 @@ REFUSED = [
     ("fp8_moe_combine_backward", COMBINE_GRAD, LAYOUT,
      [dict(dtype=2), dict(dO=A + 8), dict(lddo=250), dict(Y=A + 8), dict(ldy=128), dict(dY=A + 8), dict(lddy=252), dict(positions=A + 2),
       dict(weights=A + 2), dict(dweights=A + 2)]),
-    ("fp8_qk_norm_rope", HEADS, NULL, [*each("q_out", "k_out", "q", "k", "qw", "kw", "cos_sin"), dict(q=None, k=None, q_out=None, k_out=None)]),
+    ("fp8_qk_norm_rope", HEADS, NULL, each("q_out", "k_out", "q", "k", "qw", "kw", "cos_sin")),
     ("fp8_qk_norm_rope", HEADS, SHAPE,
      [dict(T=-1), dict(D=96), dict(D=32), dict(rot_dim=8), dict(rot_dim=144), dict(rot_dim=-16), dict(max_pos=0), dict(eps=-1.0),
       dict(eps=float("nan")), dict(Hq=-1), dict(T=1 << 30), dict(Hq=1 << 24, T=1)]),
@@ -140,6 +140,8 @@ def test_calls_without_tokens_look_at_no_tokens():
     assert call("fp8_moe_combine", COMBINE, T=0, Y=None, positions=None, out=None) == 0
     assert call("fp8_moe_combine_backward", COMBINE_GRAD, T=0, dO=None, positions=None) == 0
     assert call("fp8_qk_norm_rope", HEADS, T=0, cos_sin=None) == 0
+    assert call("fp8_qk_norm_rope", HEADS, q=None, k=None, q_out=None, k_out=None) == 0  # nor calls without heads at heads
+    assert call("fp8_qk_norm_rope", HEADS, Hq=0, q=None, q_out=A, Hk=0, k_out=None) == 0
 
 
 def test_sizes():
