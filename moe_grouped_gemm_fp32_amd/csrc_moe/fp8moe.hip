@@ -59,20 +59,26 @@ int fp8_moe_route(const void* logits, int64_t ldl, int dtype, const float* bias,
   const int log_lanes = 6 - log_groups, size = E / groups, each = (int)ceil_div(size, 1 << log_lanes);
   fp8moe::RouteParams p{logits, bias,       ids,        weights,    scores,      ldl,         lds,  scale,     T,    E,
                         top_k,  groups,     top_groups, group_best, scoring == FP8MOE_SIGMOID, renormalize != 0, size, log_lanes, each,
-                        0,      0};
-  // Experts of a lane where 16 lanes hold a row, and a group some of them. A wave for four rows,
-  // and for one, sigmoid with a bias: 16 experts, 1 token 2.3 and 2.6 us, 16384 5.2 and 7.4; 32, 1
-  // token 2.9 and 2.7, 65536 12.8 and 23.6, in 4 groups 4096 6.6 and 4.7 (a row that is done again
-  // waits for its wave), 16384 7.6 and 10.0; 64 experts, 16384 12.0 and 8.8.
+                        0,      0,          0};
+  // Experts of a lane where 16 lanes hold a row, and a group some of them. A wave for four rows
+  // shares most instructions among them, and needs many rows to fill the GPU; there has to be a
+  // lane for each choice and one more. For four rows and for one, sigmoid with a bias, us: 16
+  // experts, 1 token 2.3 and 2.6, 16384 3.4 and 7.4; 32, 1 token 2.9 and 2.7, 16384 5.8 and 8.2, in
+  // 4 groups 4096 6.6 and 4.7; 64, 4096 4.9 and 4.5, 8192 5.5 and 5.4, 16384 6.4 and 8.6, 65536 13.4
+  // and 24.3; 256, 8192 7.7 and 7.5, 16384 10.6 and 11.4, in 8 groups 12.7 and 14.2, 65536 31.8 and
+  // 43.1. Softmax of 160 in 8 groups gains last: 16384 17.0 and 16.6, 65536 38.4 and 51.5.
   const int of_16 = log_groups <= 4 ? (int)ceil_div(size, 1 << (log_lanes - 2)) : 0;
-  const bool four_rows = of_16 == 1 || (of_16 == 2 && T > 32 * cus);
+  const bool four_rows = of_16 == 1 || (of_16 == 2 && T > 32 * cus) ||
+                         (of_16 > 2 && of_16 <= 16 && top_k <= 15 && T >= (of_16 <= 4 ? 32 : 64) * cus);
   with_type(dtype, [&](auto t) {
     if (four_rows) {
-      p.even = size == 1 << log_lanes && groups == 1 << log_groups;
-      with_count<1, 2>(of_16, [&](auto count) {
+      with_count<1, 2, 4, 8, 16>(of_16, [&](auto count) {
+        constexpr int kCount = decltype(count)::value;
+        p.even = size == (kCount + 3) / 4 << log_lanes && groups == 1 << log_groups;
+        p.even_16 = size == kCount << (log_lanes - 2) && groups == 1 << log_groups;
         in_slices(ceil_div(T, 16), 256, [&](int first, dim3 grid) {
           p.first_group = first;
-          hipLaunchKernelGGL((fp8moe::route_rows_kernel<decltype(t), decltype(count)::value>), grid, dim3(256), 0, stream, p);
+          hipLaunchKernelGGL((fp8moe::route_rows_kernel<decltype(t), kCount>), grid, dim3(256), 0, stream, p);
         });
       });
       return;

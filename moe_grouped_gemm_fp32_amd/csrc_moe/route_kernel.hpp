@@ -61,6 +61,7 @@ struct RouteParams {
   int log_lanes;  // lanes of a group: 64 over the power of two that is not below `groups`
   int each;       // experts of a lane, at most VPL
   int even;       // whether every lane has VPL
+  int even_16;    // and where 16 lanes hold a row
   int first_group;  // the launch's first workgroup of the call's
 };
 
@@ -179,13 +180,12 @@ struct Exactly {
   bool sigmoid, by_score;
   double top, sum;  // of the softmax
   template <int VPL>
-  __device__ __forceinline__ Exactly(bool sigmoid, bool by_score, float top, const float (&x)[VPL])
+  __device__ __forceinline__ Exactly(bool sigmoid, bool by_score, float top, const float (&x)[VPL], int lanes = 64)
       : sigmoid(sigmoid), by_score(by_score), top(top), sum(0.0) {
     if (sigmoid || !by_score) return;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) sum += exp((double)x[j] - this->top);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    for (int off = lanes / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
   }
   __device__ __forceinline__ double key(float x, float bias) const {
     if (x == kNone) return (double)kNone;
@@ -218,6 +218,22 @@ __device__ __forceinline__ int choose_slowly(const RouteParams& p, double (&key)
       if (lane == from && j == at) key[j] = none;
   }
   return id;
+}
+
+// Whether any of the lane's keys that FP32 cannot tell from the first one that is not chosen,
+// `edge`, is another than that, by its logit and bias. Equal keys at the edge of the choice go by
+// their numbers if it holds for no lane: what is further off was decided, whatever its place.
+template <int VPL, typename T>
+__device__ __forceinline__ bool others_near(const RouteParams& p, const int (&key)[VPL], const float (&x)[VPL], int base, int2 edge, float slack,
+                                            const T* logits) {
+  const float v = value_of(edge.x), off = slack + 0x1p-22f * fabsf(v), x0 = logit(logits + edge.y), b0 = p.bias ? p.bias[edge.y] : 0.f;
+  bool other = false;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const float k = value_of(key[j]);
+    if (key[j] > kNoKey && !(fabsf(k - v) > off)) other = other || !(x[j] == x0 && (!p.bias || p.bias[base + j] == b0));
+  }
+  return other;
 }
 
 constexpr int kEnough = 8;  // candidates beyond those needed that are ranked rather than searched on
@@ -320,6 +336,11 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const int (&key)[VP
     if (__ballot(open) != 0) {
       const int last = from_before(e);
       if (open) open = !(logit(logits + last) == logit(logits + e) && (!p.bias || p.bias[last] == p.bias[e]));
+      if (need > p.top_k) {  // what follows equal keys at the edge could be larger than they are
+        const int2 edge = make_int2(lane_value(sorted, p.top_k), lane_value(e, p.top_k));
+        if (!(value_of(lane_value(sorted, p.top_k - 1)) - value_of(edge.x) > slack + 0x1p-22f * fabsf(value_of(edge.x))))
+          open = open || others_near(p, key, x, base, edge, slack, logits);
+      }
       if (__ballot(open) != 0) {
         const float t = value_of(low);
         low = ordered(t - (slack + 0x1p-22f * fabsf(t)));  // what does not reach this is less than those that are needed
@@ -344,6 +365,20 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const int (&key)[VP
   return true;
 }
 
+__device__ __forceinline__ int row16_max(int v) { return max_with<kMirror>(max_with<kHalfMirror>(max_with<kSwap2>(max_with<kSwap1>(v)))); }
+template <typename V>
+__device__ __forceinline__ V row16_sum(V v) {
+  v += dpp<kSwap1>(v, v);
+  v += dpp<kSwap2>(v, v);
+  v += dpp<kHalfMirror>(v, v);
+  return v + dpp<kMirror>(v, v);
+}
+// The sum of the chosen scores, lane i's the i-th, in the same order whichever kernel has them.
+__device__ __forceinline__ float sum_of_chosen(float s) {
+  const float row = row16_sum(s);
+  return lane_value(row, 0) + lane_value(row, 16) + lane_value(row, 32) + lane_value(row, 48);
+}
+
 // How far two keys' errors come to, twice over, for a row's largest score, whose bits have the
 // order of what is not negative. Sigmoids: s |x| (1 - s) grows up to s = 1/4 and then stays below
 // 0.28, and |x| < 0.7 (e + 1) for a largest score of 2^-e. Softmax: three roundings and the
@@ -366,18 +401,22 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
   const int base = group * p.size + begin;
   const bool limited = p.top_groups < p.groups;
   const bool by_score = p.bias || (p.group_best == 2 && limited);  // else the logits' order is the scores'
-  float x[VPL], bias[VPL];
+  float x[VPL], bias[VPL] = {};
   int key[VPL];
   if (p.even) {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) x[j] = logit(logits + base + j);
+    if (p.bias) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) bias[j] = p.bias ? p.bias[base + j] : 0.f;
+      for (int j = 0; j < VPL; ++j) bias[j] = p.bias[base + j];
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) x[j] = logit(logits + min(base + j, p.E - 1));
+    if (p.bias) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) bias[j] = p.bias ? p.bias[min(base + j, p.E - 1)] : 0.f;
+      for (int j = 0; j < VPL; ++j) bias[j] = p.bias[min(base + j, p.E - 1)];
+    }
 #pragma unroll
     for (int j = 0; j < VPL; ++j) x[j] = j < count ? x[j] : kNone;
   }
@@ -457,11 +496,11 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
     const float v = logit(logits + id);
     w = p.sigmoid ? sigmoid(v) : exp_near(v - top) * inverse;
   }
-  if (p.renormalize) w = w / (wave_sum(w) + kTiny);
+  const float over = p.renormalize ? p.scale / (sum_of_chosen(w) + kTiny) : p.scale;
   if (lane < p.top_k) {
     const int64_t out = row * p.top_k + lane;
     p.ids[out] = id;
-    p.weights[out] = w * p.scale;
+    p.weights[out] = w * over;
   }
 }
 
@@ -479,15 +518,6 @@ __device__ __forceinline__ void each_turn(const int (&key)[VPL], F f) {
   f(other, std::integral_constant<int, D>{});
   if constexpr (D < 15) each_turn<D + 1>(key, f);
 }
-__device__ __forceinline__ int row16_max(int v) { return max_with<kMirror>(max_with<kHalfMirror>(max_with<kSwap2>(max_with<kSwap1>(v)))); }
-template <typename V>
-__device__ __forceinline__ V row16_sum(V v) {
-  v += dpp<kSwap1>(v, v);
-  v += dpp<kSwap2>(v, v);
-  v += dpp<kHalfMirror>(v, v);
-  return v + dpp<kMirror>(v, v);
-}
-
 template <typename T, int VPL>
 __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
   __shared__ int2 places[4][64];
@@ -496,13 +526,14 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
   if (row < p.T) route_row<T, VPL>(p, row, threadIdx.x & 63, places[wave]);
 }
 
-// Four rows a wave, of few experts: 16 lanes hold a row, VPL experts each, and every key counts
-// the larger ones of its row as they come by. A row that FP32 leaves open is done again by
-// route_row(). 16384 rows of 16 experts (sigmoid, bias) 3.4 us, of 32 5.8.
+// Four rows a wave: 16 lanes hold a row, VPL experts each. Up to two each, every key counts the
+// larger ones of its row as they come by; more are searched for a threshold that 16 at most
+// reach, one a lane, which then count each other. What FP32 leaves open, or equal keys make too
+// many, is done again by route_row(). 16384 rows of 16 experts (sigmoid, bias) 3.4 us, of 32 5.8.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
   __shared__ int2 places[4][64];
-  __shared__ int2 order[4][4][16 * VPL];
+  __shared__ int2 order[4][4][VPL <= 2 ? 16 * VPL : 32];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), sub16 = lane & 15, mine = lane >> 4;
   const int64_t first_row = (((int64_t)p.first_group + blockIdx.x) * 4 + wave) * 4;
   if (first_row >= p.T) return;
@@ -517,12 +548,20 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
   const bool by_score = p.bias || (p.group_best == 2 && limited);
   float x[VPL], s[VPL];
   int key[VPL];
+  if (p.even_16) {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) x[j] = logit(logits + min(base + j, p.E - 1));
+    for (int j = 0; j < VPL; ++j) x[j] = logit(logits + base + j);
+  } else {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) x[j] = j < count ? x[j] : kNone;
+    for (int j = 0; j < VPL; ++j) x[j] = logit(logits + min(base + j, p.E - 1));
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) x[j] = j < count ? x[j] : kNone;
+  }
   float top = 0.f, inverse = 0.f, slack = 0.f;
-  if (p.sigmoid) {
+  if (p.sigmoid && VPL > 2 && !p.scores) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) s[j] = sigmoid_for_order(x[j]);
+  } else if (p.sigmoid) {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) s[j] = sigmoid(x[j]);
   } else {
@@ -549,9 +588,20 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
   if (by_score) {
     float largest = 0.f;
 #pragma unroll
+    for (int j = 0; j < VPL; ++j) largest = fmaxf(largest, s[j]);
+    float bias[VPL] = {};
+    if (p.bias) {
+      if (p.even_16) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) bias[j] = p.bias[base + j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) bias[j] = p.bias[min(base + j, p.E - 1)];
+      }
+    }
+#pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      largest = fmaxf(largest, s[j]);
-      const float k = p.bias ? s[j] + p.bias[min(base + j, p.E - 1)] : s[j];
+      const float k = s[j] + bias[j];
       key[j] = x[j] == kNone ? kNoKey : ordered(k == k ? k : kNanKey);
     }
     slack = slack_of(row16_max(__float_as_int(largest)), p.sigmoid);
@@ -592,66 +642,188 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) key[j] = is && rank < p.top_groups ? key[j] : kNoKey;
   }
-  int live = 0, rank[VPL], sum = 0;
+  int live = 0;
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) live += key[j] > kNoKey, rank[j] = 0;
+  for (int j = 0; j < VPL; ++j) live += key[j] > kNoKey;
   live = row16_sum(live);
-  each_turn(key, [&](const int (&other)[VPL], auto) {
+  uint64_t left;
+  if constexpr (VPL <= 2) {
+    int rank[VPL] = {}, sum = 0;
+    each_turn(key, [&](const int (&other)[VPL], auto) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
+      for (int i = 0; i < VPL; ++i)
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) rank[j] += other[i] > key[j];
-  });
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) sum += key[j] > kNoKey ? rank[j] : 0;
-  if (__ballot(row16_sum(sum) != live * (live - 1) / 2) != 0) {  // equal keys go by their numbers
-    int number[1] = {base};
-    each_turn(number, [&](const int (&other)[1], auto d) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int theirs = turned<decltype(d)::value>(key[i]);
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) rank[j] += theirs == key[j] && other[0] + i < base + j;
-      }
+        for (int j = 0; j < VPL; ++j) rank[j] += other[i] > key[j];
     });
-  }
-  if (by_score) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (key[j] > kNoKey) order[wave][mine][rank[j]] = make_int2(key[j], base + j);
-    own_lds();
+    for (int j = 0; j < VPL; ++j) sum += key[j] > kNoKey ? rank[j] : 0;
+    if (__ballot(row16_sum(sum) != live * (live - 1) / 2) != 0) {  // equal keys go by their numbers
+      int number[1] = {base};
+      each_turn(number, [&](const int (&other)[1], auto d) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      if (key[j] == kNoKey || rank[j] >= p.top_k || rank[j] + 1 >= live) continue;
-      const int2 next = order[wave][mine][rank[j] + 1];
-      const float v = value_of(key[j]), after = value_of(next.x);
-      if (!(v - after > slack + 0x1p-22f * fabsf(after)))
+        for (int i = 0; i < VPL; ++i) {
+          const int theirs = turned<decltype(d)::value>(key[i]);
+#pragma unroll
+          for (int j = 0; j < VPL; ++j) rank[j] += theirs == key[j] && other[0] + i < base + j;
+        }
+      });
+    }
+    if (by_score) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (key[j] > kNoKey) order[wave][mine][rank[j]] = make_int2(key[j], base + j);
+      own_lds();
+      bool edge = false;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        if (key[j] == kNoKey || rank[j] >= p.top_k || rank[j] + 1 >= live) continue;
+        const int2 next = order[wave][mine][rank[j] + 1];
+        const float v = value_of(key[j]), after = value_of(next.x);
+        if (v - after > slack + 0x1p-22f * fabsf(after)) continue;
         open = open || !(x[j] == logit(logits + next.y) && (!p.bias || p.bias[base + j] == p.bias[next.y]));
+        edge = edge || rank[j] + 1 == p.top_k;
+      }
+      const bool at_edge = (__ballot(edge) >> (lane & 48) & 0xFFFF) != 0;
+      if (at_edge) open = open || others_near(p, key, x, base, order[wave][mine][p.top_k], slack, logits);
     }
-  }
-  uint64_t left = __ballot(open && there);
-  const bool again = (left >> (lane & 48) & 0xFFFF) != 0;
-  float w[VPL], total = 0.f;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    w[j] = key[j] > kNoKey && rank[j] < p.top_k ? s[j] : 0.f;
-    total += w[j];
-  }
-  const float over = p.renormalize ? p.scale / (row16_sum(total) + kTiny) : p.scale;
-  if (there && !again) {
-    const int64_t out = row * p.top_k;
+    left = __ballot(open && there);
+    const bool again = (left >> (lane & 48) & 0xFFFF) != 0;
+    float w[VPL], total = 0.f;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      if (key[j] == kNoKey || rank[j] >= p.top_k) continue;
-      p.ids[out + rank[j]] = base + j;
-      p.weights[out + rank[j]] = w[j] * over;
+      w[j] = key[j] > kNoKey && rank[j] < p.top_k ? s[j] : 0.f;
+      total += w[j];
     }
-    for (int i = live + sub16; i < p.top_k; i += 16) p.ids[out + i] = -1, p.weights[out + i] = 0.f;
+    const float over = p.renormalize ? p.scale / (row16_sum(total) + kTiny) : p.scale;
+    if (there && !again) {
+      const int64_t out = row * p.top_k;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        if (key[j] == kNoKey || rank[j] >= p.top_k) continue;
+        p.ids[out + rank[j]] = base + j;
+        p.weights[out + rank[j]] = w[j] * over;
+      }
+      for (int i = live + sub16; i < p.top_k; i += 16) p.ids[out + i] = -1, p.weights[out + i] = 0.f;
+    }
+  } else {
+    const int need = min(p.top_k + (int)by_score, live);  // at most 16
+    // Of the lanes' largest keys, or their two largest, there are enough that reach the least of
+    // them; `low` is reached by enough, `high` by too few.
+    int best = key[0], second = kNoKey;
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) {
+      second = max(second, min(best, key[j]));
+      best = max(best, key[j]);
+    }
+    int low = kNoKey + 1, high = row16_max(best) + 1;
+    if (row16_sum((int)(best > kNoKey)) >= need) low = ~row16_max(best > kNoKey ? ~best : kLowest);
+    else if (2 * row16_sum((int)(second > kNoKey)) >= need) low = ~row16_max(second > kNoKey ? ~second : kLowest);
+    auto reach = [&](int t) {
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) n += key[j] >= t;
+      return row16_sum(n);
+    };
+    int found = reach(low);
+    while (__ballot(found > 16 && (unsigned)high - (unsigned)low > 1) != 0) {
+      const int mid = low + (int)(((unsigned)high - (unsigned)low) >> 1);
+      const int n = reach(mid);
+      if (found > 16 && (unsigned)high - (unsigned)low > 1) {
+        if (n >= need) low = mid, found = n;
+        else high = mid;
+      }
+    }
+    open = open || found > 16;  // then this is another's work
+    int2* const line = order[wave][mine];
+    // The keys that reach t, in the order of experts, one for each of the first lanes.
+    auto candidates = [&](int t) {
+      int take = 0;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) take += key[j] >= t;
+      int at = take;  // inclusive over the row's lanes
+      at += dpp<kShift + 1>(0, at);
+      at += dpp<kShift + 2>(0, at);
+      at += dpp<kShift + 4>(0, at);
+      at += dpp<kShift + 8>(0, at);
+      at -= take;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        if (key[j] >= t && at < 16) line[at] = make_int2(key[j], base + j);
+        at += key[j] >= t;
+      }
+      own_lds();
+      return line[sub16];
+    };
+    // What is handed over comes to the lane of its rank.
+    auto sorted = [&](int2 own, int rank, bool is) {
+      if (is) line[16 + rank] = own;
+      own_lds();
+      return line[16 + sub16];
+    };
+    const int some = min(found, 16);
+    int2 own = candidates(low);
+    if (sub16 >= some) own.x = kNoKey;
+    const int value[1] = {own.x}, number[1] = {sub16};
+    int rank = 0;
+    each_turn(value, [&](const int (&other)[1], auto) { rank += other[0] > own.x; });
+    if (__ballot(row16_sum(sub16 < some ? rank : 0) != some * (some - 1) / 2) != 0) {  // equal keys go by their numbers
+      each_turn(number, [&](const int (&other)[1], auto d) { rank += turned<decltype(d)::value>(own.x) == own.x && other[0] < sub16; });
+    }
+    int2 best_of = sorted(own, rank, sub16 < some);  // the row's sub16-th
+    if (by_score) {
+      const int before = dpp<kShift + 1>(best_of.x, best_of.x), last = dpp<kShift + 1>(best_of.y, best_of.y);
+      bool near = false;
+      if (found <= 16 && sub16 > 0 && sub16 < need) {
+        const float v = value_of(best_of.x);
+        if (!(value_of(before) - v > slack + 0x1p-22f * fabsf(v)))
+          near = true;
+      }
+      if (__ballot(near) != 0) {
+        const bool at_edge = (__ballot(near && sub16 == p.top_k) >> (lane & 48) & 0xFFFF) != 0;
+        if (near) near = !(logit(logits + last) == logit(logits + best_of.y) && (!p.bias || p.bias[last] == p.bias[best_of.y]));
+        if (at_edge) near = near || others_near(p, key, x, base, line[16 + p.top_k], slack, logits);
+      }
+      const uint64_t nears = __ballot(near);
+      if (nears != 0) {  // ranked in FP64, with whatever could be among them
+        const float t = value_of(low);
+        const int lower = max(ordered(t - (slack + 0x1p-22f * fabsf(t))), kNoKey + 1), more = reach(lower);
+        const bool mend = (nears >> (lane & 48) & 0xFFFF) != 0;
+        open = open || (mend && more > 16);
+        const int2 other = candidates(lower);
+        const Exactly exactly(p.sigmoid, true, top, x, 16);
+        const bool is = mend && sub16 < more && more <= 16;
+        const double k = is ? exactly.key(logit(logits + other.y), p.bias ? p.bias[other.y] : 0.f) : (double)kNone;
+        const uint64_t bits = __double_as_longlong(k);
+        const int low_half[1] = {(int)(uint32_t)bits}, high_half[1] = {(int)(bits >> 32)};
+        int place = 0;
+        each_turn(low_half, [&](const int (&theirs)[1], auto d) {
+          const uint64_t upper = (uint32_t)turned<decltype(d)::value>(high_half[0]);
+          const double v = __longlong_as_double((int64_t)(upper << 32 | (uint32_t)theirs[0]));
+          const int number = turned<decltype(d)::value>(sub16);  // by all lanes: those that are off have nothing to give
+          place += v > k || (v == k && number < sub16);
+        });
+        const int2 exact = sorted(other, place, is);
+        if (mend) best_of = exact;
+      }
+    }
+    const bool chosen = sub16 < min(p.top_k, need) && found <= 16;
+    left = __ballot(open && there);
+    const bool again = (left >> (lane & 48) & 0xFFFF) != 0;
+    float w = 0.f;
+    if (chosen) {
+      const float v = logit(logits + best_of.y);
+      w = p.sigmoid ? sigmoid(v) : exp_near(v - top) * inverse;
+    }
+    const float over = p.renormalize ? p.scale / (row16_sum(w) + kTiny) : p.scale;
+    if (there && !again && sub16 < p.top_k) {
+      p.ids[row * p.top_k + sub16] = chosen ? best_of.y : -1;
+      p.weights[row * p.top_k + sub16] = w * over;
+    }
   }
   while (left != 0) {
     const int which = uniform((__ffsll((unsigned long long)left) - 1) >> 4);
     left &= ~(0xFFFFull << 16 * which);
-    route_row<T, 1>(p, first_row + which, lane, places[wave]);
+    route_row<T, (VPL + 3) / 4>(p, first_row + which, lane, places[wave]);
   }
 }
 

@@ -127,6 +127,21 @@ def test_keys_that_differ_by_a_few_roundings_at_every_size(cuda_device, center):
     check(x, k, bias, "softmax")
 
 
+@pytest.mark.parametrize("E", [16, 32, 64, 128, 256, 300])
+@pytest.mark.parametrize("k", [1, 3, 10])
+def test_a_larger_key_behind_equal_ones(cuda_device, E, k):
+    """Many equal keys, and one that is larger by less than a rounding of theirs, after all of them."""
+    T = 70
+    x = torch.zeros(T, E, device=cuda_device)
+    bias = torch.full((E,), 0.1, device=cuda_device)
+    bias[E - 1] = torch.nextafter(bias[0], torch.tensor(1.0, device=cuda_device))
+    ids, _ = check(x, k, bias, "sigmoid")
+    assert ids[0].tolist() == [E - 1, *range(k - 1)]
+    bias[E // 2:] = -float("inf")  # as few equal ones as may be candidates
+    bias[E // 2 - 1] = torch.nextafter(bias[0], torch.tensor(1.0, device=cuda_device))
+    check(x, min(k, E // 2), bias, "sigmoid")
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_experts_that_are_not_there(cuda_device, scoring):
     T, E, k = 50, 96, 6
