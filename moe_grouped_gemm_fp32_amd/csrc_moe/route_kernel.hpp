@@ -343,8 +343,8 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const int (&key)[VP
       }
       if (__ballot(open) != 0) {
         const float t = value_of(low);
-        low = ordered(t - (slack + 0x1p-22f * fabsf(t)));  // what does not reach this is less than those that are needed
-        count = low > kNoKey ? reach(low) : live;          // also where it is no number
+        low = min(low, ordered(t - (slack + 0x1p-22f * fabsf(t))));  // what does not reach this is less than those that are
+        count = low > kNoKey ? reach(low) : live;                    // needed; of keys of +inf it is no number, of either sign
         if (count > 64) return false;
         candidates(max(low, kNoKey + 1));
         own_lds();
@@ -529,7 +529,10 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
 // Four rows a wave: 16 lanes hold a row, VPL experts each. Up to two each, every key counts the
 // larger ones of its row as they come by; more are searched for a threshold that 16 at most
 // reach, one a lane, which then count each other. What FP32 leaves open, or equal keys make too
-// many, is done again by route_row(). 16384 rows of 16 experts (sigmoid, bias) 3.4 us, of 32 5.8.
+// many, is done again by route_row(), up to 16 near keys of more than 32 experts in place. Vector
+// instructions a row of 256 experts in 8 groups 258, a wave's own row 362: 65536 rows 31.8 and
+// 43.1 us; of 16384, four waves a SIMD, whose chains bind it, 13.7 us and no more. 16384 rows of 16
+// experts (sigmoid, bias) 3.4 us, of 32 5.8, of 64 6.4.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
   __shared__ int2 places[4][64];
@@ -786,7 +789,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
       const uint64_t nears = __ballot(near);
       if (nears != 0) {  // ranked in FP64, with whatever could be among them
         const float t = value_of(low);
-        const int lower = max(ordered(t - (slack + 0x1p-22f * fabsf(t))), kNoKey + 1), more = reach(lower);
+        const int lower = max(min(low, ordered(t - (slack + 0x1p-22f * fabsf(t)))), kNoKey + 1), more = reach(lower);
         const bool mend = (nears >> (lane & 48) & 0xFFFF) != 0;
         open = open || (mend && more > 16);
         const int2 other = candidates(lower);

@@ -143,6 +143,21 @@ def test_a_larger_key_behind_equal_ones(cuda_device, E, k):
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(16, 1), (32, 4), (64, 1), (128, 8), (256, 1), (256, 8), (300, 3)])
+def test_biases_without_bounds(cuda_device, E, groups, scoring):
+    """Keys of +inf are equal, those of -inf are never chosen, those of FP32's largest are above others."""
+    T, k = 70, 4
+    x = logits_of(T, E, FP32, 21, cuda_device)
+    kw = dict(groups=groups, top_groups=max(groups // 2, 1), group_best=2 if groups > 1 else 1)
+    for value in (float("inf"), torch.finfo(FP32).max, -torch.finfo(FP32).max):
+        for some in (slice(1, None, 3), slice(0, E), slice(E // 2 - 1, E // 2 + 1)):
+            bias = torch.zeros(E, device=cuda_device)
+            bias[some] = value
+            bias[2] = -float("inf")
+            check(x, k, bias, scoring, **kw)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_experts_that_are_not_there(cuda_device, scoring):
     T, E, k = 50, 96, 6
     x = logits_of(T, E, FP32, 6, cuda_device)
