@@ -110,9 +110,17 @@ __device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_am
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int lanes_of(bool b) { return __popcll(__ballot(b)); }
 
+// What a group's score is off by at most: the errors of its scores, and 2^-24 of each key and of
+// their sum, which may be far smaller than they are. Twice over, like the slack.
+__device__ __forceinline__ float group_off(int best, int second, bool two, float slack) {
+  float off = __builtin_fmaf(0x1p-22f, fabsf(value_of(best)), slack);
+  if (two) off = __builtin_fmaf(0x1p-22f, fabsf(value_of(second)), off);
+  return off;
+}
+
 // Whether the lane's group is among the best. A group's lanes are neighbours. `sure` becomes
 // false where FP32 leaves that open (`tell`: keys are off by `slack`, as described at
-// choose()).
+// choose()): where a group that is kept need not be better than every one that is not.
 template <int VPL>
 __device__ __forceinline__ bool best_groups(const RouteParams& p, const int (&key)[VPL], int lane, bool tell, float slack, bool& sure) {
   int best = key[0], second = kNoKey;
@@ -131,8 +139,8 @@ __device__ __forceinline__ bool best_groups(const RouteParams& p, const int (&ke
   if (p.log_lanes > 2) join(moved<kHalfMirror>(best), moved<kHalfMirror>(second));
   if (p.log_lanes > 3) join(moved<kMirror>(best), moved<kMirror>(second));
   if (p.log_lanes > 4) join(__shfl_xor(best, 16, 64), __shfl_xor(second, 16, 64));
-  int score = best;
-  if (p.group_best == 2 && second > kNoKey) score = ordered(value_of(best) + value_of(second));
+  const bool two = p.group_best == 2 && second > kNoKey;
+  const int score = two ? ordered(value_of(best) + value_of(second)) : best;
   const int mine = lane >> p.log_lanes;
   const bool there = mine < p.groups;
   int rank = 0;
@@ -142,10 +150,11 @@ __device__ __forceinline__ bool best_groups(const RouteParams& p, const int (&ke
     for (int g = 0; g < p.groups; ++g) rank += lane_value(score, g << p.log_lanes) == score && g < mine;
   }
   if (tell) {
-    const int least = lane_value(score, __ffsll((unsigned long long)__ballot(there && rank == p.top_groups - 1)) - 1);
-    const int most = lane_value(score, __ffsll((unsigned long long)__ballot(there && rank == p.top_groups)) - 1);
+    const float off = group_off(best, second, two, slack);
+    const bool kept = there && rank < p.top_groups;
+    const int most = wave_max(there && !kept && best > kNoKey ? ordered(value_of(score) + off) : kNoKey);
     // where nobody is left out, nothing was decided
-    sure = most == kNoKey || value_of(least) - value_of(most) > 2.f * (slack + 0x1p-22f * fabsf(value_of(most)));
+    sure = most == kNoKey || __ballot(kept && !(value_of(score) - off > value_of(most))) == 0;
   }
   return there && rank < p.top_groups;
 }
@@ -627,8 +636,8 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
     if (log_lanes > 0) join(moved<kSwap1>(best), moved<kSwap1>(second));
     if (log_lanes > 1) join(moved<kSwap2>(best), moved<kSwap2>(second));
     if (log_lanes > 2) join(moved<kHalfMirror>(best), moved<kHalfMirror>(second));
-    int score[1] = {best}, number[1] = {group};
-    if (p.group_best == 2 && second > kNoKey) score[0] = ordered(value_of(best) + value_of(second));
+    const bool two = p.group_best == 2 && second > kNoKey;
+    const int score[1] = {two ? ordered(value_of(best) + value_of(second)) : best}, number[1] = {group};
     int rank = 0;  // in lanes
     each_turn(score, [&](const int (&other)[1], auto) { rank += other[0] > score[0]; });
     const bool is = group < p.groups;
@@ -639,8 +648,10 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
     }
     rank >>= log_lanes;
     if (by_score) {
-      const int least = row16_max(is && rank == p.top_groups - 1 ? score[0] : kNoKey), most = row16_max(is && rank == p.top_groups ? score[0] : kNoKey);
-      open = most != kNoKey && !(value_of(least) - value_of(most) > 2.f * (slack + 0x1p-22f * fabsf(value_of(most))));
+      const float off = group_off(best, second, two, slack);
+      const bool kept = is && rank < p.top_groups;
+      const int most = row16_max(is && !kept && best > kNoKey ? ordered(value_of(score[0]) + off) : kNoKey);
+      open = kept && most != kNoKey && !(value_of(score[0]) - off > value_of(most));
     }
 #pragma unroll
     for (int j = 0; j < VPL; ++j) key[j] = is && rank < p.top_groups ? key[j] : kNoKey;

@@ -1,0 +1,63 @@
+"""The order that routing goes by where FP32 leaves it open, of one row a wave and of four: group
+scores whose keys cancel.
+
+A decision is compared where 64 bits tell it: scores are off by less than 2^-50, keys and their
+sums by 2^-53 of the keys' magnitudes, on the kernel's side and on the oracle's, so that scores
+of groups 2^-48 (1 + the largest bias) apart are told."""
+import numpy as np
+import pytest
+import torch
+
+import moe_grouped_gemm_fp32_amd as fg
+import synth
+from oracle import moe_oracle as mo
+
+pytestmark = pytest.mark.gpu
+
+FP32 = torch.float32
+
+
+@pytest.fixture(params=[0, 1], ids=["all CUs", "one CU"])
+def cus(request):
+    """On one compute unit the host takes four rows a wave for 64 rows and more."""
+    fg.set_num_cus(request.param)
+    yield request.param
+    fg.set_num_cus(0)
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+@pytest.mark.parametrize("size", [0.5, 1.0, 5.0, 100.0])
+@pytest.mark.parametrize("scoring,center", [("sigmoid", -4.0), ("sigmoid", -8.0), ("softmax", 0.0)])
+@pytest.mark.parametrize("E,groups,top_groups", [(4, 2, 1), (16, 8, 3), (64, 2, 1), (64, 8, 3), (256, 8, 4), (512, 4, 2)])
+def test_groups_whose_two_keys_cancel(cuda_device, cus, E, groups, top_groups, scoring, center, size):
+    """In each group one bias of +size and one of -size, and scores whose sums are nearly the same."""
+    T = 300
+    g = synth.make_generator(7, cuda_device)
+    x = center + 0.3 * torch.randn(T, groups, E // groups, generator=g, device=cuda_device, dtype=torch.float64).clamp(-2, 2)
+    bias = torch.full((groups, E // groups), -4 * size, device=cuda_device)
+    bias[:, 0], bias[:, -1] = size, -size
+    if scoring == "sigmoid":
+        total = 2.2 * torch.sigmoid(torch.tensor(center, dtype=torch.float64))
+        x[..., -1] = torch.logit(total - torch.sigmoid(x[..., 0].float().double()))
+    else:
+        x[..., -1] = torch.log(2.2 - x[..., 0].float().double().exp())
+    x, bias = x.view(T, E).float(), bias.view(E)
+    ids, w = fg.moe_route(x, 2, bias=bias, scoring=scoring, groups=groups, top_groups=top_groups, group_best=2)
+    ri, rw, rs = mo.route(f64(x), 2, f64(bias), scoring, groups=groups, top_groups=top_groups, group_best=2)
+    keys = -np.sort(-(rs + f64(bias)).reshape(T, groups, -1), axis=2)
+    of = -np.sort(-keys[:, :, :2].sum(2), axis=1)
+    decided = of[:, top_groups - 1] - of[:, top_groups] > 2.0 ** -48 * (1 + size)
+    assert decided.mean() > 0.9
+    assert np.array_equal(ids.cpu().numpy()[decided], ri[decided])
+    assert np.all(np.abs(f64(w) - rw)[decided] <= 2.0 ** -16 * rw[decided])
+
+
+def test_one_row_whose_group_scores_cancel(cuda_device):
+    """Scores 8.05306e-4 and 8.05238e-4: the first group. Keys near 1 and -1 are rounded by 6e-8."""
+    x = torch.tensor([[-7.774, -7.862, -8.271, -7.506]], device=cuda_device)
+    bias = torch.tensor([1.0, -1.0, 1.0, -1.0], device=cuda_device)
+    ids, _ = fg.moe_route(x, 2, bias=bias, scoring="sigmoid", groups=2, top_groups=1, group_best=2)
+    assert ids.tolist() == [[0, 1]]
