@@ -83,6 +83,8 @@ __device__ __forceinline__ int ordered(float v) {
 __device__ __forceinline__ float value_of(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 constexpr int kNoKey = (int)0x807FFFFF;  // of -inf
 constexpr int kLowest = (int)0x80000000;
+constexpr int kInfinite = 0x7F800000;    // of +inf
+constexpr float kLargest = 3.40282346638528859812e38f;
 
 template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ int max_with(int v) {
@@ -110,6 +112,13 @@ __device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_am
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int lanes_of(bool b) { return __popcll(__ballot(b)); }
 
+// A group's score, kNoKey without experts. A sum past FP32's numbers becomes the last of them, so
+// that a group with experts has no empty one's score; such groups meet there, and FP64 decides.
+__device__ __forceinline__ int group_score(int best, int second, bool two) {
+  if (!two) return best;
+  const float sum = value_of(best) + value_of(second);
+  return ordered(best < kInfinite ? __builtin_amdgcn_fmed3f(sum, -kLargest, kLargest) : sum);
+}
 // What a group's score is off by at most: the errors of its scores, and 2^-24 of each key and of
 // their sum, which may be far smaller than they are. Twice over, like the slack.
 __device__ __forceinline__ float group_off(int best, int second, bool two, float slack) {
@@ -140,7 +149,7 @@ __device__ __forceinline__ bool best_groups(const RouteParams& p, const int (&ke
   if (p.log_lanes > 3) join(moved<kMirror>(best), moved<kMirror>(second));
   if (p.log_lanes > 4) join(__shfl_xor(best, 16, 64), __shfl_xor(second, 16, 64));
   const bool two = p.group_best == 2 && second > kNoKey;
-  const int score = two ? ordered(value_of(best) + value_of(second)) : best;
+  const int score = group_score(best, second, two);
   const int mine = lane >> p.log_lanes;
   const bool there = mine < p.groups;
   int rank = 0;
@@ -637,7 +646,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
     if (log_lanes > 1) join(moved<kSwap2>(best), moved<kSwap2>(second));
     if (log_lanes > 2) join(moved<kHalfMirror>(best), moved<kHalfMirror>(second));
     const bool two = p.group_best == 2 && second > kNoKey;
-    const int score[1] = {two ? ordered(value_of(best) + value_of(second)) : best}, number[1] = {group};
+    const int score[1] = {group_score(best, second, two)}, number[1] = {group};
     int rank = 0;  // in lanes
     each_turn(score, [&](const int (&other)[1], auto) { rank += other[0] > score[0]; });
     const bool is = group < p.groups;

@@ -1,5 +1,5 @@
 """The order that routing goes by where FP32 leaves it open, of one row a wave and of four: group
-scores whose keys cancel.
+scores whose keys cancel or pass FP32's numbers.
 
 A decision is compared where 64 bits tell it: scores are off by less than 2^-50, keys and their
 sums by 2^-53 of the keys' magnitudes, on the kernel's side and on the oracle's, so that scores
@@ -61,3 +61,27 @@ def test_one_row_whose_group_scores_cancel(cuda_device):
     bias = torch.tensor([1.0, -1.0, 1.0, -1.0], device=cuda_device)
     ids, _ = fg.moe_route(x, 2, bias=bias, scoring="sigmoid", groups=2, top_groups=1, group_best=2)
     assert ids.tolist() == [[0, 1]]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(4, 2), (16, 4), (32, 4), (64, 2), (64, 8), (256, 8), (512, 4)])
+def test_group_scores_that_pass_fp32(cuda_device, cus, E, groups, scoring):
+    """Sums of two keys below FP32's lowest value or above its largest: a group without experts is no
+    better than those, and their order is that of the sums."""
+    T, size, big = 70, E // groups, torch.finfo(FP32).max
+    x = torch.randn(T, E, generator=synth.make_generator(3, cuda_device), device=cuda_device)
+    kw = dict(groups=groups, group_best=2)
+    for top_groups in (1, max(1, groups // 2)):
+        for sign in (-1.0, 1.0):
+            for parts in ((1.0, 1.0), (1.0, 0.9), (0.9, 1.0), (1.0, 0.4)):
+                bias = torch.zeros(groups, size, device=cuda_device)
+                for i in range(groups):
+                    bias[i] = sign * big * parts[i % 2]
+                for empty in (False, True):
+                    y = x.clone()
+                    if empty:
+                        y[:, :size] = -float("inf")
+                    ids, w = fg.moe_route(y, 2, bias=bias.view(E), scoring=scoring, top_groups=top_groups, **kw)
+                    ri, rw, _ = mo.route(f64(y), 2, f64(bias.view(E)), scoring, top_groups=top_groups, **kw)
+                    assert np.array_equal(ids.cpu().numpy(), ri), (top_groups, sign, parts, empty)
+                    assert np.all(np.abs(f64(w) - rw) <= 2.0 ** -16 * rw + 2.0 ** -100)
