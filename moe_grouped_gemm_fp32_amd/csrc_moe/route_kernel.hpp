@@ -86,6 +86,9 @@ constexpr int kLowest = (int)0x80000000;
 constexpr int kInfinite = 0x7F800000;    // of +inf
 constexpr float kLargest = 3.40282346638528859812e38f;
 
+// Of an expert that its logit alone orders.
+__device__ __forceinline__ int logit_key(float x) { return ordered(x == x ? x : kNanKey); }
+
 template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ int max_with(int v) {
   // all rows: every lane has a source
@@ -195,20 +198,19 @@ __device__ __forceinline__ bool best_groups(const RouteParams& p, const double (
 
 // A row's keys in FP64.
 struct Exactly {
-  bool sigmoid, by_score;
+  bool sigmoid;
   double top, sum;  // of the softmax
   template <int VPL>
-  __device__ __forceinline__ Exactly(bool sigmoid, bool by_score, float top, const float (&x)[VPL], int lanes = 64)
-      : sigmoid(sigmoid), by_score(by_score), top(top), sum(0.0) {
-    if (sigmoid || !by_score) return;
+  __device__ __forceinline__ Exactly(bool sigmoid, float top, const float (&x)[VPL], int lanes = 64)
+      : sigmoid(sigmoid), top(top), sum(0.0) {
+    if (sigmoid) return;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) sum += exp((double)x[j] - this->top);
     for (int off = lanes / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
   }
   __device__ __forceinline__ double key(float x, float bias) const {
     if (x == kNone) return (double)kNone;
-    double k = x;
-    if (by_score) k = (sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - top) / sum) + (double)bias;
+    const double k = (sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - top) / sum) + (double)bias;
     return k == k ? k : (double)kNanKey;
   }
 };
@@ -366,7 +368,7 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const int (&key)[VP
         if (count > 64) return false;
         candidates(max(low, kNoKey + 1));
         own_lds();
-        const Exactly exactly(p.sigmoid, true, top_logit, x);
+        const Exactly exactly(p.sigmoid, top_logit, x);
         e = lane < count ? place[lane].y : 0;
         const double k = lane < count ? exactly.key(logit(logits + e), p.bias ? p.bias[e] : 0.f) : (double)kNone;
         rank = 0;
@@ -407,7 +409,7 @@ __device__ __forceinline__ float slack_of(int largest, int sigmoid) {
 
 // One row, by a wave. The keys stay in registers, a group's in neighbouring lanes. Keys are FP32;
 // what they leave open (in 2 of 1000 rows of 256 sigmoid scores with a bias) is decided in FP64.
-// Without a bias experts are compared by their logits, exactly. Bound by vector instructions:
+// Without a bias experts are compared by their logits, exactly, and only groups by scores. Bound by vector instructions:
 // 16384 rows of 256 experts in 8 groups, 8 chosen, 362 a row, 14.1 us (their bytes take 3.7);
 // without groups and bias 8.9; one row 3.4 us, most of it the launch and one chain.
 template <typename T, int VPL>
@@ -419,6 +421,7 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
   const int base = group * p.size + begin;
   const bool limited = p.top_groups < p.groups;
   const bool by_score = p.bias || (p.group_best == 2 && limited);  // else the logits' order is the scores'
+  const bool tell = p.bias;  // experts without a bias go by their logits, however their groups are found
   float x[VPL], bias[VPL] = {};
   int key[VPL];
   if (p.even) {
@@ -484,10 +487,10 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = x[j] == x[j] ? ordered(x[j]) : ordered(kNanKey);
+    for (int j = 0; j < VPL; ++j) key[j] = logit_key(x[j]);
   }
   auto exact_keys = [&](double (&wide)[VPL]) {
-    const Exactly exactly(p.sigmoid, by_score, top, x);
+    const Exactly exactly(p.sigmoid, top, x);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) wide[j] = exactly.key(x[j], p.bias ? p.bias[min(base + j, p.E - 1)] : 0.f);
   };
@@ -498,11 +501,15 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
       exact_keys(wide);
       kept = best_groups<VPL>(p, wide, lane);
     }
+    if (by_score && !tell) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) key[j] = logit_key(x[j]);
+    }
 #pragma unroll
     for (int j = 0; j < VPL; ++j) key[j] = kept ? key[j] : kNoKey;
   }
   int id;
-  if (!choose<VPL>(p, key, x, base, lane, by_score, slack, top, logits, place, id)) {
+  if (!choose<VPL>(p, key, x, base, lane, tell, slack, top, logits, place, id)) {
     double wide[VPL];
     exact_keys(wide);
 #pragma unroll
@@ -566,7 +573,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
   const int count = group < p.groups ? min(max(p.size - begin, 0), each) : 0;
   const int base = group * p.size + begin;
   const bool limited = p.top_groups < p.groups;
-  const bool by_score = p.bias || (p.group_best == 2 && limited);
+  const bool by_score = p.bias || (p.group_best == 2 && limited), tell = p.bias;
   float x[VPL], s[VPL];
   int key[VPL];
   if (p.even_16) {
@@ -628,7 +635,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
     slack = slack_of(row16_max(__float_as_int(largest)), p.sigmoid);
   } else {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = ordered(x[j] == x[j] ? x[j] : kNanKey);
+    for (int j = 0; j < VPL; ++j) key[j] = logit_key(x[j]);
   }
   bool open = false;
   if (limited) {
@@ -662,6 +669,10 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
       const int most = row16_max(is && !kept && best > kNoKey ? ordered(value_of(score[0]) + off) : kNoKey);
       open = kept && most != kNoKey && !(value_of(score[0]) - off > value_of(most));
     }
+    if (by_score && !tell) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) key[j] = logit_key(x[j]);
+    }
 #pragma unroll
     for (int j = 0; j < VPL; ++j) key[j] = is && rank < p.top_groups ? key[j] : kNoKey;
   }
@@ -691,7 +702,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
         }
       });
     }
-    if (by_score) {
+    if (tell) {
 #pragma unroll
       for (int j = 0; j < VPL; ++j)
         if (key[j] > kNoKey) order[wave][mine][rank[j]] = make_int2(key[j], base + j);
@@ -729,7 +740,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
       for (int i = live + sub16; i < p.top_k; i += 16) p.ids[out + i] = -1, p.weights[out + i] = 0.f;
     }
   } else {
-    const int need = min(p.top_k + (int)by_score, live);  // at most 16
+    const int need = min(p.top_k + (int)tell, live);  // at most 16
     // Of the lanes' largest keys, or their two largest, there are enough that reach the least of
     // them; `low` is reached by enough, `high` by too few.
     int best = key[0], second = kNoKey;
@@ -793,7 +804,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
       each_turn(number, [&](const int (&other)[1], auto d) { rank += turned<decltype(d)::value>(own.x) == own.x && other[0] < sub16; });
     }
     int2 best_of = sorted(own, rank, sub16 < some);  // the row's sub16-th
-    if (by_score) {
+    if (tell) {
       const int before = dpp<kShift + 1>(best_of.x, best_of.x), last = dpp<kShift + 1>(best_of.y, best_of.y);
       bool near = false;
       if (found <= 16 && sub16 > 0 && sub16 < need) {
@@ -813,7 +824,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
         const bool mend = (nears >> (lane & 48) & 0xFFFF) != 0;
         open = open || (mend && more > 16);
         const int2 other = candidates(lower);
-        const Exactly exactly(p.sigmoid, true, top, x, 16);
+        const Exactly exactly(p.sigmoid, top, x, 16);
         const bool is = mend && sub16 < more && more <= 16;
         const double k = is ? exactly.key(logit(logits + other.y), p.bias ? p.bias[other.y] : 0.f) : (double)kNone;
         const uint64_t bits = __double_as_longlong(k);

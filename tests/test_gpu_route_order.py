@@ -1,5 +1,5 @@
 """The order that routing goes by where FP32 leaves it open, of one row a wave and of four: group
-scores whose keys cancel or pass FP32's numbers.
+scores whose keys cancel or pass FP32's numbers, logits whose scores are the same.
 
 A decision is compared where 64 bits tell it: scores are off by less than 2^-50, keys and their
 sums by 2^-53 of the keys' magnitudes, on the kernel's side and on the oracle's, so that scores
@@ -85,3 +85,18 @@ def test_group_scores_that_pass_fp32(cuda_device, cus, E, groups, scoring):
                     ri, rw, _ = mo.route(f64(y), 2, f64(bias.view(E)), scoring, top_groups=top_groups, **kw)
                     assert np.array_equal(ids.cpu().numpy(), ri), (top_groups, sign, parts, empty)
                     assert np.all(np.abs(f64(w) - rw) <= 2.0 ** -16 * rw + 2.0 ** -100)
+
+
+@pytest.mark.parametrize("scoring,low", [("sigmoid", 37.5), ("softmax", -900.0)])
+@pytest.mark.parametrize("E,groups,top_groups", [(4, 2, 1), (32, 4, 2), (64, 2, 1), (64, 16, 7), (256, 8, 4), (512, 4, 2)])
+def test_experts_without_a_bias_go_by_their_logits(cuda_device, cus, E, groups, top_groups, scoring, low):
+    """Scores of 1 and of 0 to the last bit, whose logits differ, in groups that take two keys."""
+    T, size = 90, E // groups
+    x = low + torch.rand(T, E, generator=synth.make_generator(4, cuda_device), device=cuda_device) * 8
+    if scoring == "softmax":
+        x[:, ::size] = 0.0  # one expert of each group has the scores
+    k = min(6, top_groups * size)
+    ids, w = fg.moe_route(x, k, scoring=scoring, groups=groups, top_groups=top_groups, group_best=2)
+    ri, rw, _ = mo.route(f64(x), k, None, scoring, groups=groups, top_groups=top_groups, group_best=2)
+    assert np.array_equal(ids.cpu().numpy(), ri)
+    assert np.all(np.abs(f64(w) - rw) <= 2.0 ** -16 * rw)
