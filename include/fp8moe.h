@@ -45,7 +45,7 @@ enum { FP8MOE_SOFTMAX = 0, FP8MOE_SIGMOID = 1 };
  * keys: where FP32 cannot tell two of them apart they are computed in FP64 (without a bias
  * the logits' own order decides between experts). An expert whose logit or key is -inf is
  * never chosen; where fewer than top_k are left, the last ids are -1 with weight 0. NaN
- * keys are chosen last; the weights are what the formula gives.
+ * keys are chosen last, after every number; the weights are what the formula gives.
  *   logits  BF16 or FP32 (dtype), row stride ldl. bias fp32 [E] or NULL.
  *   ids     int32 [T, top_k], weights fp32 [T, top_k], contiguous.
  *   scores  optional fp32 [T, E], row stride lds: s.

@@ -11,7 +11,10 @@ namespace fp8moe {
 using namespace fp8layer;
 
 constexpr float kNone = -__builtin_huge_valf();
-constexpr float kNanKey = -1e30f;  // below every key that is a number of any use
+constexpr float kLargest = 3.40282346638528859812e38f;
+// Of a NaN, below every number: in FP32 it meets the last of them, and FP64 decides.
+constexpr float kNanKey = -kLargest;
+constexpr double kNanExactly = -1e300;
 constexpr float kTiny = 1e-20f;    // what a sum of chosen scores is divided with at least
 
 // exp(x): 2^(x log2 e) with the product's rounding error put back, which would otherwise be
@@ -84,10 +87,22 @@ __device__ __forceinline__ float value_of(int i) { return __int_as_float(i ^ ((i
 constexpr int kNoKey = (int)0x807FFFFF;  // of -inf
 constexpr int kLowest = (int)0x80000000;
 constexpr int kInfinite = 0x7F800000;    // of +inf
-constexpr float kLargest = 3.40282346638528859812e38f;
 
-// Of an expert that its logit alone orders.
-__device__ __forceinline__ int logit_key(float x) { return ordered(x == x ? x : kNanKey); }
+// Of experts that their logits alone order. Where a row of the wave has a NaN, numbers make room for
+// it above what is never chosen.
+template <int VPL>
+__device__ __forceinline__ void logit_keys(const float (&x)[VPL], int (&key)[VPL]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    key[j] = ordered(x[j]);
+    sum += x[j];
+  }
+  if (__ballot(sum != sum) != 0) {  // or has infinities of both signs, or sums to them
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = x[j] != x[j] ? kNoKey + 1 : key[j] + (key[j] > kNoKey);
+  }
+}
 
 template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ int max_with(int v) {
@@ -211,7 +226,7 @@ struct Exactly {
   __device__ __forceinline__ double key(float x, float bias) const {
     if (x == kNone) return (double)kNone;
     const double k = (sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - top) / sum) + (double)bias;
-    return k == k ? k : (double)kNanKey;
+    return k == k ? k : kNanExactly;
   }
 };
 
@@ -486,8 +501,7 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
         if (s[j] != s[j] && x[j] != kNone) key[j] = ordered(kNanKey);
     }
   } else {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = logit_key(x[j]);
+    logit_keys(x, key);
   }
   auto exact_keys = [&](double (&wide)[VPL]) {
     const Exactly exactly(p.sigmoid, top, x);
@@ -501,10 +515,7 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
       exact_keys(wide);
       kept = best_groups<VPL>(p, wide, lane);
     }
-    if (by_score && !tell) {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) key[j] = logit_key(x[j]);
-    }
+    if (by_score && !tell) logit_keys(x, key);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) key[j] = kept ? key[j] : kNoKey;
   }
@@ -634,8 +645,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
     }
     slack = slack_of(row16_max(__float_as_int(largest)), p.sigmoid);
   } else {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = logit_key(x[j]);
+    logit_keys(x, key);
   }
   bool open = false;
   if (limited) {
@@ -669,10 +679,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
       const int most = row16_max(is && !kept && best > kNoKey ? ordered(value_of(score[0]) + off) : kNoKey);
       open = kept && most != kNoKey && !(value_of(score[0]) - off > value_of(most));
     }
-    if (by_score && !tell) {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) key[j] = logit_key(x[j]);
-    }
+    if (by_score && !tell) logit_keys(x, key);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) key[j] = is && rank < p.top_groups ? key[j] : kNoKey;
   }

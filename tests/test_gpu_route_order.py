@@ -1,5 +1,5 @@
 """The order that routing goes by where FP32 leaves it open, of one row a wave and of four: group
-scores whose keys cancel or pass FP32's numbers, logits whose scores are the same.
+scores whose keys cancel or pass FP32's numbers, logits whose scores are the same, NaN.
 
 A decision is compared where 64 bits tell it: scores are off by less than 2^-50, keys and their
 sums by 2^-53 of the keys' magnitudes, on the kernel's side and on the oracle's, so that scores
@@ -100,3 +100,38 @@ def test_experts_without_a_bias_go_by_their_logits(cuda_device, cus, E, groups, 
     ri, rw, _ = mo.route(f64(x), k, None, scoring, groups=groups, top_groups=top_groups, group_best=2)
     assert np.array_equal(ids.cpu().numpy(), ri)
     assert np.all(np.abs(f64(w) - rw) <= 2.0 ** -16 * rw)
+
+
+@pytest.mark.parametrize("E", [3, 16, 32, 64, 256, 300])
+def test_nan_comes_after_every_number(cuda_device, cus, E):
+    """Also after FP32's lowest, which a mask may use; and before what is never chosen."""
+    T, lowest, nan, none = 70, torch.finfo(FP32).min, float("nan"), -float("inf")
+    x = torch.full((T, E), none, device=cuda_device)
+    x[:, 0], x[:, 1], x[:, E - 1] = nan, lowest, 1.0
+    for scoring in ("sigmoid", "softmax"):
+        assert fg.moe_route(x, 3, scoring=scoring)[0].tolist() == [[E - 1, 1, 0]] * T
+    assert fg.moe_route(x, 2, scoring="sigmoid")[1].isnan().sum() == 0
+    y = torch.where(x == lowest, -2e30, x)
+    assert fg.moe_route(y, 3, scoring="sigmoid")[0].tolist() == [[E - 1, 1, 0]] * T
+    x[:, 1] = 0.0
+    for value in (lowest, -2e30):
+        bias = torch.zeros(E, device=cuda_device)
+        bias[1] = value
+        assert fg.moe_route(x, 3, bias=bias, scoring="sigmoid")[0].tolist() == [[E - 1, 1, 0]] * T
+        bias[1], bias[0] = nan, value
+        z = torch.where(x.isnan(), 0.0, x)  # a bias that is none
+        assert fg.moe_route(z, 3, bias=bias, scoring="sigmoid")[0].tolist() == [[E - 1, 0, 1]] * T
+
+
+@pytest.mark.parametrize("E,groups", [(4, 2), (16, 4), (64, 2), (256, 8), (512, 4)])
+def test_groups_of_nan_come_last(cuda_device, cus, E, groups):
+    T, size, lowest = 70, E // groups, torch.finfo(FP32).min
+    x = torch.zeros(T, groups, size, device=cuda_device)
+    x[:, :-1] = float("nan")
+    for bias in (None, torch.zeros(E, device=cuda_device), torch.full((E,), lowest, device=cuda_device)):
+        for best in (1, 2):
+            ids, _ = fg.moe_route(x.view(T, E), 2, bias=bias, scoring="sigmoid", groups=groups, top_groups=1, group_best=best)
+            assert ids.tolist() == [[E - size, E - size + 1]] * T
+    x[:, -1] = lowest
+    ids, _ = fg.moe_route(x.view(T, E), 2, scoring="sigmoid", groups=groups, top_groups=1)
+    assert ids.tolist() == [[E - size, E - size + 1]] * T
