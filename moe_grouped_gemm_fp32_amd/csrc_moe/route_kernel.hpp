@@ -417,9 +417,11 @@ __device__ __forceinline__ float sum_of_chosen(float s) {
 // How far two keys' errors come to, twice over, for a row's largest score, whose bits have the
 // order of what is not negative. Sigmoids: s |x| (1 - s) grows up to s = 1/4 and then stays below
 // 0.28, and |x| < 0.7 (e + 1) for a largest score of 2^-e. Softmax: three roundings and the
-// exponent's, and the sum's, common to a row, of up to 38 terms and levels.
+// exponent's, and the sum's, common to a row, of up to 38 terms and levels. Scores below 2^-126 are
+// computed as 0.
 __device__ __forceinline__ float slack_of(int largest, int sigmoid) {
-  return __int_as_float(largest) * (sigmoid ? 0x1p-19f + 0x1p-21f * (float)(127 - (largest >> 23)) : 0x1p-17f);
+  const float relative = sigmoid ? 0x1p-19f + 0x1p-21f * (float)(127 - (largest >> 23)) : 0x1p-17f;
+  return __builtin_fmaf(__int_as_float(largest), relative, 0x1p-124f);
 }
 
 // One row, by a wave. The keys stay in registers, a group's in neighbouring lanes. Keys are FP32;

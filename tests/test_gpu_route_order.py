@@ -1,5 +1,6 @@
 """The order that routing goes by where FP32 leaves it open, of one row a wave and of four: group
-scores whose keys cancel or pass FP32's numbers, logits whose scores are the same, NaN.
+scores whose keys cancel or pass FP32's numbers, logits whose scores are the same, NaN,
+scores below the normal numbers.
 
 A decision is compared where 64 bits tell it: scores are off by less than 2^-50, keys and their
 sums by 2^-53 of the keys' magnitudes, on the kernel's side and on the oracle's, so that scores
@@ -135,3 +136,15 @@ def test_groups_of_nan_come_last(cuda_device, cus, E, groups):
     x[:, -1] = lowest
     ids, _ = fg.moe_route(x.view(T, E), 2, scoring="sigmoid", groups=groups, top_groups=1)
     assert ids.tolist() == [[E - size, E - size + 1]] * T
+
+
+@pytest.mark.parametrize("E", [16, 32, 64, 256, 300])
+def test_scores_below_the_normal_numbers(cuda_device, cus, E):
+    """sigmoid(-87.5) = 1e-38 is nothing to the card, and larger than a bias of 2e-39."""
+    T = 70
+    x = torch.full((T, E), -100.0, device=cuda_device)
+    x[:, E - 1] = -87.5
+    bias = torch.zeros(E, device=cuda_device)
+    bias[:E // 2] = 2e-39
+    ids, _ = fg.moe_route(x, 3, bias=bias, scoring="sigmoid")
+    assert ids.tolist() == [[E - 1, 0, 1]] * T
