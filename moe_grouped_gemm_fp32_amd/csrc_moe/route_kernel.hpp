@@ -134,8 +134,7 @@ __device__ __forceinline__ int lanes_of(bool b) { return __popcll(__ballot(b)); 
 // that a group with experts has no empty one's score; such groups meet there, and FP64 decides.
 __device__ __forceinline__ int group_score(int best, int second, bool two) {
   if (!two) return best;
-  const float sum = value_of(best) + value_of(second);
-  return ordered(best < kInfinite ? __builtin_amdgcn_fmed3f(sum, -kLargest, kLargest) : sum);
+  return min(max(ordered(value_of(best) + value_of(second)), kNoKey + 1), max(best, kInfinite - 1));
 }
 // What a group's score is off by at most: the errors of its scores, and 2^-24 of each key and of
 // their sum, which may be far smaller than they are. Twice over, like the slack.
@@ -168,6 +167,7 @@ __device__ __forceinline__ bool best_groups(const RouteParams& p, const int (&ke
   if (p.log_lanes > 4) join(__shfl_xor(best, 16, 64), __shfl_xor(second, 16, 64));
   const bool two = p.group_best == 2 && second > kNoKey;
   const int score = group_score(best, second, two);
+  const float off = tell ? group_off(best, second, two, slack) : 0.f;
   const int mine = lane >> p.log_lanes;
   const bool there = mine < p.groups;
   int rank = 0;
@@ -177,9 +177,8 @@ __device__ __forceinline__ bool best_groups(const RouteParams& p, const int (&ke
     for (int g = 0; g < p.groups; ++g) rank += lane_value(score, g << p.log_lanes) == score && g < mine;
   }
   if (tell) {
-    const float off = group_off(best, second, two, slack);
     const bool kept = there && rank < p.top_groups;
-    const int most = wave_max(there && !kept && best > kNoKey ? ordered(value_of(score) + off) : kNoKey);
+    const int most = wave_max(there && !kept && score > kNoKey ? ordered(value_of(score) + off) : kNoKey);
     // where nobody is left out, nothing was decided
     sure = most == kNoKey || __ballot(kept && !(value_of(score) - off > value_of(most))) == 0;
   }
@@ -421,7 +420,7 @@ __device__ __forceinline__ float sum_of_chosen(float s) {
 // computed as 0.
 __device__ __forceinline__ float slack_of(int largest, int sigmoid) {
   const float relative = sigmoid ? 0x1p-19f + 0x1p-21f * (float)(127 - (largest >> 23)) : 0x1p-17f;
-  return __builtin_fmaf(__int_as_float(largest), relative, 0x1p-124f);
+  return fmaxf(__int_as_float(largest) * relative, 0x1p-124f);
 }
 
 // One row, by a wave. The keys stay in registers, a group's in neighbouring lanes. Keys are FP32;
@@ -517,7 +516,12 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
       exact_keys(wide);
       kept = best_groups<VPL>(p, wide, lane);
     }
-    if (by_score && !tell) logit_keys(x, key);
+    if (by_score && !tell) {  // loaded again: held over FP64's groups they are 15 registers of 16 experts
+      float y[VPL];
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) y[j] = j < count ? logit(logits + min(base + j, p.E - 1)) : kNone;
+      logit_keys(y, key);
+    }
 #pragma unroll
     for (int j = 0; j < VPL; ++j) key[j] = kept ? key[j] : kNoKey;
   }
@@ -666,6 +670,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
     if (log_lanes > 2) join(moved<kHalfMirror>(best), moved<kHalfMirror>(second));
     const bool two = p.group_best == 2 && second > kNoKey;
     const int score[1] = {group_score(best, second, two)}, number[1] = {group};
+    const float off = by_score ? group_off(best, second, two, slack) : 0.f;
     int rank = 0;  // in lanes
     each_turn(score, [&](const int (&other)[1], auto) { rank += other[0] > score[0]; });
     const bool is = group < p.groups;
@@ -676,9 +681,8 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
     }
     rank >>= log_lanes;
     if (by_score) {
-      const float off = group_off(best, second, two, slack);
       const bool kept = is && rank < p.top_groups;
-      const int most = row16_max(is && !kept && best > kNoKey ? ordered(value_of(score[0]) + off) : kNoKey);
+      const int most = row16_max(is && !kept && score[0] > kNoKey ? ordered(value_of(score[0]) + off) : kNoKey);
       open = kept && most != kNoKey && !(value_of(score[0]) - off > value_of(most));
     }
     if (by_score && !tell) logit_keys(x, key);
