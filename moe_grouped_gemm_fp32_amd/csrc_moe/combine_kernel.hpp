@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(WAVES * 64) combine_backward_kernel(const Comb
       if (row[j] >= p.rows) row[j] = -1;
       w[j] = p.weights[token * p.top_k + first + j];
     }
-    for (int column = threadIdx.x * 8; column < p.N; column += WAVES * 512) {
+    for (uint32_t column = threadIdx.x * 8; column < (uint32_t)p.N; column += WAVES * 512) {  // past the last one below 2^32
       Eight<T> y[8];
       float g[8];
 #pragma unroll
