@@ -97,7 +97,7 @@ int64_t fp8_moe_rows(int T, int top_k, int E);
  *              NULL where that is 0); needs no initial value.
  * K a multiple of 128 up to 65536; Q, Qx 16-byte aligned with strides multiples of 16; ld_sa
  * >= T, ld_sax >= rows (masked: max_m), multiples of 4. 1 <= E <= 1024, 1 <= top_k <= 64;
- * T * top_k and rows below 2^31 - 2^16.
+ * T * top_k and rows below 2^31 - 2^18 (the segments of 1024 experts end within 32 bits).
  */
 int fp8_moe_dispatch(const void* Q, int64_t ldq, const float* sa, int64_t ld_sa, const int32_t* ids,
                      const float* weights, void* Qx, int64_t ldqx, float* sax, int64_t ld_sax, int32_t* positions,
@@ -151,7 +151,7 @@ int fp8_moe_combine_backward(const void* dO, int64_t lddo, const void* Y, int64_
  *   cos_sin  fp32 [max_pos][ld_cs], cosines of rot_dim / 2 angles, then their sines.
  *   positions  int32 [T], clamped to [0, max_pos); NULL: t.
  * D 64, 128 or 256; rot_dim a multiple of 16, 0 .. D (0: no table). Addresses 16-byte aligned,
- * row strides multiples of 16 bytes, ld_cs of 4. T * (Hq + Hk) below 2^31 - 2^16, Hq * D and
+ * row strides multiples of 16 bytes, ld_cs of 4. T * (Hq + Hk) below 2^31 - 2^18, Hq * D and
  * Hk * D below 2^31.
  */
 int fp8_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int dtype, const void* qw, const void* kw,
