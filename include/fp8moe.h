@@ -50,7 +50,7 @@ enum { FP8MOE_SOFTMAX = 0, FP8MOE_SIGMOID = 1 };
  *   ids     int32 [T, top_k], weights fp32 [T, top_k], contiguous.
  *   scores  optional fp32 [T, E], row stride lds: s.
  * 1 <= E <= 1024, 1 <= top_k <= min(E, 64), groups divides E and is at most 64,
- * 1 <= top_groups <= groups.
+ * 1 <= top_groups <= groups, scale between -2^60 and 2^60.
  */
 int fp8_moe_route(const void* logits, int64_t ldl, int dtype, const float* bias, int scoring, int groups,
                   int top_groups, int group_best, int renormalize, float scale, int32_t* ids, float* weights,

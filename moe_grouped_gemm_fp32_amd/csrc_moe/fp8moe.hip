@@ -19,6 +19,8 @@ using fp8moe::kPiece;
 constexpr int kMaxChoices = 64;               // of a token: a lane holds one
 constexpr int64_t kMost = INT32_MAX - (1 << 18);  // choices and rows, so that segments' ends fit 32 bits
 
+// Weights are scaled by scale / (sum of scores + 1e-20), which has to be a number.
+bool route_scale(float scale) { return std::fabs(scale) <= 0x1p60f; }
 bool route_shape(int T, int E, int top_k) { return T >= 0 && E >= 1 && E <= kMaxExperts && top_k >= 1 && top_k <= std::min(E, kMaxChoices); }
 bool rows_dtype(int t) { return norm_dtype(t); }
 // row stride of a [.., E] array of `size`-byte elements that are read one by one
@@ -44,7 +46,7 @@ int fp8_moe_route(const void* logits, int64_t ldl, int dtype, const float* bias,
                   int T, int E, int top_k, hipStream_t stream) {
   if (T != 0 && (!logits || !ids || !weights)) return FP8GEMM_ERR_NULL;
   if (!route_shape(T, E, top_k) || groups < 1 || groups > 64 || E % groups != 0 || top_groups < 1 || top_groups > groups ||
-      (group_best != 1 && group_best != 2) || !std::isfinite(scale))
+      (group_best != 1 && group_best != 2) || !route_scale(scale))
     return FP8GEMM_ERR_SHAPE;
   if (!rows_dtype(dtype) || (scoring != FP8MOE_SOFTMAX && scoring != FP8MOE_SIGMOID)) return FP8GEMM_ERR_LAYOUT;
   if (T == 0) return FP8GEMM_OK;
@@ -98,7 +100,7 @@ int fp8_moe_route_backward(const float* dweights, const void* logits, int64_t ld
                            int renormalize, float scale, const float* dscores, int64_t ldds, void* dlogits, int64_t lddl,
                            int T, int E, int top_k, hipStream_t stream) {
   if (T != 0 && (!dweights || !logits || !ids || !dlogits)) return FP8GEMM_ERR_NULL;
-  if (!route_shape(T, E, top_k) || !std::isfinite(scale)) return FP8GEMM_ERR_SHAPE;
+  if (!route_shape(T, E, top_k) || !route_scale(scale)) return FP8GEMM_ERR_SHAPE;
   if (!rows_dtype(dtype) || (scoring != FP8MOE_SOFTMAX && scoring != FP8MOE_SIGMOID)) return FP8GEMM_ERR_LAYOUT;
   if (T == 0) return FP8GEMM_OK;
   if (!narrow_rows(logits, ldl, E, size_of(dtype)) || !narrow_rows(dlogits, lddl, E, size_of(dtype)) || !aligned(ids, 4) ||

@@ -87,7 +87,8 @@ def moe_route(logits: torch.Tensor, top_k: int, bias: Optional[torch.Tensor] = N
     their group_best (1 or 2) best keys take part. weights = scale * s / (sum of the chosen s
     + 1e-20), or scale * s without renormalize. A logit or key of -inf is never chosen; where
     fewer than top_k are left, ids end with -1 and weights with 0. scores: optional float32
-    [T, E], receives s. E at most 1024, top_k at most 64, groups at most 64."""
+    [T, E], receives s. E at most 1024, top_k at most 64, groups at most 64, scale
+    at most 2^60 either way."""
     return (_native or _calls()).moe_route(logits, top_k, bias, scoring, groups, top_groups, group_best, renormalize, scale, ids,
                                            weights, scores, stream)
 

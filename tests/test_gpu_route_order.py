@@ -148,3 +148,17 @@ def test_scores_below_the_normal_numbers(cuda_device, cus, E):
     bias[:E // 2] = 2e-39
     ids, _ = fg.moe_route(x, 3, bias=bias, scoring="sigmoid")
     assert ids.tolist() == [[E - 1, 0, 1]] * T
+
+
+@pytest.mark.parametrize("E", [4, 64, 256])
+@pytest.mark.parametrize("scale", [2.0 ** 60, -2.0 ** 60])
+def test_the_largest_scales(cuda_device, cus, E, scale):
+    """Rows without experts have weights of 0, and no weight that is a number becomes another."""
+    x = torch.randn(70, E, generator=synth.make_generator(8, cuda_device), device=cuda_device)
+    x[::2] = -float("inf")
+    for scoring in ("softmax", "sigmoid"):
+        for renormalize in (True, False):
+            ids, w = fg.moe_route(x, 3, scoring=scoring, renormalize=renormalize, scale=scale)
+            ri, rw, _ = mo.route(f64(x), 3, None, scoring, renormalize=renormalize, scale=scale)
+            assert np.array_equal(ids.cpu().numpy(), ri) and bool((w[::2] == 0).all())
+            assert np.all(np.abs(f64(w) - rw) <= 2.0 ** -16 * np.abs(rw))

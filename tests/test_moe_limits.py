@@ -5,7 +5,7 @@ import re
 import pytest
 import torch
 
-from test_moe_abi import DEVICE, DISPATCH, GATHER, HEADER, HEADS, HEADS_GRAD, SHAPE, call
+from test_moe_abi import DEVICE, DISPATCH, GATHER, HEADER, HEADS, HEADS_GRAD, ROUTE, ROUTE_GRAD, SHAPE, call
 
 MOST = 2 ** 31 - 2 ** 18 - 1  # choices, rows, heads
 
@@ -38,3 +38,12 @@ def test_choices_rows_and_heads():
         kw["T"] = MOST // (Hq + Hk) + 1
         assert call("fp8_qk_norm_rope", HEADS, **kw, **out) == SHAPE
         assert call("fp8_qk_norm_rope_backward", HEADS_GRAD, **kw, **grad) == SHAPE
+
+
+def test_scales():
+    """Up to 2^60: over 1e-20, what a row without experts is scaled by, that is a number."""
+    for name, defaults in (("fp8_moe_route", ROUTE), ("fp8_moe_route_backward", ROUTE_GRAD)):
+        for scale in (2.0 ** 60, -2.0 ** 60, 0.0):
+            assert call(name, defaults, scale=scale) == DEVICE
+        for scale in (2.0 ** 61, -2.0 ** 61, 1e30, float("inf")):
+            assert call(name, defaults, scale=scale) == SHAPE
