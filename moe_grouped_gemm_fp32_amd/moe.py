@@ -118,9 +118,10 @@ class MoeLayout(NamedTuple):
 
 def moe_rows(tokens: int, top_k: int, num_experts: int) -> int:
     """Rows that the contiguous layout can need: every expert's segment rounded up to 128."""
-    rows = int(_fn("fp8_moe_rows")(tokens, top_k, num_experts))
-    _require(rows > 0 or tokens == 0, "tokens, top_k or num_experts out of range")
-    return rows
+    rows = _fn("fp8_moe_rows")
+    # 0 is also what a call out of range gets: no tokens are in range where one is
+    _require(rows(tokens or 1, top_k, num_experts) > 0, "tokens, top_k or num_experts out of range")
+    return int(rows(tokens, top_k, num_experts))
 
 
 def make_moe_layout(tokens: int, top_k: int, num_experts: int, max_m: Optional[int] = None, rows: Optional[int] = None,

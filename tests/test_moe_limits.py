@@ -5,18 +5,19 @@ import re
 import pytest
 import torch
 
+import moe_grouped_gemm_fp32_amd as fg
 from test_moe_abi import DEVICE, DISPATCH, GATHER, HEADER, HEADS, HEADS_GRAD, ROUTE, ROUTE_GRAD, SHAPE, call
 
 MOST = 2 ** 31 - 2 ** 18 - 1  # choices, rows, heads
 
 
-@pytest.fixture(autouse=True)
+@pytest.fixture
 def without_a_gpu():
     if torch.cuda.is_available():
         pytest.skip("a GPU is present: valid calls would be launched")
 
 
-def test_choices_rows_and_heads():
+def test_choices_rows_and_heads(without_a_gpu):
     assert {2 ** 31 - 2 ** int(n) - 1 for n in re.findall(r"below 2\^31 - 2\^(\d+)", open(HEADER).read())} == {MOST}
     workspace = dict(workspace_bytes=1 << 40)
     for T, top_k in ((MOST, 1), (MOST // 2, 2), (MOST // 64, 64)):
@@ -40,10 +41,20 @@ def test_choices_rows_and_heads():
         assert call("fp8_qk_norm_rope_backward", HEADS_GRAD, **kw, **grad) == SHAPE
 
 
-def test_scales():
+def test_scales(without_a_gpu):
     """Up to 2^60: over 1e-20, what a row without experts is scaled by, that is a number."""
     for name, defaults in (("fp8_moe_route", ROUTE), ("fp8_moe_route_backward", ROUTE_GRAD)):
         for scale in (2.0 ** 60, -2.0 ** 60, 0.0):
             assert call(name, defaults, scale=scale) == DEVICE
         for scale in (2.0 ** 61, -2.0 ** 61, 1e30, float("inf")):
             assert call(name, defaults, scale=scale) == SHAPE
+
+
+def test_rows_of_no_tokens_are_refused_where_those_of_one_are():
+    assert fg.moe_rows(0, 64, 1024) == 0 and fg.make_moe_layout(0, 64, 1024, device="cpu").sources.shape == (0,)
+    for top_k, experts in ((0, 8), (65, 8), (2, 0), (2, 1025)):
+        for tokens in (0, 1):
+            with pytest.raises(ValueError):
+                fg.moe_rows(tokens, top_k, experts)
+            with pytest.raises(ValueError):
+                fg.make_moe_layout(tokens, top_k, experts, device="cpu")
