@@ -16,10 +16,13 @@
  * never read by the host, strides in ELEMENTS, FP8GEMM_* status codes, nothing launched on
  * an argument error, no exception across the ABI. Calls may be captured into graphs. Types
  * of rows are FP8GEMM_QUANT_BF16 and FP8GEMM_QUANT_FP32. Sums are FP32 in an order that the
- * shapes fix, so equal inputs give equal bits. Expert and row numbers on the device are not
- * trusted with addresses: one outside its range counts as none. A call without tokens
- * (T == 0) looks at no pointer to tokens' data. Arrays do not overlap, except where said;
- * calls that may run at the same time do not share a workspace.
+ * inputs, the shapes and the compute units in use (fp8_gemm_set_num_cus) fix, so equal calls
+ * give equal bits. Among calls of other numbers of tokens or units a row's scores and weights, and
+ * the heads' weight gradients, may differ in their last bits; chosen experts, layouts and what
+ * is not summed over tokens do not. Expert and row numbers on the device are not trusted with
+ * addresses: one outside its range counts as none. A call without tokens (T == 0) looks at no
+ * pointer to tokens' data. Arrays do not overlap, except where said; calls that may run at the
+ * same time do not share a workspace.
  */
 #ifndef FP8MOE_H_
 #define FP8MOE_H_

@@ -407,7 +407,9 @@ __device__ __forceinline__ V row16_sum(V v) {
   v += dpp<kHalfMirror>(v, v);
   return v + dpp<kMirror>(v, v);
 }
-// The sum of the chosen scores, lane i's the i-th, in the same order whichever kernel has them.
+// The sum of the chosen scores, lane i's the i-th. Up to 16, in the order in which a row of 16 lanes
+// adds them; two experts a lane or fewer are added in the experts' order there, and all scores of a
+// softmax lane by lane, so weights' last bits may depend on the kernel.
 __device__ __forceinline__ float sum_of_chosen(float s) {
   const float row = row16_sum(s);
   return lane_value(row, 0) + lane_value(row, 16) + lane_value(row, 32) + lane_value(row, 48);

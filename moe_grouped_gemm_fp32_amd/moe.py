@@ -12,7 +12,9 @@ of include/fp8moe.h.
 
 Like the layer operators' calls these only marshal tensors, in native code, read numbers of
 experts and rows on the device only (every call may be captured into a graph), take a `stream`,
-and are exported by the package.
+and are exported by the package. Equal calls give equal bits; scores, routing weights and the heads' weight
+gradients may differ in their last bits between calls of other numbers of tokens or compute
+units, chosen experts do not.
 """
 from __future__ import annotations
 

@@ -162,3 +162,33 @@ def test_the_largest_scales(cuda_device, cus, E, scale):
             ri, rw, _ = mo.route(f64(x), 3, None, scoring, renormalize=renormalize, scale=scale)
             assert np.array_equal(ids.cpu().numpy(), ri) and bool((w[::2] == 0).all())
             assert np.all(np.abs(f64(w) - rw) <= 2.0 ** -16 * np.abs(rw))
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top_groups", [(16, 1, 1), (32, 1, 1), (32, 4, 2), (64, 1, 1), (160, 8, 3), (256, 1, 1), (256, 8, 4)])
+def test_a_row_alone_and_among_many(cuda_device, E, groups, top_groups, scoring):
+    """The same experts; weights that differ by the order of their sums at most. With u = 2^-24, of equal
+    exponentials and sigmoids: a softmax's total is off by up to 20 u, its reciprocal and product
+    by 2, the chosen scores' sum by 7, quotient and product by 2, on either side: below 64 u."""
+    g = synth.make_generator(9, cuda_device)
+    x = torch.randn(20000, E, generator=g, device=cuda_device)
+    bias = torch.randn(E, generator=g, device=cuda_device) * 0.1
+    bias[E // 2] = bias[0]
+    x[:64, E // 2] = x[:64, 0]
+    for b in (None, bias):
+        for renormalize in (True, False):
+            kw = dict(bias=b, scoring=scoring, groups=groups, top_groups=top_groups, group_best=2, renormalize=renormalize)
+            ids, w = fg.moe_route(x, 5, **kw)
+            again = fg.moe_route(x, 5, **kw)
+            assert torch.equal(again[0], ids) and torch.equal(again[1], w)
+            for n in (1, 50):
+                few, wf = fg.moe_route(x[:n], 5, **kw)
+                assert torch.equal(few, ids[:n]) and torch.equal(fg.moe_route(x[:n], 5, **kw)[1], wf)
+                assert bool(((wf.double() - w[:n].double()).abs() <= 64 * 2.0 ** -24 * wf.double()).all())
+                fg.set_num_cus(1)
+                try:
+                    one, w1 = fg.moe_route(x[:n], 5, **kw)
+                finally:
+                    fg.set_num_cus(0)
+                assert torch.equal(one, few)
+                assert bool(((wf.double() - w1.double()).abs() <= 64 * 2.0 ** -24 * wf.double()).all())
