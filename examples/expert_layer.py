@@ -122,7 +122,7 @@ def serve(users, prompt, steps, hidden=2048, heads=16, kv_heads=4, dim=128, ffn=
     lens = [max(1, prompt - (37 * b) % prompt) for b in range(users)]
     table, pages = paged_batch([n + steps for n in lens], page_size, device)
     groups = next(g for g in (8, 4, 2, 1) if experts % g == 0)
-    layer = ExpertLayer(hidden, heads, kv_heads, dim, ffn, pages, experts, top_k, groups, max(1, groups // 2), page_size,
+    layer = ExpertLayer(hidden, heads, kv_heads, dim, ffn, pages, experts, min(top_k, experts), groups, max(1, groups // 2), page_size,
                         max_pos=prompt + steps, device=device)
     gen = synth.make_generator(7, device)
     cu = torch.tensor([0] + lens, device=device).cumsum(0).to(torch.int32)
