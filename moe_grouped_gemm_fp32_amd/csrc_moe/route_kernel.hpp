@@ -260,12 +260,12 @@ __device__ __forceinline__ int choose_slowly(const RouteParams& p, double (&key)
 template <int VPL, typename T>
 __device__ __forceinline__ bool others_near(const RouteParams& p, const int (&key)[VPL], const float (&x)[VPL], int base, int2 edge, float slack,
                                             const T* logits) {
-  const float v = value_of(edge.x), off = slack + 0x1p-22f * fabsf(v), x0 = logit(logits + edge.y), b0 = p.bias ? p.bias[edge.y] : 0.f;
+  const float v = value_of(edge.x), off = slack + 0x1p-22f * fabsf(v), x0 = logit(logits + edge.y), b0 = p.bias[edge.y];
   bool other = false;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     const float k = value_of(key[j]);
-    if (key[j] > kNoKey && !(fabsf(k - v) > off)) other = other || !(x[j] == x0 && (!p.bias || p.bias[base + j] == b0));
+    if (key[j] > kNoKey && !(fabsf(k - v) > off)) other = other || !(x[j] == x0 && p.bias[base + j] == b0);
   }
   return other;
 }
@@ -369,7 +369,7 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const int (&key)[VP
     bool open = lane > 0 && lane < need && !(before - v > slack + 0x1p-22f * fabsf(v));
     if (__ballot(open) != 0) {
       const int last = from_before(e);
-      if (open) open = !(logit(logits + last) == logit(logits + e) && (!p.bias || p.bias[last] == p.bias[e]));
+      if (open) open = !(logit(logits + last) == logit(logits + e) && p.bias[last] == p.bias[e]);
       if (need > p.top_k) {  // what follows equal keys at the edge could be larger than they are
         const int2 edge = make_int2(lane_value(sorted, p.top_k), lane_value(e, p.top_k));
         if (!(value_of(lane_value(sorted, p.top_k - 1)) - value_of(edge.x) > slack + 0x1p-22f * fabsf(value_of(edge.x))))
@@ -384,7 +384,7 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const int (&key)[VP
         own_lds();
         const Exactly exactly(p.sigmoid, top_logit, x);
         e = lane < count ? place[lane].y : 0;
-        const double k = lane < count ? exactly.key(logit(logits + e), p.bias ? p.bias[e] : 0.f) : (double)kNone;
+        const double k = lane < count ? exactly.key(logit(logits + e), p.bias[e]) : (double)kNone;
         rank = 0;
         for (int c = 0; c < count; ++c) {
           const double other = lane_value(k, c);
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
         const int2 next = order[wave][mine][rank[j] + 1];
         const float v = value_of(key[j]), after = value_of(next.x);
         if (v - after > slack + 0x1p-22f * fabsf(after)) continue;
-        open = open || !(x[j] == logit(logits + next.y) && (!p.bias || p.bias[base + j] == p.bias[next.y]));
+        open = open || !(x[j] == logit(logits + next.y) && p.bias[base + j] == p.bias[next.y]);
         edge = edge || rank[j] + 1 == p.top_k;
       }
       const bool at_edge = (__ballot(edge) >> (lane & 48) & 0xFFFF) != 0;
@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
       }
       if (__ballot(near) != 0) {
         const bool at_edge = (__ballot(near && sub16 == p.top_k) >> (lane & 48) & 0xFFFF) != 0;
-        if (near) near = !(logit(logits + last) == logit(logits + best_of.y) && (!p.bias || p.bias[last] == p.bias[best_of.y]));
+        if (near) near = !(logit(logits + last) == logit(logits + best_of.y) && p.bias[last] == p.bias[best_of.y]);
         if (at_edge) near = near || others_near(p, key, x, base, line[16 + p.top_k], slack, logits);
       }
       const uint64_t nears = __ballot(near);
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
         const int2 other = candidates(lower);
         const Exactly exactly(p.sigmoid, top, x, 16);
         const bool is = mend && sub16 < more && more <= 16;
-        const double k = is ? exactly.key(logit(logits + other.y), p.bias ? p.bias[other.y] : 0.f) : (double)kNone;
+        const double k = is ? exactly.key(logit(logits + other.y), p.bias[other.y]) : (double)kNone;
         const uint64_t bits = __double_as_longlong(k);
         const int low_half[1] = {(int)(uint32_t)bits}, high_half[1] = {(int)(bits >> 32)};
         int place = 0;
