@@ -10,7 +10,9 @@ Serving: prompts, then one token a user and step, the step captured into a graph
     -> routing -> dispatch -> experts' gate and up product -> SwiGLU + quantise -> experts' down
     product -> weighted return to the residual stream
 
-Training: a routed linear layer and its gradients (RoutedLinear).
+Training: a routed linear layer, its gradients of the logits and of the input by way of the experts
+(RoutedLinear). The router's part of the input's gradient is a plain product of the logits'; the experts'
+weight gradients need rows scaled by columns, which the package's calls do not lay out.
 Synthetic inputs, weights drawn at random.
 """
 import argparse
@@ -85,7 +87,7 @@ class ExpertLayer(DecoderLayer):
 
 
 class RoutedLinear:
-    """y[t] = sum_j w[t, j] W[e(t, j)] x[t], with 8-bit products, and its gradients."""
+    """y[t] = sum_j w[t, j] W[e(t, j)] x[t], with 8-bit products, and gradients of x and of the logits."""
 
     def __init__(self, experts, n, k, top_k, seed=0, device="cuda"):
         gen = synth.make_generator(seed, device)

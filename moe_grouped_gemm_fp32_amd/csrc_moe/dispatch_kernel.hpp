@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 // Layout and rows of a few tokens in one launch: a workgroup takes `tokens` of them, at most
 // kFewChoices choices, counts all choices for itself, places its own and copies a slice of
 // their rows. Here scales are written one by one; there are few. 64 tokens of 8 choices and 7168
-// columns 5.1 us: a launch, and a chain of passes over LDS.
+// columns 5.4 us: a launch, and a chain of passes over LDS.
 struct FewParams {
   LayoutParams layout;
   GatherParams copy;

@@ -64,11 +64,13 @@ int fp8_moe_route(const void* logits, int64_t ldl, int dtype, const float* bias,
                         0,      0,          0};
   // Experts of a lane where 16 lanes hold a row, and a group some of them. A wave for four rows
   // shares most instructions among them, and needs many rows to fill the GPU; there has to be a
-  // lane for each choice and one more. For four rows and for one, sigmoid with a bias, us: 16
-  // experts, 1 token 2.3 and 2.6, 16384 3.4 and 7.4; 32, 1 token 2.9 and 2.7, 16384 5.8 and 8.2, in
-  // 4 groups 4096 6.6 and 4.7; 64, 4096 4.9 and 4.5, 8192 5.5 and 5.4, 16384 6.4 and 8.6, 65536 13.4
-  // and 24.3; 256, 8192 7.7 and 7.5, 16384 10.6 and 11.4, in 8 groups 12.7 and 14.2, 65536 31.8 and
-  // 43.1. Softmax of 160 in 8 groups gains last: 16384 17.0 and 16.6, 65536 38.4 and 51.5.
+  // lane for each choice and one more. For four rows and for one, FP32 logits of deviation 1.5 that the
+  // caches hold, sigmoid with a bias, calls of a graph, us: 16 experts, 1 token 2.3 and 2.6, 16384 3.3
+  // and 8.1; 32, 1 token 2.9 and 2.6, 16384 7.5 and 9.2, in 4 groups 4096 7.0 and 5.1, 16384 7.2 and
+  // 10.3; 64, 4096 5.0 and 4.8, 8192 5.1 and 6.5, 16384 6.2 and 9.0, 65536 13.9 and 26.7; 256, 8192
+  // 8.2 and 7.1, 16384 10.5 and 11.1, 65536 26.8 and 33.7, in 8 groups 8192 8.4 and 8.4, 16384 11.6
+  // and 13.7, 65536 33.4 and 44.1. Cold logits of 16384 x 256: 12.3 and 12.1, in 8 groups 14.6 and 15.0.
+  // Other rows, of which FP32 leaves others open, move these by up to 3.
   const int of_16 = log_groups <= 4 ? (int)ceil_div(size, 1 << (log_lanes - 2)) : 0;
   const bool four_rows = of_16 == 1 || (of_16 == 2 && T > 32 * cus) ||
                          (of_16 > 2 && of_16 <= 16 && top_k <= 15 && T >= (of_16 <= 4 ? 32 : 64) * cus);
@@ -120,6 +122,11 @@ int fp8_moe_route_backward(const float* dweights, const void* logits, int64_t ld
       });
     };
     // A lane holds a choice: four rows a wave where 16 lanes are enough for that and for a few experts.
+    // With 16 lanes a row and with 64, BF16 softmax and a gradient of the scores, us: 16 experts, 1000
+    // rows 2.5 and 2.6, 16384 3.2 and 6.0; 64, 1000 2.7 and 2.5, 16384 3.7 and 6.1, 65536 9.1 and 20.0; 96,
+    // 1000 3.0 and 2.5, 10007 3.8 and 4.6; 160, 4096 3.7 and 3.3, 10007 4.8 and 5.2, 65536 17.0 and 23.5;
+    // 256, 4096 4.3 and 3.8, 16384 7.6 and 8.6. Past 64 experts 16 lanes lose on few rows; what they gain
+    // on many is not taken.
     if (E <= 64 && top_k <= 16) with_count<1, 2, 4>((int)ceil_div(E, 16), [&](auto count) { go(count, Int<16>{}); });
     else with_count<1, 2, 3, 4, 6, 8, 12, 16>((int)ceil_div(E, 64), [&](auto count) { go(count, Int<64>{}); });
   });

@@ -96,8 +96,8 @@ struct HeadsParams {
   int first_group;  // the launch's first workgroup of the call's
 };
 
-// One head for D / 16 lanes. Bound by memory: 8192 tokens of 40 heads of 128 BF16 columns 36.6 us,
-// 4.6 TB/s; 64 tokens 3.2 us.
+// One head for D / 16 lanes. Bound by memory: 8192 tokens of 40 heads of 128 BF16 columns 37 us,
+// 4.6 TB/s; 64 tokens 3.5 us.
 template <typename T, int D, bool STREAM>
 __global__ void __launch_bounds__(256) heads_kernel(const HeadsParams p) {
   constexpr int kLanes = D / 16, kHeads = 256 / kLanes;
@@ -148,7 +148,7 @@ struct HeadsGradParams {
 // A workgroup takes heads of queries, or of keys, and keeps its sums for dw in registers over
 // all of them. Loading the next heads while the present ones are worked on changed nothing
 // (5003 x 32 heads of 64: 19.2 us with, 18.9 without, both launches). Bound by memory where heads
-// are many (6000 x 80 of 64 40.8 us with the launch below, 4.5 TB/s); 5003 x 32 15.4 us, and 4 below.
+// are many (6000 x 80 of 64 40.8 us with the launch below, 4.5 TB/s); 5003 x 32 15.2 us, and 4 below.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) heads_backward_kernel(const HeadsGradParams p) {
   constexpr int kLanes = D / 16, kHeads = 256 / kLanes;

@@ -276,8 +276,10 @@ constexpr int kEnough = 8;  // candidates beyond those needed that are ranked ra
 // candidates, one a lane, and each counts the larger ones. A decision is sure where two keys
 // are further apart than FP32 leaves open, `slack` + 2^-22 of a key (without `tell` the keys
 // are exact), or have equal logits and biases. Otherwise the candidates, and whatever could
-// be among them, are ranked in FP64; false if they are too many for that. `place`: LDS for
-// 64 keys and numbers.
+// be among them, are ranked in FP64; false if they are too many for that. That is so for each row
+// of more than 64 experts with a bias of which 64 are chosen, since the first that is not would be
+// the 65th: 4096 rows of 256 take 42 us, and 13 with 63 chosen; one row 25 and 4.2. `place`: LDS
+// for 64 keys and numbers.
 template <int VPL, typename T>
 __device__ __forceinline__ bool choose(const RouteParams& p, const int (&key)[VPL], const float (&x)[VPL], int base, int lane, bool tell,
                                        float slack, float top_logit, const T* logits, int2* place, int& id) {
@@ -428,8 +430,9 @@ __device__ __forceinline__ float slack_of(int largest, int sigmoid) {
 // One row, by a wave. The keys stay in registers, a group's in neighbouring lanes. Keys are FP32;
 // what they leave open (in 2 of 1000 rows of 256 sigmoid scores with a bias) is decided in FP64.
 // Without a bias experts are compared by their logits, exactly, and only groups by scores. Bound by vector instructions:
-// 16384 rows of 256 experts in 8 groups, 8 chosen, 362 a row, 14.1 us (their bytes take 3.7);
-// without groups and bias 8.9; one row 3.4 us, most of it the launch and one chain.
+// 16384 rows of 256 experts in 8 groups, 8 chosen, 388 a row, 14.2 us (their bytes take 3.7);
+// without groups and bias 9.7; one row 3.5 us, most of it the launch and one chain; 512 experts in 8
+// groups 17.7, 1024 27.9, a softmax of 1024 without groups and bias 21.0.
 template <typename T, int VPL>
 __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int lane, int2* place) {
   const T* logits = static_cast<const T*>(p.logits) + row * p.ldl;
@@ -574,9 +577,10 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
 // larger ones of its row as they come by; more are searched for a threshold that 16 at most
 // reach, one a lane, which then count each other. What FP32 leaves open, or equal keys make too
 // many, is done again by route_row(), up to 16 near keys of more than 32 experts in place. Vector
-// instructions a row of 256 experts in 8 groups 258, a wave's own row 362: 65536 rows 31.8 and
-// 43.1 us; of 16384, four waves a SIMD, whose chains bind it, 13.7 us and no more. 16384 rows of 16
-// experts (sigmoid, bias) 3.4 us, of 32 5.8, of 64 6.4.
+// instructions a row of 256 experts in 8 groups 258, a wave's own row 388: 65536 rows 31.9 and
+// 44.0 us; of 16384, four waves a SIMD, whose chains bind it, 13.4 and 14.2 (cold, 14.6). What
+// route_row() and FP64 need lives beside the fast path: 96 registers, and 46 scalars spilled to
+// lanes. 16384 rows of 16 experts (sigmoid, bias) 3.3 to 6.3 us, of 64 6.4.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(256) route_rows_kernel(const RouteParams p) {
   __shared__ int2 places[4][64];
