@@ -521,11 +521,15 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
       exact_keys(wide);
       kept = best_groups<VPL>(p, wide, lane);
     }
-    if (by_score && !tell) {  // loaded again: held over FP64's groups they are 15 registers of 16 experts
-      float y[VPL];
+    if (by_score && !tell) {
+      if constexpr (VPL > 8) {  // loaded again: kept over FP64's groups, 16 are 15 registers and a wave a SIMD
+        float y[VPL];
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) y[j] = j < count ? logit(logits + min(base + j, p.E - 1)) : kNone;
-      logit_keys(y, key);
+        for (int j = 0; j < VPL; ++j) y[j] = j < count ? logit(logits + min(base + j, p.E - 1)) : kNone;
+        logit_keys(y, key);
+      } else {
+        logit_keys(x, key);
+      }
     }
 #pragma unroll
     for (int j = 0; j < VPL; ++j) key[j] = kept ? key[j] : kNoKey;
